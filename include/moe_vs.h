@@ -61,6 +61,7 @@ extern "C" {
 #define MOE_ERR_WORKSPACE 5 /* workspace NULL or smaller than the query returned   */
 #define MOE_ERR_HIP 6       /* the HIP runtime reported an error at launch         */
 #define MOE_ERR_LIMIT 7     /* a size exceeds a documented library limit          */
+#define MOE_ERR_OPTION 8    /* an option is unknown or out of range               */
 
 /* ---- dtype and layout codes --------------------------------------------- */
 #define MOE_F32 0
@@ -361,6 +362,133 @@ size_t moe_fused_bwd_workspace_bytes(const moe_schedule *sched, int64_t K, int64
 int moe_fused_bwd(const void *dY, const void *x, const void *W, const moe_schedule *sched,
                   float *dX, void *dW, float *d_topk, int64_t K, int64_t N, int32_t dtype,
                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Routing to experts: from the router's logits to the expert_ids and
+ * topk_weights that moe_build_schedule takes.  For each row l [E] of logits:
+ *   score    s = softmax(l) (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l))
+ *            (MOE_SCORE_SIGMOID);
+ *   choice   c = l without a bias (the scores increase with l), s + bias with
+ *            one, computed in 64 bits.  An expert with l = -inf or bias = -inf
+ *            is never chosen; a NaN ranks above every number; equal values go
+ *            to the lower expert;
+ *   groups   with groups > 1 the experts form `groups` runs of E / groups; the
+ *            `topk_groups` best groups stay (equal: the lower group), by their
+ *            best choice value (MOE_GROUP_MAX) or by the sum of the two best of
+ *            s (no bias) or s + bias (MOE_GROUP_TOP2; one expert left: its value
+ *            alone; none left: never chosen);
+ *   ids      the k best experts of the groups that stay, best first; slots
+ *            left over hold -1 (which a schedule leaves out) with weight 0, so
+ *            a row of -inf (a padding token) is routed nowhere;
+ *   weight   w = scale * s / (renormalize ? sum of s over the chosen : 1).  A
+ *            NaN logit makes its row's softmax weights NaN.
+ *   logits [T, E] in `dtype`; bias [E] float or NULL; expert_ids [T, k] int32
+ *   and topk_weights [T, k] float, OVERWRITTEN.  T may be 0.
+ *   1 <= k <= min(64, E), E <= 1024, groups <= 64 a divisor of E (E / groups
+ *   >= 2 for MOE_GROUP_TOP2), 1 <= topk_groups <= groups, k <= topk_groups *
+ *   E / groups, scale finite and > 0 (MOE_ERR_OPTION).
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+int moe_route_fwd(const void *logits, const float *bias, int64_t T, int32_t E, int32_t k,
+                  int32_t score, int32_t groups, int32_t topk_groups, int32_t group_score,
+                  int32_t renormalize, float scale, int32_t *expert_ids, float *topk_weights,
+                  int32_t dtype, void *stream);
+
+/*
+ * Gradient of the routing weights with respect to the logits (the choice is
+ * held fixed; the bias gets none).  With g = d_weights, D = sum_j g_j w_j:
+ *   softmax, renormalised  dl_j = w_j (g_j - D / scale)          at the chosen, else 0
+ *   softmax, plain         dl_i = w_i g_i [i chosen] - p_i D,    p = softmax(l)
+ *   sigmoid, renormalised  dl_j = w_j (1 - s_j) (g_j - D / scale)
+ *   sigmoid, plain         dl_j = w_j (1 - s_j) g_j
+ *   d_weights, topk_weights [T, k] float and expert_ids [T, k] as moe_route_fwd
+ *   returned them for the same logits and options; ids outside [0, E) are
+ *   passed over, and an id that a row repeats gets the sum.  d_logits [T, E] in
+ *   `dtype`, OVERWRITTEN.
+ */
+int moe_route_bwd(const float *d_weights, const void *logits, const int32_t *expert_ids,
+                  const float *topk_weights, int64_t T, int32_t E, int32_t k, int32_t score,
+                  int32_t renormalize, float scale, void *d_logits, int32_t dtype, void *stream);
+
+/* Bytes of device workspace moe_router_loss_fwd needs; 0 for invalid sizes
+ * and for T = 0. */
+size_t moe_router_loss_workspace_bytes(int64_t T, int32_t E);
+
+/*
+ * The two losses a router is trained with beside the model's own:
+ *   balance = sum_e f_e * (1/V) sum_t q_te,   z = (1/V) sum_t logsumexp(l_t)^2,
+ * where V counts the rows with a logit above -inf (the others are left out),
+ * f_e = E * (assignments to e) / (all assignments), a constant for the
+ * gradient, and q the softmax of the row or its sigmoids over their sum.  An
+ * even load gives balance 1.  Both are 0 when V is 0.
+ *   logits [T, E] in `dtype`; expert_ids [T, k] int32 (outside [0, E): not an
+ *   assignment); losses [2] float = {balance, z} and stats [E + 1] float
+ *   (f, then 1/V: what the backward needs), OVERWRITTEN.  T may be 0.
+ *   workspace: moe_router_loss_workspace_bytes(T, E) bytes, 256-byte aligned.
+ * Two launches on `stream`; sums are joined in a fixed order (reproducible).
+ */
+int moe_router_loss_fwd(const void *logits, const int32_t *expert_ids, int64_t T, int32_t E,
+                        int32_t k, int32_t score, float *losses, float *stats, int32_t dtype,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of d_losses[0] * balance + d_losses[1] * z:
+ *   softmax  dl_i = d0 / V * q_i (f_i - sum_e f_e q_e) + 2 d1 / V * lse * softmax_i
+ *   sigmoid  the first term times 1 - sigmoid(l_i).
+ *   d_losses [2] float (device), logits as in the forward, stats [E + 1] from
+ *   it; d_logits [T, E] in `dtype`, OVERWRITTEN (0 in rows left out).
+ */
+int moe_router_loss_bwd(const float *d_losses, const void *logits, const float *stats, int64_t T,
+                        int32_t E, int32_t score, void *d_logits, int32_t dtype, void *stream);
+
+/*
+ * Dense linear layer with its epilogue in the product's launch (the router's
+ * logits, a shared expert's projections, added to the routed output):
+ *     z = x W^T + bias,   out = act(z) + residual.
+ *   act: MOE_ACT_NONE, _RELU, _GELU (z Phi(z)), _GELU_TANH (its tanh form),
+ *   _SILU.
+ *   x [M, K], W [N, K], bias [N] or NULL, z [M, N] or NULL (kept for the
+ *   backward, rounded to `dtype`; the activation takes it unrounded) in
+ *   `dtype`; residual [M, N] or NULL and out [M, N] in `out_dtype`, which may
+ *   be the same buffer.  dtype MOE_F32 -> out_dtype MOE_F32; dtype MOE_BF16 ->
+ *   MOE_BF16 or MOE_F32.  Element alignment; any sizes (bf16 runs fastest with
+ *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0.
+ *   workspace: moe_linear_fwd_workspace_bytes(...) bytes, 256-byte aligned
+ *   (may be NULL when that is 0).
+ */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_GELU 2
+#define MOE_ACT_GELU_TANH 3
+#define MOE_ACT_SILU 4
+size_t moe_linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t dtype);
+int moe_linear_fwd(const void *x, const void *W, const void *bias, const void *residual, void *out,
+                   void *z, int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype,
+                   int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace moe_linear_bwd needs (dz, partial sums); 0 for
+ * invalid arguments. */
+size_t moe_linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype,
+                                      int32_t out_dtype);
+
+/*
+ * Backward of moe_linear_fwd, with d_out [M, N] in `out_dtype`:
+ *   dz = d_out * act'(z) (rounded to `dtype` for the two products),
+ *   dX = dz W, dW = dz^T x, d_bias = sum of dz over the rows (unrounded dz).
+ * The residual's gradient is d_out itself.
+ *   x, W as in the forward and z as it kept it (may be NULL for MOE_ACT_NONE);
+ *   dX [M, K], dW [N, K], d_bias [N] in `dtype`: each OVERWRITTEN, or NULL to
+ *   skip.  W may be NULL without dX, x without dW.  M may be 0 (dW and d_bias
+ *   are then zeros).
+ *   workspace: moe_linear_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *z, void *dX,
+                   void *dW, void *d_bias, int64_t M, int64_t K, int64_t N, int32_t act,
+                   int32_t dtype, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                   void *stream);
 
 /*
  * Export the flat tile space the grouped kernels walk for an output of N

@@ -22,6 +22,9 @@ BM_VALUES = (32, 64, 128, 256)
 MOE_COMBINE_AUTO = 0
 MOE_COMBINE_ATOMIC = 1
 MOE_COMBINE_RANKED = 2
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_GROUP_SCORES = {"max": 0, "top2": 1}
+MOE_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class MoeSchedule(ctypes.Structure):
@@ -59,6 +62,7 @@ class MoeSchedule(ctypes.Structure):
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _SZ = ctypes.c_size_t
 _SCHED_P = ctypes.POINTER(MoeSchedule)
 
@@ -76,6 +80,18 @@ SIGNATURES = {
                                          _I64, _I64, _I32, _P, _SZ, _P]),
     "moe_fused_bwd_workspace_bytes": (_SZ, [_SCHED_P, _I64, _I64, _I32]),
     "moe_fused_bwd": (ctypes.c_int, [_P, _P, _P, _SCHED_P, _P, _P, _P, _I64, _I64, _I32, _P, _SZ, _P]),
+    "moe_route_fwd": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P,
+                                     _P, _I32, _P]),
+    "moe_route_bwd": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _I32, _P]),
+    "moe_router_loss_workspace_bytes": (_SZ, [_I64, _I32]),
+    "moe_router_loss_fwd": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _SZ, _P]),
+    "moe_router_loss_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _P, _I32, _P]),
+    "moe_linear_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "moe_linear_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P,
+                                      _SZ, _P]),
+    "moe_linear_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32, _I32]),
+    "moe_linear_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
+                                      _P, _SZ, _P]),
     "moe_tile_map": (ctypes.c_int, [_SCHED_P, _I64, _I32, _I32, _P, _P, _P, _I64, _P]),
     "moe_set_tile_rows": (ctypes.c_int, [_I32]),
     "moe_set_combine": (ctypes.c_int, [_I32]),

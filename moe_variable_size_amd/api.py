@@ -21,6 +21,7 @@ import torch
 from . import _lib
 from ._lib import MOE_BF16, MOE_F32, MOE_LAYOUT_CONTIGUOUS, MOE_LAYOUT_MASKED, BM_VALUES
 from ._lib import MOE_COMBINE_AUTO, MOE_COMBINE_ATOMIC, MOE_COMBINE_RANKED
+from ._lib import MOE_ACTS, MOE_GROUP_SCORES, MOE_SCORES
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -451,6 +452,255 @@ def moe_fused_bwd(dY: torch.Tensor, x: torch.Tensor, W: Optional[torch.Tensor], 
     return dX, dW, dT
 
 
+# ---- routing, router losses, dense linear layer -----------------------------------------------
+
+class _launch:
+    """Device and stream of a call: a context in which the tensor's device is
+    current, yielding the raw stream (the caller's, or that device's current
+    one); buffers the binding allocates inside come from that stream's pool."""
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        dev = t.device
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self._ctx = []
+        if stream is not None:  # makes the stream's device current too
+            self._ctx.append(torch.cuda.stream(stream))
+        elif dev.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(dev))
+        self._raw = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return self._raw
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _require_on(t: Optional[torch.Tensor], name: str, device) -> None:
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _option(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def moe_route_fwd(logits: torch.Tensor, k: int, *, score: str = "softmax",
+                  bias: Optional[torch.Tensor] = None, groups: int = 1, topk_groups: int = 1,
+                  group_score: str = "max", renormalize: bool = True, scale: float = 1.0,
+                  expert_ids: Optional[torch.Tensor] = None,
+                  topk_weights: Optional[torch.Tensor] = None, stream=None):
+    """Experts and weights of every token from the router's logits [T, E]
+    (float32 or bfloat16): the k best by logit, or by score + bias [E] float32,
+    of the ``topk_groups`` best of ``groups`` expert groups (ranked by their
+    best, "max", or the sum of their two best, "top2").  The weight is scale *
+    score, over the sum of the chosen scores with ``renormalize``; score is
+    "softmax" or "sigmoid".  A logit or bias of -inf bars an expert; slots left
+    over hold id -1 and weight 0.  Ties go to the lower expert.  Returns
+    (expert_ids [T, k] int32, topk_weights [T, k] float32), which
+    ``moe_build_schedule`` and ``moe`` take."""
+    lib = _lib.load()
+    _require(logits, "logits", None, 2)
+    code = _dtype_code(logits)
+    sc, gs = _option(MOE_SCORES, score, "score"), _option(MOE_GROUP_SCORES, group_score, "group_score")
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _require(bias, "bias", torch.float32, 1)
+        _require_on(bias, "bias", dev)
+        if bias.numel() != E:
+            raise ValueError(f"bias must have {E} entries, got {bias.numel()}")
+    with _launch(logits, stream) as raw:
+        if expert_ids is None:
+            expert_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        else:
+            _require_out(expert_ids, "expert_ids", torch.int32, (T, k), dev)
+        if topk_weights is None:
+            topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        else:
+            _require_out(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+        st = lib.moe_route_fwd(_ptr(logits), _ptr(bias), T, E, k, sc, groups, topk_groups, gs,
+                               bool(renormalize), scale, _ptr(expert_ids), _ptr(topk_weights), code, raw)
+    _lib.check("moe_route_fwd", st)
+    return expert_ids, topk_weights
+
+
+def moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
+                  topk_weights: torch.Tensor, *, score: str = "softmax", renormalize: bool = True,
+                  scale: float = 1.0, d_logits: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of the routing weights with respect to the logits, from the ids
+    and weights ``moe_route_fwd`` returned with the same options (the choice is
+    held fixed).  Returns d_logits [T, E] in the logits' dtype."""
+    lib = _lib.load()
+    _require(logits, "logits", None, 2)
+    code = _dtype_code(logits)
+    sc = _option(MOE_SCORES, score, "score")
+    T, E = logits.shape
+    dev = logits.device
+    _require(expert_ids, "expert_ids", torch.int32, 2)
+    shape = tuple(expert_ids.shape)
+    for t, name in ((d_weights, "d_weights"), (topk_weights, "topk_weights")):
+        _require(t, name, torch.float32, 2)
+        _require_on(t, name, dev)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have the shape of expert_ids")
+    _require_on(expert_ids, "expert_ids", dev)
+    if shape[0] != T:
+        raise ValueError("expert_ids and logits disagree on T")
+    with _launch(logits, stream) as raw:
+        if d_logits is None:
+            d_logits = torch.empty_like(logits)
+        else:
+            _require_out(d_logits, "d_logits", logits.dtype, (T, E), dev)
+        st = lib.moe_route_bwd(_ptr(d_weights), _ptr(logits), _ptr(expert_ids), _ptr(topk_weights), T,
+                               E, shape[1], sc, bool(renormalize), scale, _ptr(d_logits), code, raw)
+    _lib.check("moe_route_bwd", st)
+    return d_logits
+
+
+def moe_router_loss_fwd(logits: torch.Tensor, expert_ids: torch.Tensor, *, score: str = "softmax",
+                        stream=None):
+    """The balance loss sum_e f_e mean_t(q_te), f_e = E * the expert's share of
+    the assignments, q the softmax (or the sigmoids over their sum) of a row,
+    and the z loss mean_t(logsumexp(l_t)^2), over the rows that have a logit
+    above -inf.  Returns (losses [2] float32, stats [E + 1] float32 for
+    ``moe_router_loss_bwd``)."""
+    lib = _lib.load()
+    _require(logits, "logits", None, 2)
+    code = _dtype_code(logits)
+    sc = _option(MOE_SCORES, score, "score")
+    T, E = logits.shape
+    dev = logits.device
+    _require(expert_ids, "expert_ids", torch.int32, 2)
+    _require_on(expert_ids, "expert_ids", dev)
+    if expert_ids.shape[0] != T:
+        raise ValueError("expert_ids and logits disagree on T")
+    with _launch(logits, stream) as raw:
+        nbytes = int(lib.moe_router_loss_workspace_bytes(T, E))
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+        stats = torch.empty(E + 1, dtype=torch.float32, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        st = lib.moe_router_loss_fwd(_ptr(logits), _ptr(expert_ids), T, E, expert_ids.shape[1], sc,
+                                     _ptr(losses), _ptr(stats), code, _ptr(ws), nbytes, raw)
+    _lib.check("moe_router_loss_fwd", st)
+    return losses, stats
+
+
+def moe_router_loss_bwd(d_losses: torch.Tensor, logits: torch.Tensor, stats: torch.Tensor, *,
+                        score: str = "softmax", d_logits: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of d_losses[0] * balance + d_losses[1] * z with respect to the
+    logits (the shares f_e are constants); d_losses [2] float32 on the device."""
+    lib = _lib.load()
+    _require(logits, "logits", None, 2)
+    code = _dtype_code(logits)
+    sc = _option(MOE_SCORES, score, "score")
+    T, E = logits.shape
+    dev = logits.device
+    for t, name, n in ((d_losses, "d_losses", 2), (stats, "stats", E + 1)):
+        _require(t, name, torch.float32, 1)
+        _require_on(t, name, dev)
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    with _launch(logits, stream) as raw:
+        if d_logits is None:
+            d_logits = torch.empty_like(logits)
+        else:
+            _require_out(d_logits, "d_logits", logits.dtype, (T, E), dev)
+        st = lib.moe_router_loss_bwd(_ptr(d_losses), _ptr(logits), _ptr(stats), T, E, sc,
+                                     _ptr(d_logits), code, raw)
+    _lib.check("moe_router_loss_bwd", st)
+    return d_logits
+
+
+def moe_linear_fwd(x: torch.Tensor, W: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                   act: str = "none", residual: Optional[torch.Tensor] = None, out_dtype=None,
+                   out: Optional[torch.Tensor] = None, save_z: bool = False,
+                   z: Optional[torch.Tensor] = None, stream=None):
+    """Dense layer act(x W^T + bias) + residual in one product: x [M, K], W
+    [N, K] and bias [N] all bfloat16 or all float32; act "none", "relu",
+    "gelu", "gelu_tanh" or "silu"; residual [M, N] in ``out_dtype`` (default:
+    x's; float32 also for bfloat16 inputs), which may be ``out`` itself.
+    Returns out [M, N] and, with ``save_z`` (or ``z`` given), also z = x W^T +
+    bias in x's dtype, which the backward needs unless act is "none"."""
+    lib = _lib.load()
+    _require(x, "x", None, 2)
+    code = _dtype_code(x)
+    dt, dev = x.dtype, x.device
+    _require(W, "W", dt, 2)
+    _require_on(W, "W", dev)
+    M, K = x.shape
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("shape mismatch between x [M, K] and W [N, K]")
+    a = _option(MOE_ACTS, act, "act")
+    if out_dtype is None:
+        out_dtype = dt
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"unsupported out_dtype {out_dtype}; use float32 or bfloat16")
+    if bias is not None:
+        _require_out(bias, "bias", dt, (N,), dev)
+    if residual is not None:
+        _require_out(residual, "residual", out_dtype, (M, N), dev)
+    with _launch(x, stream) as raw:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        else:
+            _require_out(out, "out", out_dtype, (M, N), dev)
+        if z is not None:
+            _require_out(z, "z", dt, (M, N), dev)
+        elif save_z:
+            z = torch.empty((M, N), dtype=dt, device=dev)
+        nbytes = int(lib.moe_linear_fwd_workspace_bytes(M, K, N, code))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        st = lib.moe_linear_fwd(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), _ptr(z), M, K,
+                                N, a, code, _DTYPES[out_dtype], _ptr(ws), nbytes, raw)
+    _lib.check("moe_linear_fwd", st)
+    return out if z is None else (out, z)
+
+
+def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act: str = "none",
+                   z: Optional[torch.Tensor] = None, dx: bool = True, dw: bool = True,
+                   dbias: bool = True, stream=None):
+    """Backward of ``moe_linear_fwd``: (dX [M, K] | None, dW [N, K] | None,
+    d_bias [N] | None), all in x's dtype, from d_out [M, N] (float32, or x's
+    dtype) and the saved z (not needed for act "none").  The residual's
+    gradient is d_out itself."""
+    lib = _lib.load()
+    _require(x, "x", None, 2)
+    code = _dtype_code(x)
+    dt, dev = x.dtype, x.device
+    _require(W, "W", dt, 2)
+    _require_on(W, "W", dev)
+    _require(d_out, "d_out", None, 2)
+    _require_on(d_out, "d_out", dev)
+    ocode = _dtype_code(d_out)
+    M, K = x.shape
+    N = W.shape[0]
+    if W.shape[1] != K or tuple(d_out.shape) != (M, N):
+        raise ValueError("shape mismatch among d_out [M, N], x [M, K] and W [N, K]")
+    a = _option(MOE_ACTS, act, "act")
+    if a:
+        if z is None:
+            raise ValueError(f"act {act!r} needs the z its forward saved")
+        _require_out(z, "z", dt, (M, N), dev)
+    with _launch(x, stream) as raw:
+        dX = torch.empty((M, K), dtype=dt, device=dev) if dx else None
+        dW = torch.empty((N, K), dtype=dt, device=dev) if dw else None
+        db = torch.empty(N, dtype=dt, device=dev) if dbias else None
+        nbytes = int(lib.moe_linear_bwd_workspace_bytes(M, K, N, a, code, ocode))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        st = lib.moe_linear_bwd(_ptr(d_out), _ptr(x), _ptr(W), _ptr(z) if a else None, _ptr(dX), _ptr(dW),
+                                _ptr(db), M, K, N, a, code, ocode, _ptr(ws), nbytes, raw)
+    _lib.check("moe_linear_bwd", st)
+    return dX, dW, db
+
+
 def moe_tile_map(sched: Schedule, N: int, BM: int, BN: int, owner_capacity: Optional[int] = None,
                  stream=None):
     """Flat tile space of an N-column output with BM x BN tiles: (tile_start [E],
@@ -558,3 +808,85 @@ class GatedMoEFunction(torch.autograd.Function):
 
 def gated_moe(x, W_gu, W_down, expert_ids, topk_weights):
     return GatedMoEFunction.apply(x, W_gu, W_down, expert_ids, topk_weights)
+
+
+class RouteFunction(torch.autograd.Function):
+    """Differentiable routing: the weights' gradient reaches the logits; ids
+    and bias get none."""
+
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale):
+        logits = logits.detach().contiguous()
+        ids, w = moe_route_fwd(logits, k, score=score, bias=None if bias is None else bias.detach(),
+                               groups=groups, topk_groups=topk_groups, group_score=group_score,
+                               renormalize=renormalize, scale=scale)
+        ctx.mark_non_differentiable(ids)
+        ctx.save_for_backward(logits, ids, w)
+        ctx.opts = dict(score=score, renormalize=renormalize, scale=scale)
+        return ids, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_ids, gw):
+        logits, ids, w = ctx.saved_tensors
+        d = moe_route_bwd(gw.float().contiguous(), logits, ids, w, **ctx.opts)
+        return (d,) + (None,) * 8
+
+
+def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=1, group_score="max",
+          renormalize=True, scale=1.0):
+    """(expert_ids, topk_weights) as ``moe_route_fwd``; the weights carry the
+    gradient of the logits."""
+    return RouteFunction.apply(logits, k, score, bias, groups, topk_groups, group_score, renormalize,
+                               scale)
+
+
+class RouterLossFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, expert_ids, score):
+        logits = logits.detach().contiguous()
+        losses, stats = moe_router_loss_fwd(logits, expert_ids, score=score)
+        ctx.save_for_backward(logits, stats)
+        ctx.score = score
+        return losses
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        logits, stats = ctx.saved_tensors
+        return moe_router_loss_bwd(g.float().contiguous(), logits, stats, score=ctx.score), None, None
+
+
+def router_loss(logits, expert_ids, *, score="softmax"):
+    """Differentiable (balance, z) losses [2] of ``moe_router_loss_fwd``."""
+    return RouterLossFunction.apply(logits, expert_ids, score)
+
+
+class LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, act, residual, out_dtype):
+        x, W = x.detach().contiguous(), W.detach().contiguous()
+        b = None if bias is None else bias.detach().contiguous()
+        r = None if residual is None else residual.detach().contiguous()
+        keep = act != "none" and any(ctx.needs_input_grad[:3])
+        y = moe_linear_fwd(x, W, bias=b, act=act, residual=r, out_dtype=out_dtype, save_z=keep)
+        y, z = y if keep else (y, None)
+        ctx.save_for_backward(x, W, z)
+        ctx.act = act
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, W, z = ctx.saved_tensors
+        nx, nw, nb, _, nr, _ = ctx.needs_input_grad
+        dX = dW = db = None
+        if nx or nw or nb:
+            dX, dW, db = moe_linear_bwd(gy.contiguous(), x, W, act=ctx.act, z=z, dx=nx, dw=nw, dbias=nb)
+        return dX, dW, db, None, gy if nr else None, None
+
+
+def linear(x, W, bias=None, *, act="none", residual=None, out_dtype=None):
+    """Differentiable dense layer act(x W^T + bias) + residual of
+    ``moe_linear_fwd``; gradients reach x, W, bias and residual."""
+    return LinearFunction.apply(x, W, bias, act, residual, out_dtype)

@@ -5,6 +5,7 @@
 // synchronises, reads device memory back or allocates: the whole layer can be
 // captured in a HIP graph ([GG] "Failure modes": no host sync per layer;
 // [GG] = "Grouped GEMM for MoE, in depth").
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -167,7 +168,9 @@ bool gated_mfma(int32_t dtype, int64_t K, int64_t F, int64_t N) {
 const char *const kFamilies[] = {"build_schedule", "fill_zero", "grouped_gemm", "fused_fwd",
                                  "bwd_dx", "bwd_dw", "tile_map", "gated_up", "gated_down",
                                  "fused_fwd_fp8", "gated_bwd_dw_down", "gated_bwd_dh",
-                                 "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx"};
+                                 "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx", "route_fwd",
+                                 "route_bwd", "router_loss_fwd", "router_loss_bwd", "linear_fwd",
+                                 "linear_bwd"};
 constexpr int kNumFamilies = sizeof(kFamilies) / sizeof(kFamilies[0]);
 
 struct Timing {
@@ -212,7 +215,8 @@ hipError_t timed(int fam, hipStream_t st, F &&f) {
 }
 
 enum { F_SCHED = 0, F_FILL, F_BARE, F_FWD, F_DX, F_DW, F_TILEMAP, F_GATED_UP, F_GATED_DOWN,
-       F_FWD_FP8, F_GB_DWD, F_GB_DH, F_GB_DX, F_GB_DWGU, F_FWD_MX };
+       F_FWD_FP8, F_GB_DWD, F_GB_DH, F_GB_DX, F_GB_DWGU, F_FWD_MX, F_ROUTE_FWD, F_ROUTE_BWD,
+       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD };
 
 }  // namespace
 }  // namespace moe
@@ -233,6 +237,7 @@ const char *moe_status_string(int status) {
     case MOE_ERR_WORKSPACE: return "workspace NULL or too small";
     case MOE_ERR_HIP: return "HIP runtime error at launch";
     case MOE_ERR_LIMIT: return "a size exceeds a library limit";
+    case MOE_ERR_OPTION: return "an option is unknown or out of range";
     default: return "unknown status";
   }
 }
@@ -613,6 +618,170 @@ int moe_fused_bwd(const void *dY, const void *x, const void *W, const moe_schedu
   if (e == hipSuccess && dW && !dw_first)
     e = timed(F_DW, st, [&] { return simt_bwd_dw(dY, x, s, dW, (int)K, (int)N, dtype, st); });
   return hip_status(e);
+}
+
+}  // extern "C"
+
+namespace moe {
+namespace {
+// sizes and score of the routing calls
+int check_route(int64_t T, int32_t E, int32_t k, int32_t score, int32_t dtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (T < 0 || E < 1 || k < 1 || k > 64 || k > E) return MOE_ERR_SHAPE;
+  if (E > kMaxExperts || T * k >= kMax32) return MOE_ERR_LIMIT;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_OPTION;
+  return MOE_OK;
+}
+bool scale_ok(float s) { return isfinite(s) && s > 0.f; }
+
+int check_linear(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype, int32_t out_dtype) {
+  if (dtype == MOE_F32 ? out_dtype != MOE_F32
+                       : dtype != MOE_BF16 || (out_dtype != MOE_F32 && out_dtype != MOE_BF16))
+    return MOE_ERR_DTYPE;
+  if (M < 0 || K < 1 || N < 1) return MOE_ERR_SHAPE;
+  // tile indices are 32-bit, with room for a partial tile
+  if (M >= kMax32 - 512 || K >= kMax32 - 512 || N >= kMax32 - 512) return MOE_ERR_LIMIT;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return MOE_ERR_OPTION;
+  return MOE_OK;
+}
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_route_fwd(const void *logits, const float *bias, int64_t T, int32_t E, int32_t k,
+                  int32_t score, int32_t groups, int32_t topk_groups, int32_t group_score,
+                  int32_t renormalize, float scale, int32_t *expert_ids, float *topk_weights,
+                  int32_t dtype, void *stream) {
+  int rc = check_route(T, E, k, score, dtype);
+  if (rc) return rc;
+  if (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2) return MOE_ERR_OPTION;
+  if (groups < 1 || groups > 64 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+      k > topk_groups * (E / groups) || !scale_ok(scale))
+    return MOE_ERR_OPTION;
+  if (groups > 1 && group_score == MOE_GROUP_TOP2 && E / groups < 2) return MOE_ERR_OPTION;
+  if (T == 0) return MOE_OK;
+  if (!logits || !expert_ids || !topk_weights) return MOE_ERR_NULL;
+  if (!aligned(logits, esize(dtype)) || (bias && !aligned(bias, 4)) || !aligned(expert_ids, 4) ||
+      !aligned(topk_weights, 4))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_ROUTE_FWD, st, [&] {
+    return launch_route_fwd(logits, bias, T, E, k, score == MOE_SCORE_SIGMOID, groups, topk_groups,
+                            group_score == MOE_GROUP_TOP2, renormalize != 0, scale, expert_ids,
+                            topk_weights, dtype, st);
+  }));
+}
+
+int moe_route_bwd(const float *d_weights, const void *logits, const int32_t *expert_ids,
+                  const float *topk_weights, int64_t T, int32_t E, int32_t k, int32_t score,
+                  int32_t renormalize, float scale, void *d_logits, int32_t dtype, void *stream) {
+  int rc = check_route(T, E, k, score, dtype);
+  if (rc) return rc;
+  if (!scale_ok(scale)) return MOE_ERR_OPTION;
+  if (T == 0) return MOE_OK;
+  if (!d_weights || !logits || !expert_ids || !topk_weights || !d_logits) return MOE_ERR_NULL;
+  if (!aligned(logits, esize(dtype)) || !aligned(d_logits, esize(dtype)) ||
+      !aligned(d_weights, 4) || !aligned(expert_ids, 4) || !aligned(topk_weights, 4))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_ROUTE_BWD, st, [&] {
+    return launch_route_bwd(d_weights, logits, expert_ids, topk_weights, T, E, k,
+                            score == MOE_SCORE_SIGMOID, renormalize != 0, scale, d_logits, dtype,
+                            st);
+  }));
+}
+
+size_t moe_router_loss_workspace_bytes(int64_t T, int32_t E) {
+  if (T < 0 || E < 1 || E > kMaxExperts) return 0;
+  return align256(loss_workspace_bytes(T, E));
+}
+
+int moe_router_loss_fwd(const void *logits, const int32_t *expert_ids, int64_t T, int32_t E,
+                        int32_t k, int32_t score, float *losses, float *stats, int32_t dtype,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_route(T, E, k, score, dtype);
+  if (rc) return rc;
+  if (!losses || !stats || (T > 0 && (!logits || !expert_ids))) return MOE_ERR_NULL;
+  const size_t need = moe_router_loss_workspace_bytes(T, E);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned(logits, esize(dtype)) || !aligned(expert_ids, 4) || !aligned(losses, 4) ||
+      !aligned(stats, 4) || (need && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_LOSS_FWD, st, [&] {
+    return launch_loss_fwd(logits, expert_ids, T, E, k, score == MOE_SCORE_SIGMOID, losses, stats,
+                           dtype, workspace, st);
+  }));
+}
+
+int moe_router_loss_bwd(const float *d_losses, const void *logits, const float *stats, int64_t T,
+                        int32_t E, int32_t score, void *d_logits, int32_t dtype, void *stream) {
+  int rc = check_route(T, E, 1, score, dtype);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!d_losses || !logits || !stats || !d_logits) return MOE_ERR_NULL;
+  if (!aligned(logits, esize(dtype)) || !aligned(d_logits, esize(dtype)) ||
+      !aligned(d_losses, 4) || !aligned(stats, 4))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_LOSS_BWD, st, [&] {
+    return launch_loss_bwd(d_losses, logits, stats, T, E, score == MOE_SCORE_SIGMOID, d_logits,
+                           dtype, st);
+  }));
+}
+
+size_t moe_linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t dtype) {
+  if (check_linear(M, K, N, MOE_ACT_NONE, dtype, MOE_F32)) return 0;
+  return align256(linear_fwd_workspace(M, K, N, dtype));
+}
+
+int moe_linear_fwd(const void *x, const void *W, const void *bias, const void *residual, void *out,
+                   void *z, int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype,
+                   int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_linear(M, K, N, act, dtype, out_dtype);
+  if (rc) return rc;
+  if (M == 0) return MOE_OK;
+  if (!x || !W || !out) return MOE_ERR_NULL;
+  const size_t need = moe_linear_fwd_workspace_bytes(M, K, N, dtype);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  const size_t es = esize(dtype), eo = esize(out_dtype);
+  if (!aligned(x, es) || !aligned(W, es) || !aligned(bias, es) || !aligned(z, es) ||
+      !aligned(residual, eo) || !aligned(out, eo) || (need && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_LIN_FWD, st, [&] {
+    return launch_linear_fwd(x, W, bias, residual, out, z, (int)M, (int)K, (int)N, act, dtype,
+                             out_dtype, workspace, st);
+  }));
+}
+
+size_t moe_linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype,
+                                      int32_t out_dtype) {
+  if (check_linear(M, K, N, act, dtype, out_dtype)) return 0;
+  return align256(linear_bwd_workspace(M, K, N, act, dtype, out_dtype));
+}
+
+int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *z, void *dX,
+                   void *dW, void *d_bias, int64_t M, int64_t K, int64_t N, int32_t act,
+                   int32_t dtype, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+  int rc = check_linear(M, K, N, act, dtype, out_dtype);
+  if (rc) return rc;
+  if (M > 0 && (!d_out || (dX && !W) || (dW && !x) || (act != MOE_ACT_NONE && !z)))
+    return MOE_ERR_NULL;
+  const size_t need = moe_linear_bwd_workspace_bytes(M, K, N, act, dtype, out_dtype);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  const size_t es = esize(dtype);
+  if (!aligned(d_out, esize(out_dtype)) || !aligned(x, es) || !aligned(W, es) || !aligned(z, es) ||
+      !aligned(dX, es) || !aligned(dW, es) || !aligned(d_bias, es) ||
+      (need && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_LIN_BWD, st, [&] {
+    return launch_linear_bwd(d_out, x, W, z, dX, dW, d_bias, (int)M, (int)K, (int)N, act, dtype,
+                             out_dtype, workspace, st);
+  }));
 }
 
 int moe_tile_map(const moe_schedule *sched, int64_t N, int32_t BM, int32_t BN, int32_t *tile_start,

@@ -165,6 +165,30 @@ hipError_t mfma_gated_bwd_dh(const void *dY, const void *h, const void *W_down,
 // gated FFN backward: dX[t] += dgu[r] W_gu[e] (dgu by row, unweighted scatter)
 hipError_t mfma_gated_bwd_dx(const void *dgu, const void *W_gu, const moe_schedule &s, float *dX,
                              int K, int F, hipStream_t st);
+
+// routing and router losses (E <= kMaxExperts, k <= 64)
+hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, int E, int k,
+                            bool sigmoid, int groups, int keep, bool top2, bool renorm,
+                            float scale, int32_t *ids, float *w, int dtype, hipStream_t st);
+hipError_t launch_route_bwd(const float *g, const void *logits, const int32_t *ids, const float *w,
+                            int64_t T, int E, int k, bool sigmoid, bool renorm, float scale,
+                            void *d, int dtype, hipStream_t st);
+size_t loss_workspace_bytes(int64_t T, int E);
+hipError_t launch_loss_fwd(const void *logits, const int32_t *ids, int64_t T, int E, int k,
+                           bool sigmoid, float *losses, float *stats, int dtype, void *ws,
+                           hipStream_t st);
+hipError_t launch_loss_bwd(const float *dloss, const void *logits, const float *stats, int64_t T,
+                           int E, bool sigmoid, void *d, int dtype, hipStream_t st);
+
+// dense linear layer (act: MOE_ACT_*)
+size_t linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype);
+size_t linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int act, int dtype, int out_dtype);
+hipError_t launch_linear_fwd(const void *x, const void *W, const void *bias, const void *res,
+                             void *out, void *z, int M, int K, int N, int act, int dtype,
+                             int out_dtype, void *ws, hipStream_t st);
+hipError_t launch_linear_bwd(const void *dout, const void *x, const void *W, const void *z,
+                             void *dX, void *dW, void *db, int M, int K, int N, int act, int dtype,
+                             int out_dtype, void *ws, hipStream_t st);
 }  // namespace moe
 
 namespace moe {
