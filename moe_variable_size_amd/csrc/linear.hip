@@ -4,6 +4,8 @@
 //
 // All three products have one form, C[m, n] = sum_k A(m, k) B(n, k): for each operand either the
 // reduction index (K-major) or the output index (MN-major) is contiguous in memory.
+#include <stdlib.h>
+
 #include <type_traits>
 
 #include "common.hpp"
@@ -20,14 +22,38 @@ MOE_DEV void stf(float *p, float v) { *p = v; }
 MOE_DEV void stf(bf16_t *p, float v) { *p = __builtin_bit_cast(bf16_t, (__bf16)v); }
 
 // ---- activations ------------------------------------------------------------
-MOE_DEV float sigmoidf(float t) { return 1.f / (1.f + __expf(-t)); }
+MOE_DEV float sigmoidf(float t) { return __builtin_amdgcn_rcpf(1.f + __expf(-t)); }
 constexpr float kTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
+
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  The upper tail Q(x) = 1 - Phi(x),
+// x = |z|, is e G(x) with G(x) = erfcx(x / sqrt 2) / 2, fitted as a polynomial in t = 1 / (1 + 0.3 x)
+// by least squares of the relative error on Chebyshev nodes over 0 <= x <= 14 (beyond, e is 0):
+// relative error 7e-8, so the tail keeps its relative precision, where 1 + erf(z / sqrt 2) would
+// cancel.  One exponential, one reciprocal, 8 multiply-adds.
+MOE_DEV float normal_cdf(float z, float &e) {
+  const float x = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.f));
+  e = __expf(-0.5f * x * x);
+  float g = 3.88709204e-2f;
+  g = fmaf(g, t, -1.71443555e-1f);
+  g = fmaf(g, t, 2.33107471e-1f);
+  g = fmaf(g, t, -8.12823041e-2f);
+  g = fmaf(g, t, 1.45609827e-1f);
+  g = fmaf(g, t, 9.34725846e-2f);
+  g = fmaf(g, t, 1.22204592e-1f);
+  g = fmaf(g, t, 1.19451402e-1f);
+  g = fmaf(g, t, 9.09630867e-6f);
+  const float q = e * g;
+  return z < 0.f ? q : 1.f - q;
+}
 
 template <int ACT>
 MOE_DEV float act_fwd(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
-  if constexpr (ACT == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+  if constexpr (ACT == MOE_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   // 0.5 (1 + tanh u) = sigmoid(2 u)
   if constexpr (ACT == MOE_ACT_GELU_TANH)
     return z * sigmoidf(2.f * kTanhC * (z + kTanhA * z * z * z));
@@ -38,8 +64,11 @@ MOE_DEV float act_fwd(float z) {
 template <int ACT>
 MOE_DEV float act_grad(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == MOE_ACT_GELU)
-    return 0.5f * erfcf(-0.70710678f * z) + z * 0.3989422804f * __expf(-0.5f * z * z);
+  if constexpr (ACT == MOE_ACT_GELU) {
+    float e;
+    const float c = normal_cdf(z, e);
+    return fmaf(z * 0.3989422804f, e, c);
+  }
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     const float s = sigmoidf(2.f * kTanhC * (z + kTanhA * z * z * z)), t = s * (1.f - s);
     // far out t is 0 and its factor may overflow
@@ -70,74 +99,75 @@ struct GemmArgs {
   void *out, *z;           // [M, N]; z (operand type) NULL: not kept
   int M, N, K;
   int64_t lda, ldb;  // K-major: elements between rows; MN-major: between reduction rows
-  bool quad;         // N a multiple of 4, out, z, residual and bias on lines of four elements
+  bool vec;          // N a multiple of 8; out, z, residual and bias on 16-byte lines
 };
 
 // ---- epilogue -----------------------------------------------------------------
-// four values of one row at columns n .. n+3, `left` >= 1 of them inside the row; quad: rows are
-// multiples of 4 elements and the pointers on 16-byte (fp32) or 8-byte (bf16) lines, so all four
-// are inside and moved at once
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-MOE_DEV f32x4 get4(const float *p, int left, bool quad) {
-  if (quad) return *(const f32x4 *)p;
-  f32x4 v = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) if (i < left) v[i] = p[i];
-  return v;
+MOE_DEV f32x4 get4(const float *p) { return *(const f32x4 *)p; }
+MOE_DEV f32x4 get4(const bf16_t *p) {
+  const bf16x4_t b = *(const bf16x4_t *)p;
+  return f32x4{(float)b[0], (float)b[1], (float)b[2], (float)b[3]};
 }
-MOE_DEV f32x4 get4(const bf16_t *p, int left, bool quad) {
-  f32x4 v = {};
-  if (quad) {
-    const bf16x4_t b = *(const bf16x4_t *)p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)b[i];
-    return v;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) if (i < left) v[i] = ldf(p + i);
-  return v;
+MOE_DEV void put8(float *p, const f32x4 (&v)[2]) {
+  *(f32x4 *)p = v[0];
+  *(f32x4 *)(p + 4) = v[1];
 }
-MOE_DEV void put4(float *p, f32x4 v, int left, bool quad) {
-  if (quad) { *(f32x4 *)p = v; return; }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) if (i < left) p[i] = v[i];
+MOE_DEV void put8(bf16_t *p, const f32x4 (&v)[2]) {
+  *(bf16x8_t *)p = bf16x8_t{(__bf16)v[0][0], (__bf16)v[0][1], (__bf16)v[0][2], (__bf16)v[0][3],
+                            (__bf16)v[1][0], (__bf16)v[1][1], (__bf16)v[1][2], (__bf16)v[1][3]};
 }
-MOE_DEV void put4(bf16_t *p, f32x4 v, int left, bool quad) {
-  if (quad) {
-    *(bf16x4_t *)p = bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) if (i < left) stf(p + i, v[i]);
-}
-// z = v + bias, out = act(z) + residual
+// from z = product + bias: keep z, out = act(z) + residual, for 8 columns on a 16-byte line or one
 template <typename T, typename To, int ACT>
-MOE_DEV void finish4(const GemmArgs &p, f32x4 v, int n, int64_t at, bool quad) {
-  const int left = p.N - n;
-  if (p.bias) v += get4((const T *)p.bias + n, left, quad);
-  if (p.z) put4((T *)p.z + at, v, left, quad);
-  if constexpr (ACT != MOE_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_fwd<ACT>(v[i]);
+MOE_DEV void finish8(const GemmArgs &p, f32x4 (&v)[2], int64_t at) {
+  f32x4 r[2] = {};
+  if (p.res) {
+    r[0] = get4((const To *)p.res + at);
+    r[1] = get4((const To *)p.res + at + 4);
   }
-  if (p.res) v += get4((const To *)p.res + at, left, quad);
-  put4((To *)p.out + at, v, left, quad);
+  if (p.z) put8((T *)p.z + at, v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[h][i] = act_fwd<ACT>(v[h][i]) + r[h][i];
+  put8((To *)p.out + at, v);
+}
+template <typename T, typename To, int ACT>
+MOE_DEV void finish1(const GemmArgs &p, float v, int64_t at) {
+  if (p.z) stf((T *)p.z + at, v);
+  v = act_fwd<ACT>(v);
+  if (p.res) v += ldf((const To *)p.res + at);
+  stf((To *)p.out + at, v);
 }
 
-// out[m, n .. n+3] from the partial products of all ranges, added in order
+// out from the partial products of all ranges, added in order
 template <typename T, typename To, int ACT>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part, int splits) {
-  const int per = (p.N + 3) / 4;
-  const int64_t total = (int64_t)p.M * per, size = (int64_t)p.M * p.N;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per;
-    const int n = (int)(i - m * per) * 4;
-    const int64_t at = m * p.N + n;
-    const bool pq = (p.N & 3) == 0;
-    f32x4 v = get4(part + at, p.N - n, pq);
-    for (int s = 1; s < splits; ++s) v += get4(part + s * size + at, p.N - n, pq);
-    finish4<T, To, ACT>(p, v, n, at, p.quad);
+  const int64_t total = (int64_t)p.M * p.N, step = (int64_t)gridDim.x * 256;
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (p.vec) {
+    for (int64_t at = i0 * 8; at < total; at += step * 8) {
+      f32x4 v[2] = {get4(part + at), get4(part + at + 4)};
+#pragma unroll 4
+      for (int s = 1; s < splits; ++s) {
+        v[0] += get4(part + s * total + at);
+        v[1] += get4(part + s * total + at + 4);
+      }
+      if (p.bias) {
+        const int n = (int)(at % p.N);
+        v[0] += get4((const T *)p.bias + n);
+        v[1] += get4((const T *)p.bias + n + 4);
+      }
+      finish8<T, To, ACT>(p, v, at);
+    }
+  } else {
+    for (int64_t at = i0; at < total; at += step) {
+      float v = part[at];
+      for (int s = 1; s < splits; ++s) v += part[s * total + at];
+      if (p.bias) v += ldf((const T *)p.bias + at % p.N);
+      finish1<T, To, ACT>(p, v, at);
+    }
   }
 }
 
@@ -242,13 +272,7 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int m = m0 + wm + i * 32 + acc_row(e, lane);
-        if (m >= p.M) continue;
-        const int64_t at = (int64_t)m * p.N + n;
-        float v = acc[i][j][e] + b;
-        if (p.z) stf((T *)p.z + at, v);
-        v = act_fwd<ACT>(v);
-        if (p.res) v += ldf((const To *)p.res + at);
-        stf((To *)p.out + at, v);
+        if (m < p.M) finish1<T, To, ACT>(p, acc[i][j][e] + b, (int64_t)m * p.N + n);
       }
   }
 }
@@ -264,10 +288,13 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p) {
 // multiply part, with a barrier after each.  The waves of the second half of the workgroup run
 // one part behind, so on every SIMD one wave multiplies while the other loads.
 //
-// Order of issue: A0 B0 B1 of a stage two ahead (into the buffer whose halves the quarters before
-// have read), A1 of the next.  A half is waited for one quarter before its first read, five
-// halves after its issue.  The reads of a memory part are complete (lgkmcnt 0) before its
-// barrier, so the halves it read may be overwritten after it.
+// Order of issue, one half per quarter: B1 and A1 of the next stage, A0 and B0 of the one after.
+// A half goes into the place of one that was read two or more quarters before.  The multiply part
+// of a quarter consumes the quarter's reads (A0's first step is read a quarter early and consumed
+// in the next), and both groups of waves have ended that part before either is two quarters on, so
+// no read of the overwritten half is outstanding.  A half is waited for one quarter before its
+// first read, when four younger ones are in flight.  (Reads waited for in the memory part instead,
+// which allows one quarter more of lead: 198 us for 8192 x 4096 x 4096.)
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 #define LDS_AS __attribute__((address_space(3)))
@@ -373,7 +400,7 @@ struct PipeArgs {
 };
 
 template <int HM, int HN, int WGM, int WGN, bool AK, bool BKM, typename To, int ACT>
-__global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
+__global__ __launch_bounds__(512, HM * HN >= 4 ? 2 : 4) void piped_gemm(PipeArgs q) {
   constexpr int BM = 32 * HM * WGM, BN = 32 * HN * WGN, WA = BM / 2, WB = BN / 2;
   constexpr int AH = WA * 128, BH = WB * 128, STG = 2 * (AH + BH);
   constexpr int PA = HalfTile<WA, AK>::PER, PB = HalfTile<WB, BKM>::PER;
@@ -422,8 +449,8 @@ __global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
       for (int s = 0; s < 2; ++s)
         fb[half][i][s] = frag<WB, BKM>(lds + buf * STG + 2 * AH + half * BH, wn * 16 * HN + i * 16, s, lane);
   };
-  auto arrive = [&](auto VM) __attribute__((always_inline)) {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(VM)::value) : "memory");
+  auto arrive = [&]() __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PA + 2 * PB) : "memory");
     LIN_FENCE();
     __builtin_amdgcn_s_barrier();
     LIN_FENCE();
@@ -443,42 +470,35 @@ __global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
     __builtin_amdgcn_s_barrier();
     LIN_FENCE();
   };
-  using V1 = std::integral_constant<int, 3 * PA + 2 * PB>;
-  using V2 = std::integral_constant<int, 2 * PA + 3 * PB>;
-
   issueA(0, kb);
   issueB(0, kb);
   issueB(1, kb);
   issueA(1, kb);
   issueA(0, kb + 1);
   issueB(0, kb + 1);
-  issueB(1, kb + 1);
-  arrive(V2());
+  arrive();
   readA(0, 0, 0, fan);
-  if (wid >= 4) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-  }
+  if (wid >= 4) __builtin_amdgcn_s_barrier();
   LIN_FENCE();
   auto stage = [&](int kt, auto BUF) __attribute__((always_inline)) {
     constexpr int buf = decltype(BUF)::value;
     readB(buf, 0);
     readA(buf, 0, 1, fa[1]);
-    issueA(1, kt + 1);
-    arrive(V1());
+    issueB(1, kt + 1);
+    arrive();
     multiply(0, 0, fan, fa[1]);
     readB(buf, 1);
-    issueA(0, kt + 2);
-    arrive(V1());
+    issueA(1, kt + 1);
+    arrive();
     multiply(0, 1, fan, fa[1]);
     readA(buf, 1, 0, fa[0]);
     readA(buf, 1, 1, fa[1]);
-    issueB(0, kt + 2);
-    arrive(V2());
+    issueA(0, kt + 2);
+    arrive();
     multiply(1, 1, fa[0], fa[1]);
     readA(buf ^ 1, 0, 0, fan);
-    issueB(1, kt + 2);
-    arrive(V2());
+    issueB(0, kt + 2);
+    arrive();
     multiply(1, 0, fa[0], fa[1]);
   };
   int kt = kb;
@@ -488,67 +508,150 @@ __global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
   }
   if (kt < ke) stage(kt, std::integral_constant<int, 0>());
   if (wid < 4) __builtin_amdgcn_s_barrier();
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (zeros for stages that are not there)
+  // zeros for stages that are not there, and the last early read, before the LDS is used again
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 
-  // lane l of a 16 x 16 block: row l & 15, columns 4 (l >> 4) .. +3
-  const bool quad = p.quad;
+  // Epilogue, half the rows at a time through LDS as fp32 [WA][BN], so that each row's columns are
+  // read and written in whole lines (16 bytes of bf16 per lane): stored from the accumulators'
+  // own layout, 32 bytes a row, the same case took 324 us.  16-byte chunk c of row r sits at place
+  // c ^ (r & 15): the 16 rows of an accumulator store fall on 16 bank groups.
+  auto chunk = [&](int r, int c) __attribute__((always_inline)) {
+    return (f32x4 *)(lds + r * (BN * 4) + ((c ^ (r & 15)) << 4));
+  };
+  constexpr int LPR = BN / 8, RPP = 512 / LPR;  // lanes per row, rows per pass of the workgroup
+  const bool part = q.splits > 1;
+  float *const pout = q.part + (int64_t)split * p.M * p.N;
 #pragma unroll
-  for (int mh = 0; mh < 2; ++mh)
+  for (int mh = 0; mh < 2; ++mh) {
+    __syncthreads();
+    // lane l of a 16 x 16 block: row l & 15, columns 4 (l >> 4) .. +3
 #pragma unroll
-    for (int i = 0; i < HM; ++i) {
-      const int m = m0 + mh * WA + wm * 16 * HM + i * 16 + (lane & 15);
-      if (m >= p.M) continue;
+    for (int i = 0; i < HM; ++i)
 #pragma unroll
       for (int nh = 0; nh < 2; ++nh)
 #pragma unroll
-        for (int j = 0; j < HN; ++j) {
-          const int n = n0 + nh * WB + wn * 16 * HN + j * 16 + 4 * (lane >> 4);
-          if (n >= p.N) continue;
-          const f32x4 v = acc[mh][nh][i][j];
-          const int64_t at = (int64_t)m * p.N + n;
-          if (q.splits > 1)
-            put4(q.part + (int64_t)split * p.M * p.N + at, v, p.N - n, (p.N & 3) == 0);
-          else
-            finish4<bf16_t, To, ACT>(p, v, n, at, quad);
+        for (int j = 0; j < HN; ++j)
+          *chunk(wm * 16 * HM + i * 16 + (lane & 15),
+                 (nh * WB + wn * 16 * HN + j * 16) / 4 + (lane >> 4)) = acc[mh][nh][i][j];
+    __syncthreads();
+    const int r0 = threadIdx.x / LPR, c0 = (threadIdx.x % LPR) * 8;
+    if (p.vec) {
+      if (n0 + c0 >= p.N) continue;
+      f32x4 b[2] = {};
+      if (p.bias && !part) {
+        b[0] = get4((const bf16_t *)p.bias + n0 + c0);
+        b[1] = get4((const bf16_t *)p.bias + n0 + c0 + 4);
+      }
+#pragma unroll 4
+      for (int r = r0; r < WA; r += RPP) {
+        const int m = m0 + mh * WA + r;
+        if (m >= p.M) break;
+        const int64_t at = (int64_t)m * p.N + n0 + c0;
+        f32x4 v[2] = {*chunk(r, c0 / 4), *chunk(r, c0 / 4 + 1)};
+        if (part) {
+          put8(pout + at, v);
+          continue;
         }
+        v[0] += b[0];
+        v[1] += b[1];
+        finish8<bf16_t, To, ACT>(p, v, at);
+      }
+    } else {
+      for (int r = r0; r < WA; r += RPP) {
+        const int m = m0 + mh * WA + r;
+        if (m >= p.M) break;
+        for (int c = threadIdx.x % LPR; c < BN && n0 + c < p.N; c += LPR) {
+          const int64_t at = (int64_t)m * p.N + n0 + c;
+          const float v = ((const float *)chunk(r, c >> 2))[c & 3];
+          if (part)
+            pout[at] = v;
+          else
+            finish1<bf16_t, To, ACT>(p, v + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
+        }
+      }
     }
+  }
 }
 
 // ---- dz and the bias gradient ---------------------------------------------------
-// Block (bx, by): columns 64 bx .. +63, rows by, by + gridDim.y, ... (4 at a time).  Each block's
-// column sums go to part[by][N]; bias_join adds them in order.
-constexpr int DZ_BLOCKS = 64;
+// Block (bx, by): 32 V columns from 32 V bx, rows from a contiguous range, 8 at a time; V columns
+// (16 bytes of bf16 for V = 8) per thread.  Each block's column sums go to part[by][N]; bias_join
+// adds them in order.  V = 8 where rows are on 16-byte lines.
+constexpr int DZ_RANGES = 128;  // row ranges (at most)
 
-template <typename T, typename To, int ACT>
+template <typename T, int V>
+MOE_DEV void getv(const T *p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const f32x4 a = get4(p), b = get4(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+  } else {
+    v[0] = ldf(p);
+  }
+}
+template <typename T, int V>
+MOE_DEV void putv(T *p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    const f32x4 h[2] = {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
+    put8(p, h);
+  } else {
+    stf(p, v[0]);
+  }
+}
+
+template <typename T, typename To, int ACT, int V>
 __global__ __launch_bounds__(256) void dz_kernel(const To *__restrict__ dout,
                                                  const T *__restrict__ z, T *__restrict__ dz,
                                                  float *__restrict__ part, int64_t M, int N) {
-  __shared__ float red[256];
-  const int n = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  float sum = 0.f;
-  if (n < N)
-    for (int64_t m = (int64_t)blockIdx.y * 4 + q; m < M; m += (int64_t)gridDim.y * 4) {
+  __shared__ float red[8][32 * V + 1];
+  const int n = blockIdx.x * 32 * V + (threadIdx.x & 31) * V, q = threadIdx.x >> 5;
+  const int64_t lo = M * blockIdx.y / gridDim.y, hi = M * (blockIdx.y + 1) / gridDim.y;
+  float sum[V] = {};
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t m = lo + q; m < hi; m += 8) {
       const int64_t at = m * N + n;
-      float d = ldf(dout + at);
-      if constexpr (ACT != MOE_ACT_NONE) d *= act_grad<ACT>(ldf(z + at));
-      if (dz) stf(dz + at, d);
-      sum += d;
+      float d[V], zz[V];
+      getv<To, V>(dout + at, d);
+      if constexpr (ACT != MOE_ACT_NONE) {
+        getv<T, V>(z + at, zz);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= act_grad<ACT>(zz[i]);
+      }
+      if (dz) putv<T, V>(dz + at, d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += d[i];
     }
+  }
   if (!part) return;
-  red[threadIdx.x] = sum;
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[q][(threadIdx.x & 31) * V + i] = sum[i];
   __syncthreads();
-  if (q == 0 && n < N)
-    part[(size_t)blockIdx.y * N + n] =
-        (red[threadIdx.x] + red[threadIdx.x + 64]) + (red[threadIdx.x + 128] + red[threadIdx.x + 192]);
+  const int c = threadIdx.x, nc = blockIdx.x * 32 * V + c;
+  if (c < 32 * V && nc < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][c];
+    part[(size_t)blockIdx.y * N + nc] = s;
+  }
 }
 
+// 64 columns per block, 16 threads each
 template <typename T>
-__global__ __launch_bounds__(256) void bias_join(const float *__restrict__ part, T *db, int N, int blocks) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+__global__ __launch_bounds__(1024) void bias_join(const float *__restrict__ part, T *db, int N, int ranges) {
+  __shared__ float red[16][65];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
   float s = 0.f;
-  for (int b = 0; b < blocks; ++b) s += part[(size_t)b * N + n];
-  stf(db + n, s);
+  if (n < N)
+    for (int b = q; b < ranges; b += 16) s += part[(size_t)b * N + n];
+  red[q][c] = s;
+  __syncthreads();
+  if (q == 0 && n < N) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[i][c];
+    stf(db + n, s);
+  }
 }
 
 bool on_line(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
@@ -580,19 +683,48 @@ hipError_t run_piped(PipeArgs &q, int act, hipStream_t st) {
   return e;
 }
 
+// Tile shape and number of reduction ranges of a product of M x N outputs.
+struct Plan {
+  int shape, splits;  // shape: 0 = 256 x 256, 1 = 256 x 128, 2 = 128 x 128
+};
+constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  static const char *force = getenv("LIN_PLAN");
+  if (force) return Plan{force[0] - '0', atoi(force + 2)};
+  return Plan{0, 1};
+}
+size_t part_bytes(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_of(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
+}
+
+// workspace `part`: part_bytes(M, N, K)
 template <bool AK, bool BKM, typename T, typename To>
-hipError_t gemm(GemmArgs a, int act, hipStream_t st) {
-  a.quad = a.N % 4 == 0 && on_line(a.out, 4 * sizeof(To)) && on_line(a.res, 4 * sizeof(To)) &&
-           on_line(a.bias, 4 * sizeof(T)) && on_line(a.z, 4 * sizeof(T));
+hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
+  a.vec = a.N % 8 == 0 && on_line(a.out, 16) && on_line(a.res, 16) && on_line(a.bias, 16) &&
+          on_line(a.z, 16);
   if constexpr (sizeof(T) == 2) {
     // 16-byte chunks of both operands lie wholly inside or outside their rows
     const int64_t ra = AK ? a.M : a.K, rb = BKM ? a.N : a.K;
     const bool chunks = a.lda % 8 == 0 && a.ldb % 8 == 0 && on_line(a.A, 16) && on_line(a.B, 16);
     const int64_t ab = 2 * ra * a.lda, bb = 2 * rb * a.ldb;
-    // offsets of rows up to a tile past the end must not wrap
-    if (chunks && a.lda <= (1 << 21) && a.ldb <= (1 << 21) && ab < (int64_t)kOobOffset && bb < (int64_t)kOobOffset && a.K > 0) {
-      PipeArgs q{a, (uint32_t)ab, (uint32_t)bb, 0, 0, 1, nullptr};
-      return run_piped<4, 2, 2, 4, AK, BKM, To>(q, act, st);
+    // 32-bit offsets, of rows up to a tile past the end too
+    const bool small = a.lda <= (1 << 20) && a.ldb <= (1 << 20) && a.N <= (1 << 20) &&
+                       ab < (int64_t)kOobOffset && bb < (int64_t)kOobOffset;
+    if (chunks && small && a.K > 0) {
+      const Plan pl = plan_of(a.M, a.N, a.K);
+      PipeArgs q{a, (uint32_t)ab, (uint32_t)bb, 0, 0, pl.splits, (float *)part};
+      const hipError_t e = pl.shape == 0   ? run_piped<4, 2, 2, 4, AK, BKM, To>(q, act, st)
+                           : pl.shape == 1 ? run_piped<2, 2, 4, 2, AK, BKM, To>(q, act, st)
+                                           : run_piped<2, 1, 2, 4, AK, BKM, To>(q, act, st);
+      if (e != hipSuccess || pl.splits == 1) return e;
+      const int64_t groups = (int64_t)a.M * a.N / (a.vec ? 8 : 1);
+      const int grid = (int)(groups < 256 * 4096 ? (groups + 255) / 256 : 4096);
+      by_act_of<AK && BKM>(act, [&](auto A) {
+        join_kernel<T, To, decltype(A)::value><<<grid, 256, 0, st>>>(a, (const float *)part, pl.splits);
+      });
+      return hipGetLastError();
     }
   }
   const int grid = ((a.N + SBN - 1) / SBN) * ((a.M + SBM - 1) / SBM);
@@ -604,53 +736,75 @@ hipError_t gemm(GemmArgs a, int act, hipStream_t st) {
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 bool needs_dz(int act, int dtype, int out_dtype) { return act != MOE_ACT_NONE || dtype != out_dtype; }
-int dz_blocks(int64_t M) { return (int)(M < 4 * DZ_BLOCKS ? (M + 3) / 4 : DZ_BLOCKS); }
+int dz_ranges(int64_t M) { return (int)(M < 8 * DZ_RANGES ? (M + 7) / 8 : DZ_RANGES); }
+
+// workspace of the backward: dz, the column sums' parts, the partial products of dX or dW
+struct BwdSpace {
+  size_t dz, sums, part, total;
+};
+BwdSpace bwd_space(int64_t M, int64_t K, int64_t N, bool own_dz, int dtype) {
+  BwdSpace w;
+  w.dz = 0;
+  w.sums = own_dz ? up256((size_t)M * N * (dtype == MOE_F32 ? 4 : 2)) : 0;
+  w.part = w.sums + up256((size_t)dz_ranges(M) * N * 4);
+  const size_t px = part_bytes(M, K, N), pw = part_bytes(N, K, M);
+  w.total = w.part + up256(px > pw ? px : pw);
+  return w;
+}
 
 template <typename T, typename To>
 hipError_t bwd(const void *dout, const void *x, const void *W, const void *z, void *dX, void *dW,
                void *db, int M, int K, int N, int act, bool own_dz, void *ws, hipStream_t st) {
+  const BwdSpace w = bwd_space(M, K, N, own_dz, sizeof(T) == 4 ? MOE_F32 : MOE_BF16);
   const T *d = own_dz ? (const T *)ws : (const T *)dout;
-  float *part = (float *)((char *)ws + (own_dz ? up256((size_t)M * N * sizeof(T)) : 0));
-  const int blocks = dz_blocks(M);
+  float *sums = (float *)((char *)ws + w.sums);
+  void *part = (char *)ws + w.part;
+  const int ranges = dz_ranges(M);
   hipError_t e = hipSuccess;
   if (M > 0 && ((own_dz && (dX || dW)) || db)) {
-    const dim3 grid((N + 63) / 64, blocks);
+    T *dz = own_dz && (dX || dW) ? (T *)ws : nullptr;
+    const bool wide = N % 8 == 0 && on_line(dout, 16) && on_line(z, 16);
     by_act(act, [&](auto A) {
-      dz_kernel<T, To, decltype(A)::value><<<grid, 256, 0, st>>>(
-          (const To *)dout, (const T *)z, own_dz ? (T *)ws : nullptr, db ? part : nullptr, M, N);
+      constexpr int ACT = decltype(A)::value;
+      if (wide)
+        dz_kernel<T, To, ACT, 8><<<dim3((N + 255) / 256, ranges), 256, 0, st>>>(
+            (const To *)dout, (const T *)z, dz, db ? sums : nullptr, M, N);
+      else
+        dz_kernel<T, To, ACT, 1><<<dim3((N + 31) / 32, ranges), 256, 0, st>>>(
+            (const To *)dout, (const T *)z, dz, db ? sums : nullptr, M, N);
     });
     e = hipGetLastError();
   }
   if (e == hipSuccess && db) {
-    bias_join<T><<<(N + 255) / 256, 256, 0, st>>>(part, (T *)db, N, M > 0 ? blocks : 0);
+    bias_join<T><<<(N + 63) / 64, 1024, 0, st>>>(sums, (T *)db, N, M > 0 ? ranges : 0);
     e = hipGetLastError();
   }
   if (e == hipSuccess && dX && M > 0)
     e = gemm<true, false, T, T>(GemmArgs{d, W, nullptr, nullptr, dX, nullptr, M, K, N, N, K, false},
-                                MOE_ACT_NONE, st);
+                                MOE_ACT_NONE, part, st);
   if (e == hipSuccess && dW)
     e = gemm<false, false, T, T>(GemmArgs{d, x, nullptr, nullptr, dW, nullptr, N, K, M, N, K, false},
-                                 MOE_ACT_NONE, st);
+                                 MOE_ACT_NONE, part, st);
   return e;
 }
 
 }  // namespace
 
-size_t linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype) { return 0; }
+size_t linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype) {
+  return dtype == MOE_BF16 ? part_bytes(M, N, K) : 0;
+}
 
 size_t linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int act, int dtype, int out_dtype) {
-  const size_t es = dtype == MOE_F32 ? 4 : 2;
-  return (needs_dz(act, dtype, out_dtype) ? up256((size_t)M * N * es) : 0) +
-         up256((size_t)dz_blocks(M) * N * 4);
+  return bwd_space(M, K, N, needs_dz(act, dtype, out_dtype), dtype).total;
 }
 
 hipError_t launch_linear_fwd(const void *x, const void *W, const void *bias, const void *res,
                              void *out, void *z, int M, int K, int N, int act, int dtype,
                              int out_dtype, void *ws, hipStream_t st) {
   const GemmArgs a{x, W, bias, res, out, z, M, N, K, K, K, false};
-  if (dtype == MOE_F32) return gemm<true, true, float, float>(a, act, st);
-  if (out_dtype == MOE_F32) return gemm<true, true, bf16_t, float>(a, act, st);
-  return gemm<true, true, bf16_t, bf16_t>(a, act, st);
+  if (dtype == MOE_F32) return gemm<true, true, float, float>(a, act, ws, st);
+  if (out_dtype == MOE_F32) return gemm<true, true, bf16_t, float>(a, act, ws, st);
+  return gemm<true, true, bf16_t, bf16_t>(a, act, ws, st);
 }
 
 hipError_t launch_linear_bwd(const void *dout, const void *x, const void *W, const void *z,
