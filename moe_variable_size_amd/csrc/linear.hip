@@ -26,14 +26,14 @@ MOE_DEV float sigmoidf(float t) { return __builtin_amdgcn_rcpf(1.f + __expf(-t))
 constexpr float kTanhC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  The upper tail Q(x) = 1 - Phi(x),
-// x = |z|, is e G(x) with G(x) = erfcx(x / sqrt 2) / 2, fitted as a polynomial in t = 1 / (1 + 0.3 x)
+// The normal distribution's upper tail Q(x) = 1 - Phi(x) at x = |z|, and e = exp(-x^2 / 2); z Phi(z) =
+// max(z, 0) - x Q(x).  Q = e G with G(x) = erfcx(x / sqrt 2) / 2, fitted as a polynomial in t = 1 / (1 + 0.3 x)
 // by least squares of the relative error on Chebyshev nodes over 0 <= x <= 14 (beyond, e is 0):
 // relative error 7e-8, so the tail keeps its relative precision, where 1 + erf(z / sqrt 2) would
 // cancel.  One exponential, one reciprocal, 8 multiply-adds.
-MOE_DEV float normal_cdf(float z, float &e) {
+MOE_DEV float normal_tail(float z, float &e) {
   const float x = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.f));
-  e = __expf(-0.5f * x * x);
+  e = __builtin_amdgcn_exp2f(-0.72134752f * x * x);  // 1 / (2 ln 2)
   float g = 3.88709204e-2f;
   g = fmaf(g, t, -1.71443555e-1f);
   g = fmaf(g, t, 2.33107471e-1f);
@@ -43,8 +43,7 @@ MOE_DEV float normal_cdf(float z, float &e) {
   g = fmaf(g, t, 1.22204592e-1f);
   g = fmaf(g, t, 1.19451402e-1f);
   g = fmaf(g, t, 9.09630867e-6f);
-  const float q = e * g;
-  return z < 0.f ? q : 1.f - q;
+  return e * g;
 }
 
 template <int ACT>
@@ -52,7 +51,7 @@ MOE_DEV float act_fwd(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
   if constexpr (ACT == MOE_ACT_GELU) {
     float e;
-    return z * normal_cdf(z, e);
+    return fmaf(-fabsf(z), normal_tail(z, e), fmaxf(z, 0.f));
   }
   // 0.5 (1 + tanh u) = sigmoid(2 u)
   if constexpr (ACT == MOE_ACT_GELU_TANH)
@@ -66,8 +65,8 @@ MOE_DEV float act_grad(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == MOE_ACT_GELU) {
     float e;
-    const float c = normal_cdf(z, e);
-    return fmaf(z * 0.3989422804f, e, c);
+    const float q = normal_tail(z, e);
+    return fmaf(z * 0.3989422804f, e, z < 0.f ? q : 1.f - q);
   }
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     const float s = sigmoidf(2.f * kTanhC * (z + kTanhA * z * z * z)), t = s * (1.f - s);
@@ -573,6 +572,93 @@ __global__ __launch_bounds__(512, HM * HN >= 4 ? 2 : 4) void piped_gemm(PipeArgs
   }
 }
 
+// ---- streamed products: few rows or few columns --------------------------------
+// For the forward's operands (both K-major, rows on 16-byte lines) with so few rows of x or of W
+// that reading the other one is the work: 16 TI x 16 TJ outputs per workgroup, whose NW waves
+// share the reduction (wave w takes the 64-element pieces w, w + NW, ..., whole 128-byte lines of
+// bf16) and add up through LDS in wave order.  Operands go from memory to registers, 16 bytes per
+// lane, D pieces ahead; the smaller operand comes out of L2.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <typename T>
+MOE_DEV f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  } else {
+    // element e of every lane's four is one reduction index of a 16 x 16 x 4 product
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
+    return c;
+  }
+}
+
+template <typename T, typename To, int ACT, int TI, int TJ, int NW, int D>
+__global__ __launch_bounds__(NW * 64) void stream_gemm(GemmArgs p) {
+  constexpr int TM = 16 * TI, TN = 16 * TJ, E = 16 / sizeof(T);  // elements per 16 bytes
+  constexpr int PIECE = 8 * E;
+  // [NW][TM][TN], the 16-byte chunks of row m at places XORed with m, so that a fragment's rows
+  // spread over the banks
+  __shared__ __align__(16) float red[NW * TM * TN];
+  auto cell = [](int w, int m, int n) __attribute__((always_inline)) {
+    return (w * TM + m) * TN + (n ^ ((m & (TN / 4 - 1)) * 4));
+  };
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tn = (p.N + TN - 1) / TN;
+  const int m0 = blockIdx.x / tn * TM, n0 = blockIdx.x % tn * TN;
+  const uint32_t rowb = (uint32_t)p.K * (uint32_t)sizeof(T);
+  const __amdgpu_buffer_rsrc_t ra =
+      uniform_rsrc((const T *)p.A + (int64_t)m0 * p.K, min(TM, p.M - m0) * rowb);
+  const __amdgpu_buffer_rsrc_t rb =
+      uniform_rsrc((const T *)p.B + (int64_t)n0 * p.K, min(TN, p.N - n0) * rowb);
+  const uint32_t base = (lane & 15) * rowb;
+  const int pieces = (p.K + PIECE - 1) / PIECE;
+  f32x4 acc[TI][TJ] = {};
+  u32x4 a[D][2][TI], b[D][2][TJ];
+  auto load = [&](int pc, int d) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int k = pc * PIECE + s * 4 * E + (lane >> 4) * E;
+      const uint32_t off = k < p.K ? base + k * (uint32_t)sizeof(T) : kOobOffset;
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+        a[d][s][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, off + i * 16 * rowb, 0, 0);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        b[d][s][j] = __builtin_amdgcn_raw_buffer_load_b128(rb, off + j * 16 * rowb, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wid + d * NW, d);
+  for (int pc = wid; pc < pieces; pc += D * NW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j] = mfma16<T>(b[d][s][j], a[d][s][i], acc[i][j]);
+      load(pc + (D + d) * NW, d);  // (past the end: nothing is read)
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      *(f32x4 *)&red[cell(wid, i * 16 + (lane & 15), j * 16 + 4 * (lane >> 4))] = acc[i][j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < TM * TN; e += NW * 64) {
+    const int m = m0 + e / TN, n = n0 + e % TN;
+    if (m >= p.M || n >= p.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += red[cell(w, e / TN, e % TN)];
+    if (p.bias) v += ldf((const T *)p.bias + n);
+    finish1<T, To, ACT>(p, v, (int64_t)m * p.N + n);
+  }
+}
+
 // ---- dz and the bias gradient ---------------------------------------------------
 // Block (bx, by): 32 V columns from 32 V bx, rows from a contiguous range, 8 at a time; V columns
 // (16 bytes of bf16 for V = 8) per thread.  Each block's column sums go to part[by][N]; bias_join
@@ -689,10 +775,38 @@ struct Plan {
 };
 constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};
 
+// The choice minimises an estimate in us: rounds of workgroups over the chip (256 CUs; two 128 x 128
+// workgroups fit one) times the stages of a range at the shape's measured time per stage, 6 us of
+// launch, first loads and epilogue, and for split reductions the join: a launch and the partial
+// products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 (8192 x 4096 x 4096: 198 us, the
+// others 240 and 252), 256 x 128 0.92 (4096 x 2048 x 2048: 38 us, 256 x 256 49), 128 x 128 0.55
+// alone on a CU and 1.0 in pairs (2048^3: 25 us, the others 44 and 32).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   static const char *force = getenv("LIN_PLAN");
   if (force) return Plan{force[0] - '0', atoi(force + 2)};
-  return Plan{0, 1};
+  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int64_t stages = (K + PBK - 1) / PBK;
+  Plan best{0, 1};
+  double least = 0;
+  for (int sh = 0; sh < 3; ++sh) {
+    const double tiles = (double)((M + kShapeM[sh] - 1) / kShapeM[sh]) * ((N + kShapeN[sh] - 1) / kShapeN[sh]);
+    for (int k : kSplits) {
+      if (k > 1 && (stages < 2 * k || tiles * k > 512)) break;
+      const double wgs = tiles * k, per = (double)((stages + k - 1) / k);
+      double t;
+      if (sh == 2)
+        t = wgs <= 256 ? per * 0.55 : __builtin_ceil(wgs / 512) * per * 1.0;
+      else
+        t = __builtin_ceil(wgs / 256) * per * (sh == 0 ? 1.35 : 0.92);
+      t += 6;
+      if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = Plan{sh, k};
+      }
+    }
+  }
+  return best;
 }
 size_t part_bytes(int64_t M, int64_t N, int64_t K) {
   const Plan p = plan_of(M, N, K);
@@ -700,8 +814,30 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 // workspace `part`: part_bytes(M, N, K)
+// Whether the forward streams: x or W has at most 64 rows, and rows on 16-byte lines.
+bool streams(const GemmArgs &a, size_t es) {
+  return (a.M <= 64 || a.N <= 64) && a.K % (int)(16 / es) == 0 && a.K <= (1 << 22) && on_line(a.A, 16) &&
+         on_line(a.B, 16);
+}
+
+template <typename T, typename To, int TI, int TJ, int NW, int D>
+hipError_t run_stream(const GemmArgs &a, int act, hipStream_t st) {
+  const int grid = ((a.M + 16 * TI - 1) / (16 * TI)) * ((a.N + 16 * TJ - 1) / (16 * TJ));
+  by_act(act, [&](auto A) {
+    stream_gemm<T, To, decltype(A)::value, TI, TJ, NW, D><<<grid, NW * 64, 0, st>>>(a);
+  });
+  return hipGetLastError();
+}
+
 template <bool AK, bool BKM, typename T, typename To>
 hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
+  if constexpr (AK && BKM) {
+    if (streams(a, sizeof(T))) {
+      if (a.M <= 16 || a.N <= 16) return run_stream<T, To, 1, 1, 16, 4>(a, act, st);
+      if (a.M <= a.N) return run_stream<T, To, 4, 2, 8, 2>(a, act, st);
+      return run_stream<T, To, 2, 4, 8, 2>(a, act, st);
+    }
+  }
   a.vec = a.N % 8 == 0 && on_line(a.out, 16) && on_line(a.res, 16) && on_line(a.bias, 16) &&
           on_line(a.z, 16);
   if constexpr (sizeof(T) == 2) {
