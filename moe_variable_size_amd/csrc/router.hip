@@ -1,13 +1,11 @@
 // Routing to experts and the losses that keep a router balanced: from a row of
 // logits to the expert ids and weights a schedule is built from, and back.
 //
-// A wave takes a row of E <= 1024 logits, VPL = ceil(E / 64) of them per lane
-// (expert e = 64 i + lane in slot i), and keeps the row in registers.
-//
-// Choice.  Experts are ranked by a 64-bit key that orders like the choice value
-// (the logit, or score + bias computed in 64 bits) with NaN above everything
-// and an expert that may not be chosen below everything; equal keys go to the
-// lower expert.  k rounds of wave-wide maximum take the k best.
+// All kernels are bound by reading or writing [T, E] once; what keeps them from
+// it is the work per row.  LPR = 16 lanes (E <= 256; 32 up to 512, 64 up to 1024)
+// share a row, V values each in registers, so a wave works on 64 / LPR rows and
+// row-wide sums and maxima are 4 steps inside 16 lanes (data-parallel moves, no
+// LDS) instead of 6 across the wave.
 #include <type_traits>
 
 #include "common.hpp"
@@ -46,6 +44,113 @@ MOE_DEV float wave_max(float v) {  // NaN is passed over
   return v;
 }
 
+// ---- rows shared by LPR lanes ----------------------------------------------------
+// data-parallel moves inside 16 lanes: exchange with the lane 1 and 2 away in the quad,
+// mirrored in 8, mirrored in 16: after all four every lane has seen all 16
+template <int CTRL>
+MOE_DEV uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
+}
+template <int LPR, class Op>
+MOE_DEV uint32_t row_reduce(uint32_t v, Op op) {
+  v = op(v, dpp<0xB1>(v));
+  v = op(v, dpp<0x4E>(v));
+  v = op(v, dpp<0x141>(v));
+  v = op(v, dpp<0x140>(v));
+#pragma unroll
+  for (int d = 16; d < LPR; d <<= 1) v = op(v, (uint32_t)__shfl_xor((int)v, d, kWave));
+  return v;
+}
+MOE_DEV uint32_t f2u(float f) { return __float_as_uint(f); }
+MOE_DEV float u2f(uint32_t u) { return __uint_as_float(u); }
+template <int LPR>
+MOE_DEV float row_sum(float v) {
+  return u2f(row_reduce<LPR>(f2u(v), [](uint32_t a, uint32_t b) { return f2u(u2f(a) + u2f(b)); }));
+}
+template <int LPR>
+MOE_DEV float row_max(float v) {  // NaN is passed over
+  return u2f(row_reduce<LPR>(f2u(v), [](uint32_t a, uint32_t b) { return f2u(fmaxf(u2f(a), u2f(b))); }));
+}
+template <int LPR>
+MOE_DEV uint32_t row_umax(uint32_t v) {
+  return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int LPR>
+MOE_DEV uint32_t row_umin(uint32_t v) {
+  return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
+// Expert of a lane's value i: runs of C = min(V, 4) experts dealt to the row's lanes in turn.
+template <int LPR, int V>
+struct RowMap {
+  static constexpr int C = V < 4 ? V : 4;
+  MOE_DEV static int expert(int sub, int i) { return i / C * (C * LPR) + sub * C + i % C; }
+};
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+MOE_DEV void ld4(const float *p, float (&v)[4]) {
+  const f32x4 a = *(const f32x4 *)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = a[i];
+}
+MOE_DEV void ld4(const bf16_t *p, float (&v)[4]) {
+  const u32x2 a = *(const u32x2 *)p;
+  v[0] = u2f(a[0] << 16);
+  v[1] = u2f(a[0] & 0xffff0000u);
+  v[2] = u2f(a[1] << 16);
+  v[3] = u2f(a[1] & 0xffff0000u);
+}
+MOE_DEV void st4(float *p, const float (&v)[4]) { *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]}; }
+MOE_DEV void st4(bf16_t *p, const float (&v)[4]) {
+  typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+  *(bf16x4_t *)p = bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+// a row's values, -inf past E; vec: E a multiple of 4 and rows on lines of four elements
+template <int LPR, int V, typename T>
+MOE_DEV void load_row(const T *row, int E, int sub, bool vec, float (&l)[V]) {
+  using M = RowMap<LPR, V>;
+  if constexpr (M::C == 4) {
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        const int e = M::expert(sub, 4 * q);
+        float v[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+        if (e < E) ld4(row + e, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[4 * q + i] = v[i];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = M::expert(sub, i);
+    l[i] = e < E ? ldf(row + e) : -__builtin_inff();
+  }
+}
+template <int LPR, int V, typename T>
+MOE_DEV void store_row(T *row, int E, int sub, bool vec, const float (&d)[V]) {
+  using M = RowMap<LPR, V>;
+  if constexpr (M::C == 4) {
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        const int e = M::expert(sub, 4 * q);
+        const float v[4] = {d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        if (e < E) st4(row + e, v);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = M::expert(sub, i);
+    if (e < E) stf(row + e, d[i]);
+  }
+}
+// exp through the hardware's exp2: x log2(e) rounded once, relative error (|x| + 2) 2^-24
+MOE_DEV float fexp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
 struct RouteArgs {
   const void *logits;
   const float *bias;
@@ -55,140 +160,355 @@ struct RouteArgs {
   int E, k, G, keep;
   int sigmoid, top2, renorm;
   float scale;
+  bool vec, vec_bias;  // load_row
+  uint32_t per_magic;  // e * per_magic >> 20 = e / (E / G) for e < 1024 (2^20 > e (E / G - 1))
 };
+
+// LDS written by lanes of a wave, read by others of the same wave: the hardware keeps a wave's LDS
+// accesses in order, the compiler has to as well
+MOE_DEV void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // score of a logit relative to exp(shift): exp(l - shift) (softmax, shift = the
 // row's or the chosen maximum) or sigmoid(l) exp(-shift) (shift = min(maximum,
 // 0), so that a row of very negative logits keeps a nonzero sum)
 MOE_DEV float shifted_score(float l, float shift, bool sigmoid) {
-  if (!sigmoid) return expf(l - shift);
-  return expf(fminf(l, 0.f) - shift) / (1.f + expf(-fabsf(l)));
+  if (!sigmoid) return fexp(l - shift);
+  return fexp(fminf(l, 0.f) - shift) * __builtin_amdgcn_rcpf(1.f + fexp(-fabsf(l)));
 }
 
+// ---- the choice in 64 bits, by a whole wave --------------------------------------
+// Experts are ranked by a 64-bit key that orders like the choice value with NaN above everything
+// and an expert that may not be chosen below everything; equal keys go to the lower expert.  k
+// rounds of wave-wide maximum take the k best; lane j returns slot j (-1: nothing left).
+// lds: VPL * 64 + 64 keys of this wave (used with groups only).
 template <typename T, int VPL>
-__global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
-  extern __shared__ int64_t smem[];  // per wave: E keys, 64 group values
+MOE_DEV int choose_exact(const RouteArgs &p, const T *row, int64_t *lds, int lane) {
+  int64_t *keys = lds, *gval = lds + VPL * 64;
+  float l[VPL];
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 64 + lane;
+    l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
+    m = fmaxf(m, l[i]);
+  }
+  m = wave_max(m);
+  const bool scored = p.bias || (p.G > 1 && p.top2);
+  int64_t key[VPL];
+  double s[VPL];
+  if (scored) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      s[i] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i]))
+                       : (l[i] == -__builtin_inff() ? 0.0 : exp((double)l[i] - (double)m));
+      sum += s[i];
+    }
+    if (!p.sigmoid) {
+      sum = wave_sum(sum);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] /= sum;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 64 + lane;
+    const float b = p.bias && e < p.E ? p.bias[e] : 0.f;
+    const bool barred = l[i] == -__builtin_inff() || b == -__builtin_inff();
+    key[i] = barred ? kBarred : order_key(p.bias ? s[i] + (double)b : (double)l[i]);
+  }
+  if (p.G > 1) {
+    const int per = p.E / p.G;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      keys[i * 64 + lane] = key[i] == kBarred ? kBarred : p.bias || !p.top2 ? key[i] : order_key(s[i]);
+    wave_lds_sync();
+    int64_t gk = kBarred;
+    if (lane < p.G) {
+      int64_t a = kBarred, b = kBarred;  // the two best
+      for (int j = 0; j < per; ++j) {
+        const int64_t v = keys[lane * per + j];
+        if (v > a) { b = a; a = v; } else if (v > b) b = v;
+      }
+      gk = !p.top2 || b == kBarred ? a : order_key(key_value(a) + key_value(b));
+      gval[lane] = gk;
+    }
+    wave_lds_sync();
+    bool kept = false;
+    if (lane < p.G && gk != kBarred) {
+      int rank = 0;
+      for (int g = 0; g < p.G; ++g) rank += gval[g] > gk || (gval[g] == gk && g < lane);
+      kept = rank < p.keep;
+    }
+    const uint64_t mask = __ballot(kept);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int g = (i * 64 + lane) / per;
+      if (g >= p.G || !((mask >> g) & 1)) key[i] = kBarred;
+    }
+    wave_lds_sync();
+  }
+  int id = -1;
+  for (int j = 0; j < p.k; ++j) {
+    int64_t best = kBarred;
+    int at = INT32_MAX;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (key[i] > best) { best = key[i]; at = i * 64 + lane; }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      const int64_t ok = __shfl_xor(best, d, kWave);
+      const int oa = __shfl_xor(at, d, kWave);
+      if (ok > best || (ok == best && oa < at)) { best = ok; at = oa; }
+    }
+    if (best == kBarred) break;
+    if (lane == j) id = at;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (at == i * 64 + lane) key[i] = kBarred;
+  }
+  return id;
+}
+
+// weight of a lane's chosen expert (id, or -1) with logit lj, chosen experts in the first lanes of
+// the LPR that share the row; m, sum: the row's maximum and sum of exp(l - m) (plain softmax);
+// bad: a NaN if the row holds one (softmax), else 0
+template <int LPR>
+MOE_DEV float chosen_weight(const RouteArgs &p, int id, float lj, float m, float sum, float bad) {
+  const bool on = id >= 0;
+  float w;
+  if (p.renorm) {
+    const float mc = row_max<LPR>(on ? lj : -__builtin_inff());
+    const float sj = on ? shifted_score(lj, p.sigmoid ? fminf(mc, 0.f) : mc, p.sigmoid) : 0.f;
+    w = sj / (row_sum<LPR>(sj) + bad) * p.scale;
+  } else if (p.sigmoid) {
+    w = shifted_score(lj, 0.f, true) * p.scale;
+  } else {
+    w = fexp(lj - m) / sum * p.scale;
+  }
+  return on ? w : 0.f;
+}
+
+// ---- a wave per row: what the kernel below does not take ---------------------------
+template <typename T, int VPL>
+__global__ __launch_bounds__(NT) void route_wave_kernel(RouteArgs p) {
+  extern __shared__ int64_t smem[];  // with groups, per wave: VPL * 64 keys, 64 group values
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  int64_t *keys = smem + (size_t)wid * (VPL * 64 + 64), *gval = keys + VPL * 64;
+  int64_t *lds = smem + (size_t)wid * (VPL * 64 + 64);
   for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < p.T; t += (int64_t)gridDim.x * NW) {
     const T *row = (const T *)p.logits + t * p.E;
-    float l[VPL];
-    float m = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
-      m = fmaxf(m, l[i]);
-    }
-    m = wave_max(m);
-    // choice values
-    const bool scored = p.bias || (p.G > 1 && p.top2);
-    int64_t key[VPL];
-    double s[VPL];
-    if (scored) {
-      double sum = 0.0;
+    const int id = choose_exact<T, VPL>(p, row, lds, lane);
+    float m = -__builtin_inff(), sum = 0.f, bad = 0.f;
+    if (!p.sigmoid) {
+      float l[VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        s[i] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i]))
-                         : (l[i] == -__builtin_inff() ? 0.0 : exp((double)l[i] - (double)m));
-        sum += s[i];
+        const int e = i * 64 + lane;
+        l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
+        m = fmaxf(m, l[i]);
+        bad += l[i] != l[i] ? l[i] : 0.f;
       }
-      if (!p.sigmoid) {
-        sum = wave_sum(sum);
+      m = wave_max(m);
+      bad = wave_sum(bad);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] /= sum;
-      }
+      for (int i = 0; i < VPL; ++i) sum += l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
+      sum = wave_sum(sum);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      const float b = p.bias && e < p.E ? p.bias[e] : 0.f;
-      const bool barred = l[i] == -__builtin_inff() || b == -__builtin_inff();
-      key[i] = barred ? kBarred : order_key(p.bias ? s[i] + (double)b : (double)l[i]);
-    }
-    if (p.G > 1) {
-      const int per = p.E / p.G;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        keys[i * 64 + lane] = key[i] == kBarred ? kBarred : p.bias || !p.top2 ? key[i] : order_key(s[i]);
-      __builtin_amdgcn_wave_barrier();
-      __threadfence_block();
-      int64_t gk = kBarred;
-      if (lane < p.G) {
-        int64_t a = kBarred, b = kBarred;  // the two best
-        for (int j = 0; j < per; ++j) {
-          const int64_t v = keys[lane * per + j];
-          if (v > a) { b = a; a = v; } else if (v > b) b = v;
-        }
-        gk = !p.top2 || b == kBarred ? a : order_key(key_value(a) + key_value(b));
-        gval[lane] = gk;
-      }
-      __builtin_amdgcn_wave_barrier();
-      __threadfence_block();
-      bool kept = false;
-      if (lane < p.G && gk != kBarred) {
-        int rank = 0;
-        for (int g = 0; g < p.G; ++g) rank += gval[g] > gk || (gval[g] == gk && g < lane);
-        kept = rank < p.keep;
-      }
-      const uint64_t mask = __ballot(kept);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int g = (i * 64 + lane) / per;
-        if (g >= p.G || !((mask >> g) & 1)) key[i] = kBarred;
-      }
-      __builtin_amdgcn_wave_barrier();
-      __threadfence_block();
-    }
-    // k rounds
-    int id = -1;      // lane j: slot j
-    float lj = -__builtin_inff();
-    for (int j = 0; j < p.k; ++j) {
-      int64_t best = kBarred;
-      int at = INT32_MAX;
-      float la = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) { best = key[i]; at = i * 64 + lane; la = l[i]; }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) {
-        const int64_t ok = __shfl_xor(best, d, kWave);
-        const int oa = __shfl_xor(at, d, kWave);
-        const float ol = __shfl_xor(la, d, kWave);
-        if (ok > best || (ok == best && oa < at)) { best = ok; at = oa; la = ol; }
-      }
-      if (best == kBarred) break;
-      if (lane == j) { id = at; lj = la; }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (at == i * 64 + lane) key[i] = kBarred;
-    }
-    // weights
-    const bool on = id >= 0;
-    float wgt;
-    if (p.renorm) {
-      const float mc = wave_max(on ? lj : -__builtin_inff());
-      const float sj = on ? shifted_score(lj, p.sigmoid ? fminf(mc, 0.f) : mc, p.sigmoid) : 0.f;
-      float all = wave_sum(sj);
-      if (!p.sigmoid) {  // a NaN anywhere in the row is in its softmax
-        float bad = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) bad += l[i] != l[i] ? l[i] : 0.f;
-        all += wave_sum(bad);
-      }
-      wgt = sj / all * p.scale;
-    } else if (p.sigmoid) {
-      wgt = shifted_score(lj, 0.f, true) * p.scale;
-    } else {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += l[i] == -__builtin_inff() ? 0.f : expf(l[i] - m);
-      wgt = expf(lj - m) / wave_sum(sum) * p.scale;
-    }
+    const float w = chosen_weight<64>(p, id, id >= 0 ? ldf(row + id) : 0.f, m, sum, bad);
     if (lane < p.k) {
       p.ids[t * p.k + lane] = id;
-      p.w[t * p.k + lane] = on ? wgt : 0.f;
+      p.w[t * p.k + lane] = w;
     }
+  }
+}
+
+// ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= LPR ------------------
+// 32-bit keys that order like the choice value in fp32 (0: may not be chosen), in registers and in
+// LDS by expert.  Every lane keeps the best of its V experts.  A round reduces the row's best and
+// its expert over the lanes, strikes it out in LDS, and the lanes look at the struck owner's V
+// values, one each, for the owner's new best: about 36 instructions a round for all rows of the
+// wave, where striking out and searching again in registers takes 80.
+//
+// Without a bias the keys are the logits' own order: exact.  With one (and for groups by sums of
+// scores) the values are fp32 approximations.  A score is off by less than 2 eps of the row's largest,
+// eps = (x + 24) 2^-24: x, the span of the exponentials' arguments, is rounded twice, and the
+// exponential, a sum 20 additions deep and the reciprocal add less than 48 roundings; adding the bias
+// rounds the value once more.  Where two values next to each other in the order, or the groups on
+// both sides of the cut, are closer than their errors together, the wave chooses that row again in
+// 64 bits (about one row in 300 of normally distributed logits).
+MOE_DEV uint32_t key32(float c) {
+  const uint32_t u = f2u(c + 0.f);  // -0 -> +0
+  return c != c ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+MOE_DEV float key32_value(uint32_t k) {
+  return k == 0xFFFFFFFFu ? __builtin_nanf("") : u2f((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+template <typename T, int LPR, int V, bool SCORED>
+__global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
+  using M = RowMap<LPR, V>;
+  constexpr int RPW = 64 / LPR, EP = LPR * V;   // rows per wave, experts (padded)
+  constexpr int PITCH = EP + 16;                // keys per row: the rows of a wave on other banks
+  constexpr int XV = (EP + 63) / 64;            // values per lane of a whole wave
+  constexpr int WORDS = RPW * PITCH > 2 * (XV * 64 + 64) ? RPW * PITCH : 2 * (XV * 64 + 64);
+  __shared__ __align__(16) uint32_t smem[NW * WORDS];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int sub = lane & (LPR - 1), rw = lane / LPR;
+  uint32_t *const keys = smem + wid * WORDS + rw * PITCH;
+  const int64_t t = ((int64_t)blockIdx.x * NW + wid) * RPW + rw;
+  const bool live = t < p.T;
+  const T *row = (const T *)p.logits + (live ? t : 0) * p.E;
+  float l[V];
+  load_row<LPR, V>(row, p.E, sub, p.vec, l);
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+  m = row_max<LPR>(m);
+  // sum of the softmax, where anything needs it
+  float sum = 0.f;
+  if (!p.sigmoid && (SCORED || !p.renorm)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
+    sum = row_sum<LPR>(sum);
+  }
+  uint32_t key[V], gkey[SCORED ? V : 1];  // gkey: what the groups are ranked by, if not the key
+  float err = 0.f;  // bound of a value's error, times 2 (two values' together)
+  if constexpr (SCORED) {
+    const float inv = __builtin_amdgcn_rcpf(sum);
+    float span = 0.f, top = 0.f, mag = 0.f, bs[V];
+    if (p.bias) {
+      load_row<LPR, V>(p.bias, p.E, sub, p.vec_bias, bs);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) bs[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool out = l[i] == -__builtin_inff(), barred = out || bs[i] == -__builtin_inff();
+      const float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + fexp(-l[i])) : out ? 0.f : fexp(l[i] - m) * inv;
+      const float c = s + bs[i];
+      key[i] = barred ? 0u : key32(p.bias ? c : l[i]);
+      gkey[i] = barred ? 0u : p.bias ? key[i] : key32(s);
+      top = fmaxf(top, s);
+      mag = fmaxf(mag, barred ? 0.f : fabsf(c));
+      span = fmaxf(span, out ? 0.f : p.sigmoid ? -l[i] : m - l[i]);
+    }
+    const float eps = (fminf(row_max<LPR>(span), 104.f) + 24.f) * 0x1p-24f;
+    err = 4.f * (eps * row_max<LPR>(top) + 0x1p-24f * row_max<LPR>(mag));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i] == -__builtin_inff() ? 0u : key32(l[i]);
+  }
+  // whether two values (of `terms` scores each) may stand in the other order in 64 bits; a NaN may
+  auto close = [&](uint32_t hi, uint32_t lo, float terms) __attribute__((always_inline)) {
+    return !(key32_value(hi) - key32_value(lo) > terms * err);
+  };
+  bool doubt = false;
+  if (p.G > 1) {
+    const int per = p.E / p.G;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (SCORED) keys[M::expert(sub, i)] = gkey[i];
+      else keys[M::expert(sub, i)] = key[i];
+    }
+    wave_lds_sync();
+    // lanes g, g + G', ... of the row scan group g (G' = the power of two above G - 1)
+    int gp = 1;
+    while (gp < p.G) gp <<= 1;
+    const int g = sub & (gp - 1), part = sub / gp, parts = LPR / gp;
+    uint32_t a = 0, b = 0;  // the two best
+    if (g < p.G)
+#pragma unroll 8
+      for (int j = part; j < per; j += parts) {
+        const uint32_t v = keys[g * per + j];
+        b = max(b, min(a, v));
+        a = max(a, v);
+      }
+    for (int d = gp; d < LPR; d <<= 1) {
+      const uint32_t oa = __shfl_xor(a, d, kWave), ob = __shfl_xor(b, d, kWave);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    const uint32_t gv = !p.top2 || b == 0u ? a : key32(key32_value(a) + key32_value(b));
+    // rank of the lane's group; the kept one of lowest value and the best of the others
+    int rank = 0;
+    for (int d = 0; d < p.G; ++d) {
+      const uint32_t o = __shfl(gv, (lane & ~(LPR - 1)) + d, kWave);
+      rank += o > gv || (o == gv && d < g);
+    }
+    const bool kept = g < p.G && gv != 0u && rank < p.keep;
+    if (SCORED && p.keep < p.G) {
+      const uint32_t lo = row_umin<LPR>(kept ? gv : 0xFFFFFFFFu);
+      const uint32_t hi = row_umax<LPR>(kept || g >= p.G ? 0u : gv);
+      doubt = hi != 0u && close(lo, hi, 2.f);  // (sums of two carry both errors)
+    }
+    const uint64_t mask = __ballot(kept && sub < gp) >> (lane & ~(LPR - 1));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = M::expert(sub, i);
+      if (e >= p.E || !((mask >> (__umul24(e, p.per_magic) >> 20)) & 1)) key[i] = 0u;
+    }
+    wave_lds_sync();
+  }
+  uint32_t best = 0, at = 0xFFFFFFFFu;  // the lane's best key, and its expert
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = M::expert(sub, i);
+    keys[e] = key[i];
+    if (key[i] > best) { best = key[i]; at = e; }
+  }
+  wave_lds_sync();
+  int id = -1;
+  uint32_t last = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t mx = row_umax<LPR>(best);
+    const uint32_t e = row_umin<LPR>(best == mx ? at : 0xFFFFFFFFu);
+    if (sub == j && mx != 0u) id = (int)e;
+    if constexpr (SCORED) {
+      if (p.bias) doubt |= j > 0 && mx != 0u && close(last, mx, 1.f);
+      last = mx;
+    }
+    const bool hit = mx != 0u;
+    const int owner = hit ? (int)(e / M::C) & (LPR - 1) : 0;
+    if (hit && sub == 0) keys[e] = 0u;
+    wave_lds_sync();
+    const int oe = M::expert(owner, sub & (V - 1));
+    const uint32_t v = keys[oe];
+    const uint32_t nb = row_umax<LPR>(v);
+    const uint32_t ne = row_umin<LPR>(v == nb ? (uint32_t)oe : 0xFFFFFFFFu);
+    if (hit && sub == owner) { best = nb; at = ne; }
+  }
+  if constexpr (SCORED) {
+    if (p.bias) {
+      const uint32_t mx = row_umax<LPR>(best);
+      doubt |= mx != 0u && last != 0u && close(last, mx, 1.f);
+    }
+  }
+  if constexpr (SCORED) {
+    // every lane of a row has the same doubt
+    uint64_t again = __ballot(doubt && live && sub == 0);
+    while (again) {
+      const int r = (__ffsll((unsigned long long)again) - 1) / LPR;
+      again &= again - 1;
+      const int64_t tr = ((int64_t)blockIdx.x * NW + wid) * RPW + r;
+      const int x = choose_exact<T, XV>(p, (const T *)p.logits + tr * p.E, (int64_t *)(smem + wid * WORDS), lane);
+      const int mine = __shfl(x, sub, kWave);
+      if (rw == r) id = mine;
+    }
+  }
+  float bad = 0.f;
+  if (p.renorm && !p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad += l[i] != l[i] ? l[i] : 0.f;
+    bad = row_sum<LPR>(bad);
+  }
+  const float w = chosen_weight<LPR>(p, id, id >= 0 ? ldf(row + id) : 0.f, m, sum, bad);
+  if (live && sub < p.k) {
+    p.ids[t * p.k + sub] = id;
+    p.w[t * p.k + sub] = w;
   }
 }
 
@@ -201,68 +521,76 @@ struct RouteBwdArgs {
   int64_t T;
   int E, k, sigmoid, renorm;
   float scale;
+  bool vec;
 };
 
 // g_j = dL/dw_j.  With D = sum_j g_j w_j:
 //   renormalised: dl_j = w_j (g_j - D / scale), times 1 - s_j for the sigmoid;
 //   plain softmax: dl_i = w_i g_i [i chosen] - p_i D;  plain sigmoid: dl_j = g_j w_j (1 - s_j).
-template <typename T, int VPL>
+template <typename T, int LPR, int V>
 __global__ __launch_bounds__(NT) void route_bwd_kernel(RouteBwdArgs p) {
-  __shared__ float rows[NW][VPL * 64];
+  using M = RowMap<LPR, V>;
+  constexpr int RPW = 64 / LPR, EP = LPR * V, NS = 64 / LPR;  // NS: slots per lane (k <= 64)
+  __shared__ __align__(16) float rows[NW * RPW * EP];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  float *buf = rows[wid];
-  for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < p.T; t += (int64_t)gridDim.x * NW) {
-    const T *row = (const T *)p.logits + t * p.E;
-    const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
-    const bool on = id >= 0 && id < p.E;
-    const float w = on ? p.w[t * p.k + lane] : 0.f, g = on ? p.g[t * p.k + lane] : 0.f;
-    const float D = wave_sum(g * w);
-    float c = w * (p.renorm ? g - D / p.scale : g);
-    if (p.sigmoid && on) {  // 1 - s = sigmoid(-l)
-      const float l = ldf(row + id);
-      c *= shifted_score(-l, 0.f, true);
-    }
-    const bool dense = !p.renorm && !p.sigmoid;
-    float l[VPL], m = -__builtin_inff(), sum = 0.f;
+  const int sub = lane & (LPR - 1), rw = lane / LPR;
+  float *buf = rows + (wid * RPW + rw) * EP;
+  const int64_t t = ((int64_t)blockIdx.x * NW + wid) * RPW + rw;
+  const bool live = t < p.T;
+  const T *row = (const T *)p.logits + (live ? t : 0) * p.E;
+  const bool dense = !p.renorm && !p.sigmoid;
+  float l[V], m = -__builtin_inff();
+  if (dense) load_row<LPR, V>(row, p.E, sub, p.vec, l);
+  int id[NS];
+  float w[NS], g[NS], D = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      buf[e] = 0.f;
-      l[i] = dense && e < p.E ? ldf(row + e) : -__builtin_inff();
-      m = fmaxf(m, l[i]);
-    }
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    if (on) atomicAdd(&buf[id], c);  // ids of one row differ; repeated ones add up
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    if (dense) {
-      m = wave_max(m);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        l[i] = l[i] == -__builtin_inff() ? 0.f : expf(l[i] - m);
-        sum += l[i];
-      }
-      sum = wave_sum(sum);
-      const float f = sum > 0.f || sum != sum ? D / sum : 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) l[i] *= f;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      if (e < p.E) stf((T *)p.d + t * p.E + e, buf[e] - (dense ? l[i] : 0.f));
-    }
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
+  for (int q = 0; q < NS; ++q) {
+    const int j = q * LPR + sub;
+    id[q] = live && j < p.k ? p.ids[t * p.k + j] : -1;
+    if (id[q] >= p.E) id[q] = -1;
+    w[q] = id[q] >= 0 ? p.w[t * p.k + j] : 0.f;
+    g[q] = id[q] >= 0 ? p.g[t * p.k + j] : 0.f;
+    D += g[q] * w[q];
   }
+  D = row_sum<LPR>(D);
+#pragma unroll
+  for (int i = 0; i < V; ++i) buf[M::expert(sub, i)] = 0.f;
+  wave_lds_sync();
+#pragma unroll
+  for (int q = 0; q < NS; ++q) {
+    if (id[q] < 0) continue;
+    float c = w[q] * (p.renorm ? g[q] - D / p.scale : g[q]);
+    if (p.sigmoid) c *= shifted_score(-ldf(row + id[q]), 0.f, true);  // 1 - s = sigmoid(-l)
+    atomicAdd(&buf[id[q]], c);  // ids of one row differ; repeated ones add up
+  }
+  wave_lds_sync();
+  float d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[i] = buf[M::expert(sub, i)];
+  if (dense) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    m = row_max<LPR>(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      l[i] = l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
+      sum += l[i];
+    }
+    sum = row_sum<LPR>(sum);
+    const float f = sum > 0.f || sum != sum ? D / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] -= l[i] * f;
+  }
+  if (live) store_row<LPR, V>((T *)p.d + t * p.E, p.E, sub, p.vec, d);
 }
 
 // ---- losses --------------------------------------------------------------------
 // Forward: every block sums its rows' probabilities and counts its ids per
 // expert, and its rows' squared log-sum-exps; one block joins the partial sums in
 // a fixed order.  Workspace: [blocks][2 E + 2] words: sums, counts, z, rows.
-constexpr int kLossBlocks = 256;
+constexpr int kLossBlocks = 128;   // partial sums that one workgroup then reads (E = 128: 132 KB)
+constexpr int LT = 1024, LW = LT / kWave;
 
 struct LossArgs {
   const void *logits;
@@ -273,196 +601,225 @@ struct LossArgs {
   void *d;
   int64_t T;
   int E, k, sigmoid, blocks;
+  bool vec;
 };
 
-// probabilities of a row (softmax, or the sigmoids over their sum); lse; empty
-// rows (every logit -inf) give zeros.  soft[]: the softmax, q[]: the probabilities
-template <int VPL>
-MOE_DEV bool row_probs(const float (&l)[VPL], bool sigmoid, float (&soft)[VPL], float (&q)[VPL],
-                       float &lse) {
+// soft[]: the softmax of a row; q[]: its probabilities (the softmax, or the sigmoids over their
+// sum); lse.  An empty row (every logit -inf) gives zeros and false.
+template <int LPR, int V>
+MOE_DEV bool row_probs(const float (&l)[V], bool sigmoid, float (&soft)[V], float (&q)[V], float &lse) {
   float m = -__builtin_inff();
-  bool any = false;
+  float any = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
+  for (int i = 0; i < V; ++i) {
     m = fmaxf(m, l[i]);
-    any |= l[i] != -__builtin_inff();
+    any = l[i] != -__builtin_inff() ? 1.f : any;  // a NaN counts
   }
-  any = __any(any);
-  m = wave_max(m);
+  const bool some = row_max<LPR>(any) != 0.f;
+  m = row_max<LPR>(m);
   float sum = 0.f, qsum = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
+  for (int i = 0; i < V; ++i) {
     const bool off = l[i] == -__builtin_inff();
-    soft[i] = off ? 0.f : expf(l[i] - m);
+    soft[i] = off ? 0.f : fexp(l[i] - m);
     sum += soft[i];
     if (sigmoid) {
       q[i] = off ? 0.f : shifted_score(l[i], fminf(m, 0.f), true);
       qsum += q[i];
     }
   }
-  sum = wave_sum(sum);
-  lse = any ? m + logf(sum) : 0.f;
-  const float inv = any ? 1.f / sum : 0.f;
+  sum = row_sum<LPR>(sum);
+  lse = some ? m + logf(sum) : 0.f;
+  const float inv = some ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) soft[i] *= inv;
+  for (int i = 0; i < V; ++i) soft[i] *= inv;
   if (sigmoid) {
-    qsum = wave_sum(qsum);
-    const float qinv = any ? 1.f / qsum : 0.f;
+    qsum = row_sum<LPR>(qsum);
+    const float qinv = some ? 1.f / qsum : 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) q[i] *= qinv;
+    for (int i = 0; i < V; ++i) q[i] *= qinv;
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) q[i] = soft[i];
+    for (int i = 0; i < V; ++i) q[i] = soft[i];
   }
-  return any;
+  return some;
 }
 
-template <typename T, int VPL>
-__global__ __launch_bounds__(NT) void loss_fwd_kernel(LossArgs p) {
-  __shared__ float psum[NW][VPL * 64];
-  __shared__ int cnt[VPL * 64];
-  __shared__ float zs[NW];
-  __shared__ int rs[NW];
+// Every lane sums its own V experts over the block's rows; the row groups of a wave and the waves
+// join through LDS.
+template <typename T, int LPR, int V>
+__global__ __launch_bounds__(LT) void loss_fwd_kernel(LossArgs p) {
+  using M = RowMap<LPR, V>;
+  constexpr int RPW = 64 / LPR, EP = LPR * V;
+  __shared__ float psum[LW][EP];  // <= 64 KB (EP <= 1024)
+  __shared__ int cnt[EP];
+  __shared__ float zs[LW];
+  __shared__ int rs[LW];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < VPL * 64; e += NT) cnt[e] = 0;
+  const int sub = lane & (LPR - 1), rw = lane / LPR;
+  for (int e = threadIdx.x; e < EP; e += LT) cnt[e] = 0;
   __syncthreads();
-  float acc[VPL] = {}, z = 0.f;
+  float acc[V] = {}, z = 0.f;
   int rows = 0;
-  for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < p.T; t += (int64_t)gridDim.x * NW) {
-    const T *row = (const T *)p.logits + t * p.E;
-    float l[VPL], soft[VPL], q[VPL], lse;
+  const int64_t step = (int64_t)gridDim.x * LW * RPW;
+  // a block takes runs of LW * RPW consecutive rows
+  for (int64_t t0 = (int64_t)blockIdx.x * LW * RPW; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + wid * RPW + rw;
+    if (t < p.T) {  // (whole rows: the lanes that share one go together)
+      float l[V], soft[V], q[V], lse;
+      load_row<LPR, V>((const T *)p.logits + t * p.E, p.E, sub, p.vec, l);
+      rows += row_probs<LPR, V>(l, p.sigmoid, soft, q, lse);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
+      for (int i = 0; i < V; ++i) acc[i] += q[i];
+      z += lse * lse;
     }
-    rows += row_probs<VPL>(l, p.sigmoid, soft, q, lse);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += q[i];
-    z += lse * lse;
-    if (lane < p.k) {
-      const int id = p.ids[t * p.k + lane];
+    const int64_t i0 = t0 * p.k, i1 = min(p.T, t0 + LW * RPW) * p.k;
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += LT) {
+      const int id = p.ids[i];
       if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
     }
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) psum[wid][i * 64 + lane] = acc[i];
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int d = LPR; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d, kWave);
+    if (rw == 0) psum[wid][M::expert(sub, i)] = acc[i];
+  }
+#pragma unroll
+  for (int d = LPR; d < 64; d <<= 1) {
+    z += __shfl_xor(z, d, kWave);
+    rows += __shfl_xor(rows, d, kWave);
+  }
   if (lane == 0) { zs[wid] = z; rs[wid] = rows; }
   __syncthreads();
   float *part = p.part + (size_t)blockIdx.x * (2 * p.E + 2);
-  for (int e = threadIdx.x; e < p.E; e += NT) {
+  for (int e = threadIdx.x; e < p.E; e += LT) {
     float v = 0.f;
-    for (int w = 0; w < NW; ++w) v += psum[w][e];
+#pragma unroll
+    for (int w = 0; w < LW; ++w) v += psum[w][e];
     part[e] = v;
     part[p.E + e] = __int_as_float(cnt[e]);
   }
   if (threadIdx.x == 0) {
     float v = 0.f;
     int r = 0;
-    for (int w = 0; w < NW; ++w) { v += zs[w]; r += rs[w]; }
+    for (int w = 0; w < LW; ++w) { v += zs[w]; r += rs[w]; }
     part[2 * p.E] = v;
     part[2 * p.E + 1] = __int_as_float(r);
   }
 }
 
-__global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs p) {
-  __shared__ double red[1024];
-  __shared__ long long ired[1024];
-  const int tid = threadIdx.x;
-  const int pitch = 2 * p.E + 2;
-  double P = 0.0;
-  long long c = 0;
-  if (tid < p.E)
-    for (int b = 0; b < p.blocks; ++b) {
-      P += p.part[(size_t)b * pitch + tid];
-      c += __float_as_int(p.part[(size_t)b * pitch + p.E + tid]);
-    }
-  double z = 0.0;
+// Sum over the block of a value per thread, in a fixed order.
+template <typename S>
+MOE_DEV S block_sum(S v, S *red) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, kWave);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  S s = red[0];
+#pragma unroll
+  for (int w = 1; w < LW; ++w) s += red[w];
+  __syncthreads();
+  return s;
+}
+
+// One workgroup joins the blocks' parts: W = the power of two from E up (at least 64) threads side by
+// side per expert, the LT / W others of a column take every (LT / W)-th part.
+__global__ __launch_bounds__(LT) void loss_join_kernel(LossArgs p) {
+  __shared__ double psum[LT];
+  __shared__ int csum[LT];
+  __shared__ double dred[LW];
+  __shared__ long long ired[LW];
+  const int tid = threadIdx.x, pitch = 2 * p.E + 2;
+  int W = 64;
+  while (W < p.E) W <<= 1;
+  const int e = tid & (W - 1), q = tid / W, Q = LT / W;
+  double P = 0.0, z = 0.0;
+  int c = 0;
   long long r = 0;
-  for (int b = tid; b < p.blocks; b += 1024) {
-    z += p.part[(size_t)b * pitch + 2 * p.E];
-    r += __float_as_int(p.part[(size_t)b * pitch + 2 * p.E + 1]);
+  if (e < p.E) {
+#pragma unroll 8
+    for (int b = q; b < p.blocks; b += Q) {
+      P += p.part[(size_t)b * pitch + e];
+      c += __float_as_int(p.part[(size_t)b * pitch + p.E + e]);
+    }
   }
-  auto isum = [&](long long v) {
-    ired[tid] = v;
-    __syncthreads();
-    for (int d = 512; d; d >>= 1) {
-      if (tid < d) ired[tid] += ired[tid + d];
-      __syncthreads();
+  if (tid < p.blocks) {
+    z = p.part[(size_t)tid * pitch + 2 * p.E];
+    r = __float_as_int(p.part[(size_t)tid * pitch + 2 * p.E + 1]);
+  }
+  psum[tid] = P;
+  csum[tid] = c;
+  __syncthreads();
+  if (q == 0)
+    for (int i = 1; i < Q; ++i) {
+      P += psum[i * W + e];
+      c += csum[i * W + e];
     }
-    const long long s = ired[0];
-    __syncthreads();
-    return s;
-  };
-  auto dsum = [&](double v) {
-    red[tid] = v;
-    __syncthreads();
-    for (int d = 512; d; d >>= 1) {
-      if (tid < d) red[tid] += red[tid + d];
-      __syncthreads();
-    }
-    const double s = red[0];
-    __syncthreads();
-    return s;
-  };
-  const long long C = isum(c), V = isum(r);
-  const double inv = V > 0 ? 1.0 / (double)V : 0.0;
+  const bool mine = q == 0 && e < p.E;
+  const long long C = block_sum<long long>(mine ? c : 0, ired), N = block_sum<long long>(r, ired);
+  const double inv = N > 0 ? 1.0 / (double)N : 0.0;
   const float f = C > 0 ? (float)((double)p.E * (double)c / (double)C) : 0.f;
-  if (tid < p.E) p.stats[tid] = f;
-  const double bal = dsum(tid < p.E ? (double)f * P : 0.0), zz = dsum(z);
+  if (mine) p.stats[e] = f;
+  const double bal = block_sum<double>(mine ? (double)f * P : 0.0, dred), zz = block_sum<double>(z, dred);
   if (tid == 0) {
     p.stats[p.E] = (float)inv;
     p.losses[0] = (float)(bal * inv);
     p.losses[1] = (float)(zz * inv);
   }
 }
+static_assert(kLossBlocks <= LT, "a thread per part");
 
-template <typename T, int VPL>
+template <typename T, int LPR, int V>
 __global__ __launch_bounds__(NT) void loss_bwd_kernel(LossArgs p) {
+  using M = RowMap<LPR, V>;
+  constexpr int RPW = 64 / LPR;
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int sub = lane & (LPR - 1), rw = lane / LPR;
   const float inv = p.stats[p.E];
   const float gb = p.dloss[0] * inv, gz = 2.f * p.dloss[1] * inv;
-  float f[VPL];
+  float f[V];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) f[i] = i * 64 + lane < p.E ? p.stats[i * 64 + lane] : 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < p.T; t += (int64_t)gridDim.x * NW) {
-    const T *row = (const T *)p.logits + t * p.E;
-    float l[VPL], soft[VPL], q[VPL], lse;
+  for (int i = 0; i < V; ++i) f[i] = M::expert(sub, i) < p.E ? p.stats[M::expert(sub, i)] : 0.f;
+  for (int64_t t = ((int64_t)blockIdx.x * NW + wid) * RPW + rw; t < p.T; t += (int64_t)gridDim.x * NW * RPW) {
+    float l[V], soft[V], q[V], lse, dot = 0.f;
+    load_row<LPR, V>((const T *)p.logits + t * p.E, p.E, sub, p.vec, l);
+    row_probs<LPR, V>(l, p.sigmoid, soft, q, lse);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
-    }
-    row_probs<VPL>(l, p.sigmoid, soft, q, lse);
-    float dot = 0.f;
+    for (int i = 0; i < V; ++i) dot += f[i] * q[i];
+    dot = row_sum<LPR>(dot);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dot += f[i] * q[i];
-    dot = wave_sum(dot);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
+    for (int i = 0; i < V; ++i) {
       float d = gb * q[i] * (f[i] - dot);
       if (p.sigmoid && l[i] != -__builtin_inff()) d *= shifted_score(-l[i], 0.f, true);
-      d += gz * lse * soft[i];
-      if (e < p.E) stf((T *)p.d + t * p.E + e, d);
+      l[i] = d + gz * lse * soft[i];
     }
+    store_row<LPR, V>((T *)p.d + t * p.E, p.E, sub, p.vec, l);
   }
 }
 
-// f(integral_constant<VPL>) for E experts
+// f(integral_constant<LPR>, integral_constant<V>) for E experts
 template <class F>
 hipError_t by_width(int E, F &&f) {
-  if (E <= 64) f(std::integral_constant<int, 1>());
-  else if (E <= 128) f(std::integral_constant<int, 2>());
-  else if (E <= 256) f(std::integral_constant<int, 4>());
-  else if (E <= 512) f(std::integral_constant<int, 8>());
-  else f(std::integral_constant<int, 16>());
+  using std::integral_constant;
+  const auto l16 = integral_constant<int, 16>();
+  if (E <= 16) f(l16, integral_constant<int, 1>());
+  else if (E <= 32) f(l16, integral_constant<int, 2>());
+  else if (E <= 64) f(l16, integral_constant<int, 4>());
+  else if (E <= 128) f(l16, integral_constant<int, 8>());
+  else if (E <= 256) f(l16, integral_constant<int, 16>());
+  else if (E <= 512) f(integral_constant<int, 32>(), integral_constant<int, 16>());
+  else f(integral_constant<int, 64>(), integral_constant<int, 16>());
   return hipGetLastError();
 }
 
-int row_grid(int64_t T) {
-  const int64_t g = (T + NW - 1) / NW;
-  return (int)(g < 1 ? 1 : g > 65536 ? 65536 : g);
+// blocks of `rows` rows each
+int row_grid(int64_t T, int rows) { return (int)((T + rows - 1) / rows); }
+
+// rows of E elements on lines of four
+bool rows_on_lines(const void *p, int E, int dtype) {
+  const size_t es = dtype == MOE_F32 ? 4 : 2;
+  return E % 4 == 0 && (uintptr_t)p % (4 * es) == 0;
 }
 
 }  // namespace
@@ -470,68 +827,89 @@ int row_grid(int64_t T) {
 hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, int E, int k,
                             bool sigmoid, int G, int keep, bool top2, bool renorm, float scale,
                             int32_t *ids, float *w, int dtype, hipStream_t st) {
-  RouteArgs a{logits, bias, ids, w, T, E, k, G, keep, sigmoid, top2, renorm, scale};
-  return by_width(E, [&](auto V) {
-    constexpr int VPL = decltype(V)::value;
-    const size_t sm = G > 1 ? (size_t)NW * (VPL * 64 + 64) * sizeof(int64_t) : 0;
-    if (dtype == MOE_F32)
-      route_kernel<float, VPL><<<row_grid(T), NT, sm, st>>>(a);
-    else
-      route_kernel<bf16_t, VPL><<<row_grid(T), NT, sm, st>>>(a);
+  const RouteArgs a{logits, bias, ids, w, T, E, k, G, keep, sigmoid, top2, renorm, scale,
+                    rows_on_lines(logits, E, dtype), bias && rows_on_lines(bias, E, MOE_F32),
+                    ((1u << 20) + E / G - 1) / (E / G)};
+  const bool scored = bias || (G > 1 && top2);
+  return by_width(E, [&](auto L, auto W) {
+    constexpr int LPR = decltype(L)::value, V = decltype(W)::value, VPL = (LPR * V + 63) / 64;
+    if (LPR == 64 || k > LPR || G > LPR) {
+      const size_t sm = G > 1 ? (size_t)NW * (VPL * 64 + 64) * sizeof(int64_t) : 0;
+      const int64_t g = row_grid(T, NW);
+      const int grid = (int)(g > (1 << 20) ? (1 << 20) : g);
+      if (dtype == MOE_F32)
+        route_wave_kernel<float, VPL><<<grid, NT, sm, st>>>(a);
+      else
+        route_wave_kernel<bf16_t, VPL><<<grid, NT, sm, st>>>(a);
+    } else if constexpr (LPR < 64) {
+      const int grid = row_grid(T, NW * (64 / LPR));
+      if (dtype == MOE_F32) {
+        if (scored) route_kernel<float, LPR, V, true><<<grid, NT, 0, st>>>(a);
+        else route_kernel<float, LPR, V, false><<<grid, NT, 0, st>>>(a);
+      } else {
+        if (scored) route_kernel<bf16_t, LPR, V, true><<<grid, NT, 0, st>>>(a);
+        else route_kernel<bf16_t, LPR, V, false><<<grid, NT, 0, st>>>(a);
+      }
+    }
   });
 }
 
 hipError_t launch_route_bwd(const float *g, const void *logits, const int32_t *ids, const float *w,
                             int64_t T, int E, int k, bool sigmoid, bool renorm, float scale,
                             void *d, int dtype, hipStream_t st) {
-  RouteBwdArgs a{g, logits, ids, w, d, T, E, k, sigmoid, renorm, scale};
-  return by_width(E, [&](auto V) {
-    constexpr int VPL = decltype(V)::value;
+  const RouteBwdArgs a{g, logits, ids, w, d, T, E, k, sigmoid, renorm, scale,
+                       rows_on_lines(logits, E, dtype) && rows_on_lines(d, E, dtype)};
+  return by_width(E, [&](auto L, auto W) {
+    constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
+    const int grid = row_grid(T, NW * (64 / LPR));
     if (dtype == MOE_F32)
-      route_bwd_kernel<float, VPL><<<row_grid(T), NT, 0, st>>>(a);
+      route_bwd_kernel<float, LPR, V><<<grid, NT, 0, st>>>(a);
     else
-      route_bwd_kernel<bf16_t, VPL><<<row_grid(T), NT, 0, st>>>(a);
+      route_bwd_kernel<bf16_t, LPR, V><<<grid, NT, 0, st>>>(a);
   });
 }
 
-static int loss_blocks(int64_t T) {
-  const int64_t g = (T + NW - 1) / NW;
+static int loss_blocks(int64_t T, int E) {
+  const int lpr = E <= 256 ? 16 : E <= 512 ? 32 : 64;
+  const int64_t g = (T + LW * (64 / lpr) - 1) / (LW * (64 / lpr));
   return (int)(g > kLossBlocks ? kLossBlocks : g);
 }
 
 size_t loss_workspace_bytes(int64_t T, int E) {
-  return (size_t)loss_blocks(T) * (2 * (size_t)E + 2) * sizeof(float);
+  return (size_t)loss_blocks(T, E) * (2 * (size_t)E + 2) * sizeof(float);
 }
 
 hipError_t launch_loss_fwd(const void *logits, const int32_t *ids, int64_t T, int E, int k,
                            bool sigmoid, float *losses, float *stats, int dtype, void *ws,
                            hipStream_t st) {
-  LossArgs a{logits, ids, (float *)ws, losses, stats, nullptr, nullptr, T, E, k, sigmoid,
-             loss_blocks(T)};
+  const LossArgs a{logits, ids, (float *)ws, losses, stats, nullptr, nullptr, T, E, k, sigmoid,
+                   loss_blocks(T, E), rows_on_lines(logits, E, dtype)};
   hipError_t e = hipSuccess;
   if (a.blocks > 0)
-    e = by_width(E, [&](auto V) {
-      constexpr int VPL = decltype(V)::value;
+    e = by_width(E, [&](auto L, auto W) {
+      constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
       if (dtype == MOE_F32)
-        loss_fwd_kernel<float, VPL><<<a.blocks, NT, 0, st>>>(a);
+        loss_fwd_kernel<float, LPR, V><<<a.blocks, LT, 0, st>>>(a);
       else
-        loss_fwd_kernel<bf16_t, VPL><<<a.blocks, NT, 0, st>>>(a);
+        loss_fwd_kernel<bf16_t, LPR, V><<<a.blocks, LT, 0, st>>>(a);
     });
   if (e != hipSuccess) return e;
-  loss_join_kernel<<<1, 1024, 0, st>>>(a);
+  loss_join_kernel<<<1, LT, 0, st>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_loss_bwd(const float *dloss, const void *logits, const float *stats, int64_t T,
                            int E, bool sigmoid, void *d, int dtype, hipStream_t st) {
-  LossArgs a{logits, nullptr, nullptr, nullptr, const_cast<float *>(stats), dloss, d, T, E, 0,
-             sigmoid, 0};
-  return by_width(E, [&](auto V) {
-    constexpr int VPL = decltype(V)::value;
+  const LossArgs a{logits, nullptr, nullptr, nullptr, const_cast<float *>(stats), dloss, d, T, E, 0,
+                   sigmoid, 0, rows_on_lines(logits, E, dtype) && rows_on_lines(d, E, dtype)};
+  return by_width(E, [&](auto L, auto W) {
+    constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
+    const int64_t g = row_grid(T, NW * (64 / LPR));
+    const int grid = (int)(g > 4096 ? 4096 : g);
     if (dtype == MOE_F32)
-      loss_bwd_kernel<float, VPL><<<row_grid(T), NT, 0, st>>>(a);
+      loss_bwd_kernel<float, LPR, V><<<grid, NT, 0, st>>>(a);
     else
-      loss_bwd_kernel<bf16_t, VPL><<<row_grid(T), NT, 0, st>>>(a);
+      loss_bwd_kernel<bf16_t, LPR, V><<<grid, NT, 0, st>>>(a);
   });
 }
 
