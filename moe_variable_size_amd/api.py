@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -454,35 +455,45 @@ def moe_fused_bwd(dY: torch.Tensor, x: torch.Tensor, W: Optional[torch.Tensor], 
 
 # ---- routing, router losses, dense linear layer -----------------------------------------------
 
-class _launch:
-    """Device and stream of a call: a context in which the tensor's device is
-    current, yielding the raw stream (the caller's, or that device's current
-    one); buffers the binding allocates inside come from that stream's pool."""
-
-    def __init__(self, t: torch.Tensor, stream=None):
-        dev = t.device
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        self._ctx = []
-        if stream is not None:  # makes the stream's device current too
-            self._ctx.append(torch.cuda.stream(stream))
-        elif dev.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(dev))
-        self._raw = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        return self._raw
-
-    def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
+_HERE = contextlib.nullcontext()
 
 
-def _require_on(t: Optional[torch.Tensor], name: str, device) -> None:
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _launch(t: torch.Tensor, stream=None):
+    """Context and raw stream of a call on t's device: buffers the binding
+    allocates inside the context come from that stream's pool.  The usual case,
+    the current stream of the current device, costs no context switch."""
+    index = t.get_device()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(index)), raw
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _need(t: torch.Tensor, name: str, dtype, ndim: int, index: int) -> None:
+    """A dense device tensor of this dtype (None: any) and rank on device ``index``."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype == dtype) \
+            and t.dim() == ndim and t.is_contiguous() and (index < 0 or t.get_device() == index):
+        return
+    _require(t, name, dtype, ndim)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+# workspace sizes depend on the call's sizes alone
+@functools.lru_cache(maxsize=4096)
+def _loss_workspace(T, E):
+    return int(_lib.load().moe_router_loss_workspace_bytes(T, E))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_fwd_workspace(M, K, N, code):
+    return int(_lib.load().moe_linear_fwd_workspace_bytes(M, K, N, code))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_bwd_workspace(M, K, N, act, code, out_code):
+    return int(_lib.load().moe_linear_bwd_workspace_bytes(M, K, N, act, code, out_code))
 
 
 def _option(table: dict, value, name: str) -> int:
@@ -506,17 +517,17 @@ def moe_route_fwd(logits: torch.Tensor, k: int, *, score: str = "softmax",
     (expert_ids [T, k] int32, topk_weights [T, k] float32), which
     ``moe_build_schedule`` and ``moe`` take."""
     lib = _lib.load()
-    _require(logits, "logits", None, 2)
-    code = _dtype_code(logits)
+    _need(logits, "logits", None, 2, -1)
+    code, index = _dtype_code(logits), logits.get_device()
     sc, gs = _option(MOE_SCORES, score, "score"), _option(MOE_GROUP_SCORES, group_score, "group_score")
     T, E = logits.shape
     dev = logits.device
     if bias is not None:
-        _require(bias, "bias", torch.float32, 1)
-        _require_on(bias, "bias", dev)
+        _need(bias, "bias", torch.float32, 1, index)
         if bias.numel() != E:
             raise ValueError(f"bias must have {E} entries, got {bias.numel()}")
-    with _launch(logits, stream) as raw:
+    ctx, raw = _launch(logits, stream)
+    with ctx:
         if expert_ids is None:
             expert_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         else:
@@ -538,22 +549,21 @@ def moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, expert_ids: tor
     and weights ``moe_route_fwd`` returned with the same options (the choice is
     held fixed).  Returns d_logits [T, E] in the logits' dtype."""
     lib = _lib.load()
-    _require(logits, "logits", None, 2)
-    code = _dtype_code(logits)
+    _need(logits, "logits", None, 2, -1)
+    code, index = _dtype_code(logits), logits.get_device()
     sc = _option(MOE_SCORES, score, "score")
     T, E = logits.shape
     dev = logits.device
-    _require(expert_ids, "expert_ids", torch.int32, 2)
-    shape = tuple(expert_ids.shape)
+    _need(expert_ids, "expert_ids", torch.int32, 2, index)
+    shape = expert_ids.shape
     for t, name in ((d_weights, "d_weights"), (topk_weights, "topk_weights")):
-        _require(t, name, torch.float32, 2)
-        _require_on(t, name, dev)
-        if tuple(t.shape) != shape:
+        _need(t, name, torch.float32, 2, index)
+        if t.shape != shape:
             raise ValueError(f"{name} must have the shape of expert_ids")
-    _require_on(expert_ids, "expert_ids", dev)
     if shape[0] != T:
         raise ValueError("expert_ids and logits disagree on T")
-    with _launch(logits, stream) as raw:
+    ctx, raw = _launch(logits, stream)
+    with ctx:
         if d_logits is None:
             d_logits = torch.empty_like(logits)
         else:
@@ -572,17 +582,17 @@ def moe_router_loss_fwd(logits: torch.Tensor, expert_ids: torch.Tensor, *, score
     above -inf.  Returns (losses [2] float32, stats [E + 1] float32 for
     ``moe_router_loss_bwd``)."""
     lib = _lib.load()
-    _require(logits, "logits", None, 2)
-    code = _dtype_code(logits)
+    _need(logits, "logits", None, 2, -1)
+    code, index = _dtype_code(logits), logits.get_device()
     sc = _option(MOE_SCORES, score, "score")
     T, E = logits.shape
     dev = logits.device
-    _require(expert_ids, "expert_ids", torch.int32, 2)
-    _require_on(expert_ids, "expert_ids", dev)
+    _need(expert_ids, "expert_ids", torch.int32, 2, index)
     if expert_ids.shape[0] != T:
         raise ValueError("expert_ids and logits disagree on T")
-    with _launch(logits, stream) as raw:
-        nbytes = int(lib.moe_router_loss_workspace_bytes(T, E))
+    ctx, raw = _launch(logits, stream)
+    with ctx:
+        nbytes = _loss_workspace(T, E)
         losses = torch.empty(2, dtype=torch.float32, device=dev)
         stats = torch.empty(E + 1, dtype=torch.float32, device=dev)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
@@ -597,17 +607,17 @@ def moe_router_loss_bwd(d_losses: torch.Tensor, logits: torch.Tensor, stats: tor
     """Gradient of d_losses[0] * balance + d_losses[1] * z with respect to the
     logits (the shares f_e are constants); d_losses [2] float32 on the device."""
     lib = _lib.load()
-    _require(logits, "logits", None, 2)
-    code = _dtype_code(logits)
+    _need(logits, "logits", None, 2, -1)
+    code, index = _dtype_code(logits), logits.get_device()
     sc = _option(MOE_SCORES, score, "score")
     T, E = logits.shape
     dev = logits.device
     for t, name, n in ((d_losses, "d_losses", 2), (stats, "stats", E + 1)):
-        _require(t, name, torch.float32, 1)
-        _require_on(t, name, dev)
+        _need(t, name, torch.float32, 1, index)
         if t.numel() != n:
             raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    with _launch(logits, stream) as raw:
+    ctx, raw = _launch(logits, stream)
+    with ctx:
         if d_logits is None:
             d_logits = torch.empty_like(logits)
         else:
@@ -629,11 +639,10 @@ def moe_linear_fwd(x: torch.Tensor, W: torch.Tensor, *, bias: Optional[torch.Ten
     Returns out [M, N] and, with ``save_z`` (or ``z`` given), also z = x W^T +
     bias in x's dtype, which the backward needs unless act is "none"."""
     lib = _lib.load()
-    _require(x, "x", None, 2)
-    code = _dtype_code(x)
+    _need(x, "x", None, 2, -1)
+    code, index = _dtype_code(x), x.get_device()
     dt, dev = x.dtype, x.device
-    _require(W, "W", dt, 2)
-    _require_on(W, "W", dev)
+    _need(W, "W", dt, 2, index)
     M, K = x.shape
     N = W.shape[0]
     if W.shape[1] != K:
@@ -647,7 +656,8 @@ def moe_linear_fwd(x: torch.Tensor, W: torch.Tensor, *, bias: Optional[torch.Ten
         _require_out(bias, "bias", dt, (N,), dev)
     if residual is not None:
         _require_out(residual, "residual", out_dtype, (M, N), dev)
-    with _launch(x, stream) as raw:
+    ctx, raw = _launch(x, stream)
+    with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=out_dtype, device=dev)
         else:
@@ -656,7 +666,7 @@ def moe_linear_fwd(x: torch.Tensor, W: torch.Tensor, *, bias: Optional[torch.Ten
             _require_out(z, "z", dt, (M, N), dev)
         elif save_z:
             z = torch.empty((M, N), dtype=dt, device=dev)
-        nbytes = int(lib.moe_linear_fwd_workspace_bytes(M, K, N, code))
+        nbytes = _linear_fwd_workspace(M, K, N, code)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         st = lib.moe_linear_fwd(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), _ptr(z), M, K,
                                 N, a, code, _DTYPES[out_dtype], _ptr(ws), nbytes, raw)
@@ -672,13 +682,11 @@ def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act
     dtype) and the saved z (not needed for act "none").  The residual's
     gradient is d_out itself."""
     lib = _lib.load()
-    _require(x, "x", None, 2)
-    code = _dtype_code(x)
+    _need(x, "x", None, 2, -1)
+    code, index = _dtype_code(x), x.get_device()
     dt, dev = x.dtype, x.device
-    _require(W, "W", dt, 2)
-    _require_on(W, "W", dev)
-    _require(d_out, "d_out", None, 2)
-    _require_on(d_out, "d_out", dev)
+    _need(W, "W", dt, 2, index)
+    _need(d_out, "d_out", None, 2, index)
     ocode = _dtype_code(d_out)
     M, K = x.shape
     N = W.shape[0]
@@ -689,11 +697,12 @@ def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act
         if z is None:
             raise ValueError(f"act {act!r} needs the z its forward saved")
         _require_out(z, "z", dt, (M, N), dev)
-    with _launch(x, stream) as raw:
+    ctx, raw = _launch(x, stream)
+    with ctx:
         dX = torch.empty((M, K), dtype=dt, device=dev) if dx else None
         dW = torch.empty((N, K), dtype=dt, device=dev) if dw else None
         db = torch.empty(N, dtype=dt, device=dev) if dbias else None
-        nbytes = int(lib.moe_linear_bwd_workspace_bytes(M, K, N, a, code, ocode))
+        nbytes = _linear_bwd_workspace(M, K, N, a, code, ocode)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         st = lib.moe_linear_bwd(_ptr(d_out), _ptr(x), _ptr(W), _ptr(z) if a else None, _ptr(dX), _ptr(dW),
                                 _ptr(db), M, K, N, a, code, ocode, _ptr(ws), nbytes, raw)

@@ -6,6 +6,7 @@
 // reduction index (K-major) or the output index (MN-major) is contiguous in memory.
 #include <stdlib.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.hpp"
@@ -171,35 +172,41 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 }
 
 // ---- staged tiles: any alignment and size ------------------------------------
-// 128 x 128 outputs per 4 waves (2 x 2, 64 x 64 each), 32 reduction elements per
-// step through registers into LDS, element loads with bounds checks.
-constexpr int SBM = 128, SBN = 128, SBK = 32, SNT = 256;
+// 64 S x 64 S outputs per 4 waves (2 x 2, S x S blocks of 32 x 32 each), 32 reduction elements per
+// step through registers into LDS, element loads with bounds checks.  fp32 multiplies on the
+// matrix cores' fp32 instructions (exact products, fp32 sums; 64 clocks per 2 reduction elements of
+// a block, so the loads hide behind them); a reduction may be cut into ranges as below.
+constexpr int SBK = 32, SNT = 256;
 
 template <typename T>
 struct Pitch {  // LDS row pitch in elements: rows 16-byte aligned, spread over the banks
   static constexpr int v = sizeof(T) == 2 ? SBK + 8 : SBK + 1;
 };
 
-// a 128 x 32 tile of an operand: element (r, k) to lds[r][k]; thread t brings 16 elements
-template <typename T, bool KMAJ>
-MOE_DEV void stage_load(const T *p, int64_t ld, int r0, int rows, int k0, int K, T (&v)[16]) {
+// a 64 S x 32 tile of an operand: element (r, k) to lds[r][k]; thread t brings 8 S elements
+template <int S, bool KMAJ>
+MOE_DEV void stage_at(int i, int &r, int &k) {
   const int t = threadIdx.x;
+  r = KMAJ ? i * 8 + (t >> 5) : t % (64 * S);
+  k = KMAJ ? t & 31 : i * (4 / S) + t / (64 * S);
+}
+template <typename T, int S, bool KMAJ>
+MOE_DEV void stage_load(const T *p, int64_t ld, int r0, int rows, int k0, int K, T (&v)[8 * S]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = KMAJ ? i * 8 + (t >> 5) : t & 127;
-    const int k = KMAJ ? t & 31 : i * 2 + (t >> 7);
+  for (int i = 0; i < 8 * S; ++i) {
+    int r, k;
+    stage_at<S, KMAJ>(i, r, k);
     const bool ok = r0 + r < rows && k0 + k < K;
     const int64_t at = KMAJ ? (int64_t)(r0 + r) * ld + k0 + k : (int64_t)(k0 + k) * ld + r0 + r;
     v[i] = ok ? p[at] : (T)0;
   }
 }
-template <typename T, bool KMAJ>
-MOE_DEV void stage_store(T *lds, const T (&v)[16]) {
-  const int t = threadIdx.x;
+template <typename T, int S, bool KMAJ>
+MOE_DEV void stage_store(T *lds, const T (&v)[8 * S]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = KMAJ ? i * 8 + (t >> 5) : t & 127;
-    const int k = KMAJ ? t & 31 : i * 2 + (t >> 7);
+  for (int i = 0; i < 8 * S; ++i) {
+    int r, k;
+    stage_at<S, KMAJ>(i, r, k);
     lds[r * Pitch<T>::v + k] = v[i];
   }
 }
@@ -207,71 +214,82 @@ MOE_DEV void stage_store(T *lds, const T (&v)[16]) {
 // row of register i of a 32 x 32 accumulator
 MOE_DEV int acc_row(int i, int lane) { return ((i >> 2) << 3) + ((lane >> 5) << 2) + (i & 3); }
 
-template <typename T, typename To, bool AK, bool BKM, int ACT>
-__global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p) {
-  constexpr int P = Pitch<T>::v;
-  __shared__ T As[SBM * P], Bs[SBN * P];
+// splits > 1: range blockIdx / tiles of the reduction, fp32 products to part [splits][M][N]
+template <typename T, typename To, int S, bool AK, bool BKM, int ACT>
+__global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part) {
+  constexpr int P = Pitch<T>::v, TS = 64 * S;
+  __shared__ __align__(16) T As[TS * P], Bs[TS * P];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int wm = (wid >> 1) * 64, wn = (wid & 1) * 64;
-  const int tn = (p.N + SBN - 1) / SBN;
-  const int m0 = blockIdx.x / tn * SBM, n0 = blockIdx.x % tn * SBN;
-  f32x16 acc[2][2] = {};
-  T va[16], vb[16];
-  stage_load<T, AK>((const T *)p.A, p.lda, m0, p.M, 0, p.K, va);
-  stage_load<T, BKM>((const T *)p.B, p.ldb, n0, p.N, 0, p.K, vb);
-  for (int k0 = 0; k0 < p.K; k0 += SBK) {
+  const int wm = (wid >> 1) * 32 * S, wn = (wid & 1) * 32 * S;
+  const int tn = (p.N + TS - 1) / TS, tiles = tn * ((p.M + TS - 1) / TS);
+  const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+  const int m0 = tile / tn * TS, n0 = tile % tn * TS;
+  const int steps = (p.K + SBK - 1) / SBK;
+  const int kb = (int)((int64_t)steps * split / splits) * SBK;
+  const int ke = min(p.K, (int)((int64_t)steps * (split + 1) / splits) * SBK);
+  f32x16 acc[S][S] = {};
+  T va[8 * S], vb[8 * S];
+  stage_load<T, S, AK>((const T *)p.A, p.lda, m0, p.M, kb, ke, va);
+  stage_load<T, S, BKM>((const T *)p.B, p.ldb, n0, p.N, kb, ke, vb);
+  for (int k0 = kb; k0 < ke; k0 += SBK) {
     __syncthreads();
-    stage_store<T, AK>(As, va);
-    stage_store<T, BKM>(Bs, vb);
+    stage_store<T, S, AK>(As, va);
+    stage_store<T, S, BKM>(Bs, vb);
     __syncthreads();
-    if (k0 + SBK < p.K) {
-      stage_load<T, AK>((const T *)p.A, p.lda, m0, p.M, k0 + SBK, p.K, va);
-      stage_load<T, BKM>((const T *)p.B, p.ldb, n0, p.N, k0 + SBK, p.K, vb);
+    if (k0 + SBK < ke) {
+      stage_load<T, S, AK>((const T *)p.A, p.lda, m0, p.M, k0 + SBK, ke, va);
+      stage_load<T, S, BKM>((const T *)p.B, p.ldb, n0, p.N, k0 + SBK, ke, vb);
     }
     const int r = lane & 31, h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int s = 0; s < SBK / 16; ++s) {
-        bf16x8_t a[2], b[2];
+        bf16x8_t a[S], b[S];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S; ++i) {
           a[i] = *(const bf16x8_t *)&As[(wm + i * 32 + r) * P + s * 16 + h * 8];
           b[i] = *(const bf16x8_t *)&Bs[(wn + i * 32 + r) * P + s * 16 + h * 8];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < S; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < S; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
       }
     } else {
 #pragma unroll
       for (int s = 0; s < SBK / 2; ++s) {
-        float a[2], b[2];
+        float a[S], b[S];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S; ++i) {
           a[i] = As[(wm + i * 32 + r) * P + s * 2 + h];
           b[i] = Bs[(wn + i * 32 + r) * P + s * 2 + h];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < S; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < S; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[j], acc[i][j], 0, 0, 0);
       }
     }
   }
+  if (splits > 1) part += (int64_t)split * p.M * p.N;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < S; ++j) {
     const int n = n0 + wn + j * 32 + (lane & 31);
     if (n >= p.N) continue;
     const float b = p.bias ? ldf((const T *)p.bias + n) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int m = m0 + wm + i * 32 + acc_row(e, lane);
-        if (m < p.M) finish1<T, To, ACT>(p, acc[i][j][e] + b, (int64_t)m * p.N + n);
+        if (m >= p.M) continue;
+        const int64_t at = (int64_t)m * p.N + n;
+        if (splits > 1)
+          part[at] = acc[i][j][e];
+        else
+          finish1<T, To, ACT>(p, acc[i][j][e] + b, at);
       }
   }
 }
@@ -577,7 +595,8 @@ __global__ __launch_bounds__(512, HM * HN >= 4 ? 2 : 4) void piped_gemm(PipeArgs
 // that reading the other one is the work: 16 TI x 16 TJ outputs per workgroup, whose NW waves
 // share the reduction (wave w takes the 64-element pieces w, w + NW, ..., whole 128-byte lines of
 // bf16) and add up through LDS in wave order.  Operands go from memory to registers, 16 bytes per
-// lane, D pieces ahead; the smaller operand comes out of L2.
+// lane, D pieces ahead; the smaller operand comes out of L2.  Workgroups start at different pieces:
+// rows are often a power of two apart, and all workgroups on the same piece meet on few channels.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 MOE_DEV f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -615,11 +634,15 @@ __global__ __launch_bounds__(NW * 64) void stream_gemm(GemmArgs p) {
   const int pieces = (p.K + PIECE - 1) / PIECE;
   f32x4 acc[TI][TJ] = {};
   u32x4 a[D][2][TI], b[D][2][TJ];
+  const int rot = (int)(blockIdx.x % (uint32_t)pieces);
   auto load = [&](int pc, int d) __attribute__((always_inline)) {
+    const bool on = pc < pieces;  // (past the end nothing is read)
+    int at = pc + rot;
+    at = at >= pieces ? at - pieces : at;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = pc * PIECE + s * 4 * E + (lane >> 4) * E;
-      const uint32_t off = k < p.K ? base + k * (uint32_t)sizeof(T) : kOobOffset;
+      const int k = at * PIECE + s * 4 * E + (lane >> 4) * E;
+      const uint32_t off = on && k < p.K ? base + k * (uint32_t)sizeof(T) : kOobOffset;
 #pragma unroll
       for (int i = 0; i < TI; ++i)
         a[d][s][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, off + i * 16 * rowb, 0, 0);
@@ -639,7 +662,7 @@ __global__ __launch_bounds__(NW * 64) void stream_gemm(GemmArgs p) {
         for (int i = 0; i < TI; ++i)
 #pragma unroll
           for (int j = 0; j < TJ; ++j) acc[i][j] = mfma16<T>(b[d][s][j], a[d][s][i], acc[i][j]);
-      load(pc + (D + d) * NW, d);  // (past the end: nothing is read)
+      load(pc + (D + d) * NW, d);
     }
   }
 #pragma unroll
@@ -656,6 +679,62 @@ __global__ __launch_bounds__(NW * 64) void stream_gemm(GemmArgs p) {
     for (int w = 0; w < NW; ++w) v += red[cell(w, e / TN, e % TN)];
     if (p.bias) v += ldf((const T *)p.bias + n);
     finish1<T, To, ACT>(p, v, (int64_t)m * p.N + n);
+  }
+}
+
+// ---- at most 4 rows of x: a wave per output column ---------------------------------
+// 64 lanes read a row of W in whole lines, U x 16 bytes per lane in flight, and multiply it by every
+// row of x (out of L1); fp32 sums per lane, then across the wave.
+template <typename T>
+MOE_DEV void dot16(u32x4 a, u32x4 b, float &s) {
+  if constexpr (sizeof(T) == 4) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(x[i], y[i], s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+      s = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), s);
+    }
+  }
+}
+
+template <typename T, typename To, int ACT, int MR>
+__global__ __launch_bounds__(512) void row_gemm(GemmArgs p) {
+  constexpr int E = 16 / sizeof(T), U = MR == 1 ? 8 : 4;
+  const int lane = threadIdx.x & 63;
+  const int n = blockIdx.x * 8 + (threadIdx.x >> 6);
+  if (n >= p.N) return;
+  const u32x4 *w = (const u32x4 *)((const T *)p.B + (int64_t)n * p.K);
+  const u32x4 *x[MR];
+#pragma unroll
+  for (int m = 0; m < MR; ++m) x[m] = (const u32x4 *)((const T *)p.A + (int64_t)min(m, p.M - 1) * p.K);
+  float s[MR][2] = {};
+  const int chunks = p.K / E;
+  for (int c0 = 0; c0 < chunks; c0 += 64 * U) {
+    u32x4 wv[U], xv[U][MR];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 64 + lane;
+      wv[u] = c < chunks ? w[c] : u32x4{};
+#pragma unroll
+      for (int m = 0; m < MR; ++m) xv[u][m] = c < chunks ? x[m][c] : u32x4{};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MR; ++m) dot16<T>(wv[u], xv[u][m], s[m][u & 1]);
+  }
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    float v = s[m][0] + s[m][1];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    if (lane == m && m < p.M) {
+      if (p.bias) v += ldf((const T *)p.bias + n);
+      finish1<T, To, ACT>(p, v, (int64_t)m * p.N + n);
+    }
   }
 }
 
@@ -760,7 +839,15 @@ hipError_t run_piped(PipeArgs &q, int act, hipStream_t st) {
   hipError_t e = hipSuccess;
   by_act_of<AK && BKM>(act, [&](auto A) {
     auto k = piped_gemm<HM, HN, WGM, WGN, AK, BKM, To, decltype(A)::value>;
-    e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    // once per device (the attribute is the function's on that device)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (e == hipSuccess && !(done.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+      if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (e == hipSuccess) {
       k<<<grid, 512, SMEM, st>>>(q);
       e = hipGetLastError();
@@ -808,16 +895,39 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   }
   return best;
 }
-size_t part_bytes(int64_t M, int64_t N, int64_t K) {
-  const Plan p = plan_of(M, N, K);
-  return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
+// The staged kernel's: 128 x 128 (S = 2) where that fills the chip twice; else 64 x 64, with the
+// reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
+// backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us).
+Plan staged_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t t2 = ((M + 127) / 128) * ((N + 127) / 128), t1 = ((M + 63) / 64) * ((N + 63) / 64);
+  if (t2 >= 512) return Plan{2, 1};
+  const int64_t steps = (K + SBK - 1) / SBK;
+  int64_t k = t1 > 0 ? 1024 / t1 : 1;
+  if (k > steps / 4) k = steps / 4;
+  if (k > 16) k = 16;
+  return Plan{1, (int)(k < 1 ? 1 : k)};
+}
+// workspace for the partial products of either kernel
+size_t part_bytes(int64_t M, int64_t N, int64_t K, bool bf16) {
+  const int a = staged_plan(M, N, K).splits, b = bf16 ? plan_of(M, N, K).splits : 1;
+  const int k = a > b ? a : b;
+  return k > 1 ? (size_t)k * M * N * 4 : 0;
 }
 
-// workspace `part`: part_bytes(M, N, K)
 // Whether the forward streams: x or W has at most 64 rows, and rows on 16-byte lines.
 bool streams(const GemmArgs &a, size_t es) {
   return (a.M <= 64 || a.N <= 64) && a.K % (int)(16 / es) == 0 && a.K <= (1 << 22) && on_line(a.A, 16) &&
          on_line(a.B, 16);
+}
+
+template <bool FWD, typename T, typename To>
+hipError_t join(const GemmArgs &a, int act, const void *part, int splits, hipStream_t st) {
+  const int64_t groups = (int64_t)a.M * a.N / (a.vec ? 8 : 1);
+  const int grid = (int)(groups < 256 * 4096 ? (groups + 255) / 256 : 4096);
+  by_act_of<FWD>(act, [&](auto A) {
+    join_kernel<T, To, decltype(A)::value><<<grid, 256, 0, st>>>(a, (const float *)part, splits);
+  });
+  return hipGetLastError();
 }
 
 template <typename T, typename To, int TI, int TJ, int NW, int D>
@@ -833,6 +943,16 @@ template <bool AK, bool BKM, typename T, typename To>
 hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
   if constexpr (AK && BKM) {
     if (streams(a, sizeof(T))) {
+      if (a.M <= 4) {
+        by_act(act, [&](auto A) {
+          constexpr int ACT = decltype(A)::value;
+          if (a.M == 1)
+            row_gemm<T, To, ACT, 1><<<(a.N + 7) / 8, 512, 0, st>>>(a);
+          else
+            row_gemm<T, To, ACT, 4><<<(a.N + 7) / 8, 512, 0, st>>>(a);
+        });
+        return hipGetLastError();
+      }
       if (a.M <= 16 || a.N <= 16) return run_stream<T, To, 1, 1, 16, 4>(a, act, st);
       if (a.M <= a.N) return run_stream<T, To, 4, 2, 8, 2>(a, act, st);
       return run_stream<T, To, 2, 4, 8, 2>(a, act, st);
@@ -855,19 +975,22 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
                            : pl.shape == 1 ? run_piped<2, 2, 4, 2, AK, BKM, To>(q, act, st)
                                            : run_piped<2, 1, 2, 4, AK, BKM, To>(q, act, st);
       if (e != hipSuccess || pl.splits == 1) return e;
-      const int64_t groups = (int64_t)a.M * a.N / (a.vec ? 8 : 1);
-      const int grid = (int)(groups < 256 * 4096 ? (groups + 255) / 256 : 4096);
-      by_act_of<AK && BKM>(act, [&](auto A) {
-        join_kernel<T, To, decltype(A)::value><<<grid, 256, 0, st>>>(a, (const float *)part, pl.splits);
-      });
-      return hipGetLastError();
+      return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
     }
   }
-  const int grid = ((a.N + SBN - 1) / SBN) * ((a.M + SBM - 1) / SBM);
+  const Plan pl = staged_plan(a.M, a.N, a.K);
+  const int ts = 64 * pl.shape;
+  const int grid = ((a.N + ts - 1) / ts) * ((a.M + ts - 1) / ts) * pl.splits;
   by_act_of<AK && BKM>(act, [&](auto A) {
-    staged_gemm<T, To, AK, BKM, decltype(A)::value><<<grid, SNT, 0, st>>>(a);
+    constexpr int ACT = decltype(A)::value;
+    if (pl.shape == 2)
+      staged_gemm<T, To, 2, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part);
+    else
+      staged_gemm<T, To, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part);
   });
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pl.splits == 1) return e;
+  return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -883,7 +1006,8 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t N, bool own_dz, int dtype) {
   w.dz = 0;
   w.sums = own_dz ? up256((size_t)M * N * (dtype == MOE_F32 ? 4 : 2)) : 0;
   w.part = w.sums + up256((size_t)dz_ranges(M) * N * 4);
-  const size_t px = part_bytes(M, K, N), pw = part_bytes(N, K, M);
+  const bool bf16 = dtype == MOE_BF16;
+  const size_t px = part_bytes(M, K, N, bf16), pw = part_bytes(N, K, M, bf16);
   w.total = w.part + up256(px > pw ? px : pw);
   return w;
 }
@@ -927,7 +1051,7 @@ hipError_t bwd(const void *dout, const void *x, const void *W, const void *z, vo
 }  // namespace
 
 size_t linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype) {
-  return dtype == MOE_BF16 ? part_bytes(M, N, K) : 0;
+  return part_bytes(M, N, K, dtype == MOE_BF16);
 }
 
 size_t linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int act, int dtype, int out_dtype) {

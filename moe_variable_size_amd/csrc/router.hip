@@ -88,6 +88,7 @@ struct RowMap {
 };
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 MOE_DEV void ld4(const float *p, float (&v)[4]) {
   const f32x4 a = *(const f32x4 *)p;
 #pragma unroll
@@ -326,28 +327,55 @@ __global__ __launch_bounds__(NT) void route_wave_kernel(RouteArgs p) {
 }
 
 // ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= LPR ------------------
-// 32-bit keys that order like the choice value in fp32 (0: may not be chosen), in registers and in
+// 32-bit keys that order like the choice value in fp32 (that of -inf: never chosen), in registers and in
 // LDS by expert.  Every lane keeps the best of its V experts.  A round reduces the row's best and
 // its expert over the lanes, strikes it out in LDS, and the lanes look at the struck owner's V
 // values, one each, for the owner's new best: about 36 instructions a round for all rows of the
 // wave, where striking out and searching again in registers takes 80.
 //
 // Without a bias the keys are the logits' own order: exact.  With one (and for groups by sums of
-// scores) the values are fp32 approximations.  A score is off by less than 2 eps of the row's largest,
-// eps = (x + 24) 2^-24: x, the span of the exponentials' arguments, is rounded twice, and the
-// exponential, a sum 20 additions deep and the reciprocal add less than 48 roundings; adding the bias
-// rounds the value once more.  Where two values next to each other in the order, or the groups on
-// both sides of the cut, are closer than their errors together, the wave chooses that row again in
-// 64 bits (about one row in 300 of normally distributed logits).
+// scores) the values are fp32 approximations, u = 2^-24:
+//   sigmoid: the exponential's argument is rounded once and it is off by 2 u itself, 1 + e by u, the
+//     reciprocal by 2 u: s (1 - s) (|l| + 2) u + 3 s u, which is at most 5 u times the largest score
+//     of the row (times 1 - max l where that is below 0);
+//   softmax: with x the distance from the maximum, two roundings of x, and 28 more of the
+//     exponential, a sum 21 additions deep, the reciprocal and the product; the sum's terms carry
+//     2 x u each, weighted by their share at most 2 ln E = 13 u: e^-x (2 x + 13 + 28) u <= 42 u
+//     times the largest score.
+// Adding the bias rounds once more.  Where two values next to each other in the order, or the groups
+// on both sides of the cut, are closer than their two errors, or the row holds a NaN, the wave
+// chooses that row again in 64 bits.
 MOE_DEV uint32_t key32(float c) {
   const uint32_t u = f2u(c + 0.f);  // -0 -> +0
   return c != c ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+MOE_DEV uint32_t key32_number(float c) {  // of a number, and of no -0
+  const uint32_t u = f2u(c);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 MOE_DEV float key32_value(uint32_t k) {
   return k == 0xFFFFFFFFu ? __builtin_nanf("") : u2f((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-template <typename T, int LPR, int V, bool SCORED>
+// What the fp32 keys are: the logits' own; score + bias; the logits', with groups ranked by scores.
+enum { BY_LOGIT = 0, BY_BIASED = 1, GROUPS_BY_SCORE = 2 };
+constexpr uint32_t kBarred32 = 0x007FFFFFu;  // key of -inf
+
+// the keys of a lane to the row's table in LDS (by expert)
+template <int LPR, int V>
+MOE_DEV void put_keys(uint32_t *keys, int sub, const uint32_t (&key)[V]) {
+  using M = RowMap<LPR, V>;
+  if constexpr (M::C == 4) {
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q)
+      *(u32x4 *)(keys + M::expert(sub, 4 * q)) = u32x4{key[4 * q], key[4 * q + 1], key[4 * q + 2], key[4 * q + 3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) keys[M::expert(sub, i)] = key[i];
+  }
+}
+
+template <typename T, int LPR, int V, int MODE>
 __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
   using M = RowMap<LPR, V>;
   constexpr int RPW = 64 / LPR, EP = LPR * V;   // rows per wave, experts (padded)
@@ -363,56 +391,63 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
   const T *row = (const T *)p.logits + (live ? t : 0) * p.E;
   float l[V];
   load_row<LPR, V>(row, p.E, sub, p.vec, l);
-  float m = l[0];
+  float m = 0.f, sum = 0.f;  // the softmax's maximum and sum, and the maximum for the error bound
+  if (MODE != BY_LOGIT || !(p.sigmoid || p.renorm)) {
+    m = l[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-  m = row_max<LPR>(m);
-  // sum of the softmax, where anything needs it
-  float sum = 0.f;
-  if (!p.sigmoid && (SCORED || !p.renorm)) {
+    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+    m = row_max<LPR>(m);
+    if (!p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
-    sum = row_sum<LPR>(sum);
+      for (int i = 0; i < V; ++i) sum += l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
+      sum = row_sum<LPR>(sum);
+    }
   }
-  uint32_t key[V], gkey[SCORED ? V : 1];  // gkey: what the groups are ranked by, if not the key
-  float err = 0.f;  // bound of a value's error, times 2 (two values' together)
-  if constexpr (SCORED) {
+  float bad = 0.f;  // a NaN if the row holds one
+  if (p.renorm && !p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad += l[i] != l[i] ? l[i] : 0.f;
+    bad = row_sum<LPR>(bad);
+  }
+  uint32_t key[V];
+  float err = 0.f;  // of two scores together
+  bool doubt = false;
+  if constexpr (MODE == BY_LOGIT) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = key32(l[i]);
+  } else {
     const float inv = __builtin_amdgcn_rcpf(sum);
-    float span = 0.f, top = 0.f, mag = 0.f, bs[V];
-    if (p.bias) {
-      load_row<LPR, V>(p.bias, p.E, sub, p.vec_bias, bs);
+    float nan = 0.f, c[V];
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + fexp(-l[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) bs[i] = 0.f;
+      for (int i = 0; i < V; ++i) c[i] = fexp(l[i] - m) * inv;
+    }
+    if constexpr (MODE == BY_BIASED) {
+      float bs[V];
+      load_row<LPR, V>(p.bias, p.E, sub, p.vec_bias, bs);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] += bs[i];
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool out = l[i] == -__builtin_inff(), barred = out || bs[i] == -__builtin_inff();
-      const float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + fexp(-l[i])) : out ? 0.f : fexp(l[i] - m) * inv;
-      const float c = s + bs[i];
-      key[i] = barred ? 0u : key32(p.bias ? c : l[i]);
-      gkey[i] = barred ? 0u : p.bias ? key[i] : key32(s);
-      top = fmaxf(top, s);
-      mag = fmaxf(mag, barred ? 0.f : fabsf(c));
-      span = fmaxf(span, out ? 0.f : p.sigmoid ? -l[i] : m - l[i]);
+      c[i] = l[i] == -__builtin_inff() ? -__builtin_inff() : c[i];
+      nan += c[i];
+      key[i] = key32_number(c[i]);
     }
-    const float eps = (fminf(row_max<LPR>(span), 104.f) + 24.f) * 0x1p-24f;
-    err = 4.f * (eps * row_max<LPR>(top) + 0x1p-24f * row_max<LPR>(mag));
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i] == -__builtin_inff() ? 0u : key32(l[i]);
+    const float top = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + fexp(-m)) : inv;
+    err = 2.f * top * (p.sigmoid ? 5.f * (1.f + fmaxf(-m, 0.f)) : 42.f) * 0x1p-24f;
+    nan = row_sum<LPR>(nan);  // (of -inf and +inf too)
+    doubt = nan != nan;
   }
-  // whether two values (of `terms` scores each) may stand in the other order in 64 bits; a NaN may
-  auto close = [&](uint32_t hi, uint32_t lo, float terms) __attribute__((always_inline)) {
-    return !(key32_value(hi) - key32_value(lo) > terms * err);
-  };
-  bool doubt = false;
   if (p.G > 1) {
     const int per = p.E / p.G;
+    put_keys<LPR, V>(keys, sub, key);
+    if constexpr (MODE == GROUPS_BY_SCORE) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if constexpr (SCORED) keys[M::expert(sub, i)] = gkey[i];
-      else keys[M::expert(sub, i)] = key[i];
+      for (int i = 0; i < V; ++i) key[i] = key32(l[i]);
     }
     wave_lds_sync();
     // lanes g, g + G', ... of the row scan group g (G' = the power of two above G - 1)
@@ -432,46 +467,58 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       b = max(min(a, oa), max(b, ob));
       a = max(a, oa);
     }
-    const uint32_t gv = !p.top2 || b == 0u ? a : key32(key32_value(a) + key32_value(b));
+    const bool two = p.top2 && b > kBarred32;
+    const float fa = key32_value(a), fb = two ? key32_value(b) : 0.f;
+    const uint32_t gv = two ? key32(fa + fb) : a;
     // rank of the lane's group; the kept one of lowest value and the best of the others
     int rank = 0;
     for (int d = 0; d < p.G; ++d) {
-      const uint32_t o = __shfl(gv, (lane & ~(LPR - 1)) + d, kWave);
+      const uint32_t o = __shfl(gv, d, LPR);
       rank += o > gv || (o == gv && d < g);
     }
-    const bool kept = g < p.G && gv != 0u && rank < p.keep;
-    if (SCORED && p.keep < p.G) {
-      const uint32_t lo = row_umin<LPR>(kept ? gv : 0xFFFFFFFFu);
+    const bool kept = g < p.G && gv > kBarred32 && rank < p.keep;
+    if (MODE != BY_LOGIT && p.keep < p.G) {
+      const float lo = key32_value(row_umin<LPR>(kept ? gv : 0xFFFFFFFFu));
       const uint32_t hi = row_umax<LPR>(kept || g >= p.G ? 0u : gv);
-      doubt = hi != 0u && close(lo, hi, 2.f);  // (sums of two carry both errors)
+      // two scores each, and each value's and the sum's own rounding
+      const float mag = row_max<LPR>(g < p.G && a > kBarred32 ? fabsf(fa) + fabsf(fb) : 0.f);
+      doubt |= hi > kBarred32 && !(lo - key32_value(hi) > 2.f * err + mag * 0x1p-21f);
     }
-    const uint64_t mask = __ballot(kept && sub < gp) >> (lane & ~(LPR - 1));
+    const uint32_t mask = (uint32_t)(__ballot(kept && sub < gp) >> (lane & ~(LPR - 1)));
+    if (M::C == 4 && per % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = M::expert(sub, i);
-      if (e >= p.E || !((mask >> (__umul24(e, p.per_magic) >> 20)) & 1)) key[i] = 0u;
+      for (int q = 0; q < (V + 3) / 4; ++q) {
+        const int e = M::expert(sub, 4 * q < V ? 4 * q : 0);
+        const bool in = e < p.E && ((mask >> (__umul24(e, p.per_magic) >> 20)) & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * q + i < V) key[4 * q + i] = in ? key[4 * q + i] : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = M::expert(sub, i);
+        if (e >= p.E || !((mask >> (__umul24(e, p.per_magic) >> 20)) & 1)) key[i] = 0u;
+      }
     }
     wave_lds_sync();
   }
-  uint32_t best = 0, at = 0xFFFFFFFFu;  // the lane's best key, and its expert
+  put_keys<LPR, V>(keys, sub, key);
+  uint32_t best = kBarred32, at = 0xFFFFFFFFu;  // the lane's best key, and its expert
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = M::expert(sub, i);
-    keys[e] = key[i];
-    if (key[i] > best) { best = key[i]; at = e; }
-  }
+  for (int i = 0; i < V; ++i)
+    if (key[i] > best) { best = key[i]; at = M::expert(sub, i); }
   wave_lds_sync();
   int id = -1;
-  uint32_t last = 0;
+  uint32_t won = 0;  // key of the lane's slot
   for (int j = 0; j < p.k; ++j) {
     const uint32_t mx = row_umax<LPR>(best);
     const uint32_t e = row_umin<LPR>(best == mx ? at : 0xFFFFFFFFu);
-    if (sub == j && mx != 0u) id = (int)e;
-    if constexpr (SCORED) {
-      if (p.bias) doubt |= j > 0 && mx != 0u && close(last, mx, 1.f);
-      last = mx;
+    const bool hit = mx > kBarred32;
+    if (sub == j && hit) {
+      id = (int)e;
+      won = mx;
     }
-    const bool hit = mx != 0u;
     const int owner = hit ? (int)(e / M::C) & (LPR - 1) : 0;
     if (hit && sub == 0) keys[e] = 0u;
     wave_lds_sync();
@@ -481,14 +528,16 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
     const uint32_t ne = row_umin<LPR>(v == nb ? (uint32_t)oe : 0xFFFFFFFFu);
     if (hit && sub == owner) { best = nb; at = ne; }
   }
-  if constexpr (SCORED) {
-    if (p.bias) {
-      const uint32_t mx = row_umax<LPR>(best);
-      doubt |= mx != 0u && last != 0u && close(last, mx, 1.f);
+  if constexpr (MODE != BY_LOGIT) {
+    if (MODE == BY_BIASED) {  // each slot's value against the next one's, the last against the best one left
+      const uint32_t left = row_umax<LPR>(best);
+      uint32_t next = __shfl_down(won, 1, LPR);
+      if (sub == p.k - 1) next = left;
+      const float hi = key32_value(won), lo = key32_value(next);
+      doubt |= sub < p.k && next > kBarred32 && !(hi - lo > err + (fabsf(hi) + fabsf(lo)) * 0x1p-23f);
     }
-  }
-  if constexpr (SCORED) {
     // every lane of a row has the same doubt
+    doubt = row_umax<LPR>(doubt) != 0u;
     uint64_t again = __ballot(doubt && live && sub == 0);
     while (again) {
       const int r = (__ffsll((unsigned long long)again) - 1) / LPR;
@@ -498,12 +547,6 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       const int mine = __shfl(x, sub, kWave);
       if (rw == r) id = mine;
     }
-  }
-  float bad = 0.f;
-  if (p.renorm && !p.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) bad += l[i] != l[i] ? l[i] : 0.f;
-    bad = row_sum<LPR>(bad);
   }
   const float w = chosen_weight<LPR>(p, id, id >= 0 ? ldf(row + id) : 0.f, m, sum, bad);
   if (live && sub < p.k) {
@@ -830,7 +873,6 @@ hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, in
   const RouteArgs a{logits, bias, ids, w, T, E, k, G, keep, sigmoid, top2, renorm, scale,
                     rows_on_lines(logits, E, dtype), bias && rows_on_lines(bias, E, MOE_F32),
                     ((1u << 20) + E / G - 1) / (E / G)};
-  const bool scored = bias || (G > 1 && top2);
   return by_width(E, [&](auto L, auto W) {
     constexpr int LPR = decltype(L)::value, V = decltype(W)::value, VPL = (LPR * V + 63) / 64;
     if (LPR == 64 || k > LPR || G > LPR) {
@@ -844,11 +886,13 @@ hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, in
     } else if constexpr (LPR < 64) {
       const int grid = row_grid(T, NW * (64 / LPR));
       if (dtype == MOE_F32) {
-        if (scored) route_kernel<float, LPR, V, true><<<grid, NT, 0, st>>>(a);
-        else route_kernel<float, LPR, V, false><<<grid, NT, 0, st>>>(a);
+        if (bias) route_kernel<float, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
+        else if (G > 1 && top2) route_kernel<float, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
+        else route_kernel<float, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
       } else {
-        if (scored) route_kernel<bf16_t, LPR, V, true><<<grid, NT, 0, st>>>(a);
-        else route_kernel<bf16_t, LPR, V, false><<<grid, NT, 0, st>>>(a);
+        if (bias) route_kernel<bf16_t, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
+        else if (G > 1 && top2) route_kernel<bf16_t, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
+        else route_kernel<bf16_t, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
       }
     }
   });
