@@ -4,8 +4,6 @@
 //
 // All three products have one form, C[m, n] = sum_k A(m, k) B(n, k): for each operand either the
 // reduction index (K-major) or the output index (MN-major) is contiguous in memory.
-#include <stdlib.h>
-
 #include <atomic>
 #include <type_traits>
 
@@ -416,8 +414,77 @@ struct PipeArgs {
   float *part;         // [splits][M][N]
 };
 
+// Epilogue of a workgroup's tile, half the rows at a time through LDS as fp32 [WA][BN], so that each
+// row's columns are read and written in whole lines (16 bytes of bf16 per lane): stored from the
+// accumulators' own layout, 32 bytes a row, the forward of 8192 x 4096 x 4096 with gelu, residual and
+// kept z took 324 us instead of 236.  16-byte chunk c of row r sits at place c ^ (r & 15): the 16 rows
+// of an accumulator store fall on 16 bank groups.  Every wave is done with the LDS when this begins.
+template <int HM, int HN, int WGM, int WGN, typename To, int ACT>
+MOE_DEV void tile_epilogue(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2][HM][HN], int wm, int wn,
+                           int m0, int n0, int split) {
+  constexpr int BM = 32 * HM * WGM, BN = 32 * HN * WGN, WA = BM / 2, WB = BN / 2;
+  const GemmArgs &p = q.g;
+  const int lane = threadIdx.x & 63;
+  auto chunk = [&](int r, int c) __attribute__((always_inline)) {
+    return (f32x4 *)(lds + r * (BN * 4) + ((c ^ (r & 15)) << 4));
+  };
+  constexpr int LPR = BN / 8, RPP = 512 / LPR;  // lanes per row, rows per pass of the workgroup
+  const bool part = q.splits > 1;
+  float *const pout = q.part + (int64_t)split * p.M * p.N;
+#pragma unroll
+  for (int mh = 0; mh < 2; ++mh) {
+    __syncthreads();
+    // lane l of a 16 x 16 block: row l & 15, columns 4 (l >> 4) .. +3
+#pragma unroll
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int nh = 0; nh < 2; ++nh)
+#pragma unroll
+        for (int j = 0; j < HN; ++j)
+          *chunk(wm * 16 * HM + i * 16 + (lane & 15),
+                 (nh * WB + wn * 16 * HN + j * 16) / 4 + (lane >> 4)) = acc[mh][nh][i][j];
+    __syncthreads();
+    const int r0 = threadIdx.x / LPR, c0 = (threadIdx.x % LPR) * 8;
+    if (p.vec) {
+      if (n0 + c0 >= p.N) continue;
+      f32x4 b[2] = {};
+      if (p.bias && !part) {
+        b[0] = get4((const bf16_t *)p.bias + n0 + c0);
+        b[1] = get4((const bf16_t *)p.bias + n0 + c0 + 4);
+      }
+#pragma unroll 4
+      for (int r = r0; r < WA; r += RPP) {
+        const int m = m0 + mh * WA + r;
+        if (m >= p.M) break;
+        const int64_t at = (int64_t)m * p.N + n0 + c0;
+        f32x4 v[2] = {*chunk(r, c0 / 4), *chunk(r, c0 / 4 + 1)};
+        if (part) {
+          put8(pout + at, v);
+          continue;
+        }
+        v[0] += b[0];
+        v[1] += b[1];
+        finish8<bf16_t, To, ACT>(p, v, at);
+      }
+    } else {
+      for (int r = r0; r < WA; r += RPP) {
+        const int m = m0 + mh * WA + r;
+        if (m >= p.M) break;
+        for (int c = threadIdx.x % LPR; c < BN && n0 + c < p.N; c += LPR) {
+          const int64_t at = (int64_t)m * p.N + n0 + c;
+          const float v = ((const float *)chunk(r, c >> 2))[c & 3];
+          if (part)
+            pout[at] = v;
+          else
+            finish1<bf16_t, To, ACT>(p, v + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
+        }
+      }
+    }
+  }
+}
+
 template <int HM, int HN, int WGM, int WGN, bool AK, bool BKM, typename To, int ACT>
-__global__ __launch_bounds__(512, HM * HN >= 4 ? 2 : 4) void piped_gemm(PipeArgs q) {
+__global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
   constexpr int BM = 32 * HM * WGM, BN = 32 * HN * WGN, WA = BM / 2, WB = BN / 2;
   constexpr int AH = WA * 128, BH = WB * 128, STG = 2 * (AH + BH);
   constexpr int PA = HalfTile<WA, AK>::PER, PB = HalfTile<WB, BKM>::PER;
@@ -528,66 +595,95 @@ __global__ __launch_bounds__(512, HM * HN >= 4 ? 2 : 4) void piped_gemm(PipeArgs
   // zeros for stages that are not there, and the last early read, before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 
-  // Epilogue, half the rows at a time through LDS as fp32 [WA][BN], so that each row's columns are
-  // read and written in whole lines (16 bytes of bf16 per lane): stored from the accumulators'
-  // own layout, 32 bytes a row, the same case took 324 us.  16-byte chunk c of row r sits at place
-  // c ^ (r & 15): the 16 rows of an accumulator store fall on 16 bank groups.
-  auto chunk = [&](int r, int c) __attribute__((always_inline)) {
-    return (f32x4 *)(lds + r * (BN * 4) + ((c ^ (r & 15)) << 4));
+  tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
+}
+
+// The same product with 128 x 128 tiles for problems whose 256-wide tiles leave CUs idle: 8 waves of
+// 64 x 32 outputs, NST stages in a ring, one barrier per stage.  A stage is two 32-deep steps; each
+// step's fragments are read while the step before multiplies.  The barrier between them also frees
+// the stage's place (its reads are waited for just before) for the stage NST ahead.
+//   NST = 4 (128 KB of LDS, one workgroup per CU) when there are at most as many workgroups as CUs: then
+//           the bytes in flight are the limit; NST = 2 (64 KB, two per CU) otherwise.
+template <int NST, bool AK, bool BKM, typename To, int ACT>
+__global__ __launch_bounds__(512, NST == 2 ? 4 : 2) void ring_gemm(PipeArgs q) {
+  constexpr int HM = 2, HN = 1, WGM = 2, WGN = 4, W = 128, OPB = W * 128, STG = 2 * OPB;
+  using TA = HalfTile<W, AK>;
+  using TB = HalfTile<W, BKM>;
+  constexpr int D = TA::PER + TB::PER;  // loads per thread and stage
+  extern __shared__ __align__(16) char lds[];
+  const GemmArgs &p = q.g;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wid % WGM, wn = wid / WGM;
+  const int tiles = q.tm * q.tn;
+  const int split = blockIdx.x / tiles;
+  int mb, nb;
+  tile_of(blockIdx.x - split * tiles, tiles, q.tm, q.tn, mb, nb);
+  const int m0 = mb * W, n0 = nb * W;
+  const int stages = (p.K + PBK - 1) / PBK;
+  const int kb = (int)((int64_t)stages * split / q.splits), ke = (int)((int64_t)stages * (split + 1) / q.splits);
+  const int kend = min(p.K, ke * PBK);
+  TA ta;
+  TB tb;
+  ta.setup(m0, p.M, p.lda);
+  tb.setup(n0, p.N, p.ldb);
+  const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(p.A, q.a_bytes), rb = uniform_rsrc(p.B, q.b_bytes);
+  const uint32_t lda2 = (uint32_t)(2 * p.lda), ldb2 = (uint32_t)(2 * p.ldb);
+  const uint32_t l0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(LDS_AS char *)lds) + wid * 1024;
+  f32x4 acc[2][2][HM][HN] = {};
+  bf16x8_t fa[2][2][HM], fb[2][2][HN];  // [step][half]
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t at = l0 + ((kt - kb) & (NST - 1)) * STG;
+    ta.issue(ra, 0, kt, kend, lda2, at);
+    tb.issue(rb, 0, kt, kend, ldb2, at + OPB);
   };
-  constexpr int LPR = BN / 8, RPP = 512 / LPR;  // lanes per row, rows per pass of the workgroup
-  const bool part = q.splits > 1;
-  float *const pout = q.part + (int64_t)split * p.M * p.N;
+  auto read = [&](int kt, int s) __attribute__((always_inline)) {
+    const char *t = lds + ((kt - kb) & (NST - 1)) * STG;
 #pragma unroll
-  for (int mh = 0; mh < 2; ++mh) {
-    __syncthreads();
-    // lane l of a 16 x 16 block: row l & 15, columns 4 (l >> 4) .. +3
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < HM; ++i)
+      for (int i = 0; i < HM; ++i) fa[s][h][i] = frag<W, AK>(t, h * 64 + wm * 16 * HM + i * 16, s, lane);
+#pragma unroll
+      for (int j = 0; j < HN; ++j) fb[s][h][j] = frag<W, BKM>(t + OPB, h * 64 + wn * 16 * HN + j * 16, s, lane);
+    }
+  };
+  auto multiply = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int mh = 0; mh < 2; ++mh)
 #pragma unroll
       for (int nh = 0; nh < 2; ++nh)
 #pragma unroll
-        for (int j = 0; j < HN; ++j)
-          *chunk(wm * 16 * HM + i * 16 + (lane & 15),
-                 (nh * WB + wn * 16 * HN + j * 16) / 4 + (lane >> 4)) = acc[mh][nh][i][j];
-    __syncthreads();
-    const int r0 = threadIdx.x / LPR, c0 = (threadIdx.x % LPR) * 8;
-    if (p.vec) {
-      if (n0 + c0 >= p.N) continue;
-      f32x4 b[2] = {};
-      if (p.bias && !part) {
-        b[0] = get4((const bf16_t *)p.bias + n0 + c0);
-        b[1] = get4((const bf16_t *)p.bias + n0 + c0 + 4);
-      }
-#pragma unroll 4
-      for (int r = r0; r < WA; r += RPP) {
-        const int m = m0 + mh * WA + r;
-        if (m >= p.M) break;
-        const int64_t at = (int64_t)m * p.N + n0 + c0;
-        f32x4 v[2] = {*chunk(r, c0 / 4), *chunk(r, c0 / 4 + 1)};
-        if (part) {
-          put8(pout + at, v);
-          continue;
-        }
-        v[0] += b[0];
-        v[1] += b[1];
-        finish8<bf16_t, To, ACT>(p, v, at);
-      }
-    } else {
-      for (int r = r0; r < WA; r += RPP) {
-        const int m = m0 + mh * WA + r;
-        if (m >= p.M) break;
-        for (int c = threadIdx.x % LPR; c < BN && n0 + c < p.N; c += LPR) {
-          const int64_t at = (int64_t)m * p.N + n0 + c;
-          const float v = ((const float *)chunk(r, c >> 2))[c & 3];
-          if (part)
-            pout[at] = v;
-          else
-            finish1<bf16_t, To, ACT>(p, v + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
-        }
-      }
-    }
+        for (int i = 0; i < HM; ++i)
+#pragma unroll
+          for (int j = 0; j < HN; ++j)
+            acc[mh][nh][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[s][nh][j], fa[s][mh][i],
+                                                                        acc[mh][nh][i][j], 0, 0, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < NST; ++i) issue(kb + i);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * D) : "memory");
+  LIN_FENCE();
+  __builtin_amdgcn_s_barrier();
+  LIN_FENCE();
+  read(kb, 0);
+  for (int kt = kb; kt < ke; ++kt) {
+    LIN_FENCE();
+    read(kt, 1);
+    LIN_FENCE();
+    multiply(0);
+    LIN_FENCE();
+    // stage kt + 1 has landed; this wave's reads of stage kt are done
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * D) : "memory");
+    LIN_FENCE();
+    __builtin_amdgcn_s_barrier();
+    LIN_FENCE();
+    read(kt + 1, 0);
+    issue(kt + NST);
+    LIN_FENCE();
+    multiply(1);
   }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
 }
 
 // ---- streamed products: few rows or few columns --------------------------------
@@ -830,28 +926,42 @@ void by_act_of(int act, F &&f) {
     f(std::integral_constant<int, MOE_ACT_NONE>());
 }
 
-template <int HM, int HN, int WGM, int WGN, bool AK, bool BKM, typename To>
-hipError_t run_piped(PipeArgs &q, int act, hipStream_t st) {
-  constexpr int BM = 32 * HM * WGM, BN = 32 * HN * WGN, SMEM = 2 * 128 * (BM + BN);
-  q.tm = (q.g.M + BM - 1) / BM;
-  q.tn = (q.g.N + BN - 1) / BN;
+constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};  // tile shapes
+
+// launch of a kernel with more LDS than the default allows; the attribute is set once per device
+template <auto KERNEL>
+hipError_t launch_lds(int grid, size_t smem, const PipeArgs &q, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute((const void *)KERNEL, hipFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != hipSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  KERNEL<<<grid, 512, smem, st>>>(q);
+  return hipGetLastError();
+}
+
+template <bool AK, bool BKM, typename To>
+hipError_t run_piped(PipeArgs &q, int shape, int act, hipStream_t st) {
+  const int bm = kShapeM[shape], bn = kShapeN[shape];
+  q.tm = (q.g.M + bm - 1) / bm;
+  q.tn = (q.g.N + bn - 1) / bn;
   const int grid = q.tm * q.tn * q.splits;
   hipError_t e = hipSuccess;
   by_act_of<AK && BKM>(act, [&](auto A) {
-    auto k = piped_gemm<HM, HN, WGM, WGN, AK, BKM, To, decltype(A)::value>;
-    // once per device (the attribute is the function's on that device)
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    e = hipGetDevice(&dev);
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (e == hipSuccess && !(done.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-      if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    }
-    if (e == hipSuccess) {
-      k<<<grid, 512, SMEM, st>>>(q);
-      e = hipGetLastError();
-    }
+    constexpr int ACT = decltype(A)::value;
+    if (shape == 0)
+      e = launch_lds<piped_gemm<4, 2, 2, 4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
+    else if (shape == 1)
+      e = launch_lds<piped_gemm<2, 2, 4, 2, AK, BKM, To, ACT>>(grid, 96 << 10, q, st);
+    else if (grid <= device_cu_count())
+      e = launch_lds<ring_gemm<4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
+    else
+      e = launch_lds<ring_gemm<2, AK, BKM, To, ACT>>(grid, 64 << 10, q, st);
   });
   return e;
 }
@@ -860,17 +970,15 @@ hipError_t run_piped(PipeArgs &q, int act, hipStream_t st) {
 struct Plan {
   int shape, splits;  // shape: 0 = 256 x 256, 1 = 256 x 128, 2 = 128 x 128
 };
-constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};
 
 // The choice minimises an estimate in us: rounds of workgroups over the chip (256 CUs; two 128 x 128
 // workgroups fit one) times the stages of a range at the shape's measured time per stage, 6 us of
-// launch, first loads and epilogue, and for split reductions the join: a launch and the partial
-// products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 (8192 x 4096 x 4096: 198 us, the
-// others 240 and 252), 256 x 128 0.92 (4096 x 2048 x 2048: 38 us, 256 x 256 49), 128 x 128 0.55
-// alone on a CU and 1.0 in pairs (2048^3: 25 us, the others 44 and 32).
+// launch, first loads and epilogue, and for split reductions the join: a launch, and the partial
+// products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 us, 256 x 128 0.92, 128 x 128 0.5
+// alone on a CU and 1.0 in pairs.  Measured, us (256 x 256 / 256 x 128 / 128 x 128 / the last in two
+// ranges): 8192 x 4096 x 4096 198 / 240 / 252 / 389, 4096 x 2048 x 2048 47 / 35 / 38 / 60, 2048^3 43 / 31 /
+// 24 / 35, 512 x 4096 x 4096 74 / 51 / 33 / 31, 64 x 4096 x 4096 71 / 49 / 30 / 21 (four ranges 15.5).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  static const char *force = getenv("LIN_PLAN");
-  if (force) return Plan{force[0] - '0', atoi(force + 2)};
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t stages = (K + PBK - 1) / PBK;
   Plan best{0, 1};
@@ -882,7 +990,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
       const double wgs = tiles * k, per = (double)((stages + k - 1) / k);
       double t;
       if (sh == 2)
-        t = wgs <= 256 ? per * 0.55 : __builtin_ceil(wgs / 512) * per * 1.0;
+        t = wgs <= 256 ? per * 0.5 : __builtin_ceil(wgs / 512) * per * 1.0;
       else
         t = __builtin_ceil(wgs / 256) * per * (sh == 0 ? 1.35 : 0.92);
       t += 6;
@@ -914,9 +1022,11 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K, bool bf16) {
   return k > 1 ? (size_t)k * M * N * 4 : 0;
 }
 
-// Whether the forward streams: x or W has at most 64 rows, and rows on 16-byte lines.
+// Whether the forward streams: x or W has at most 16 rows, and rows on 16-byte lines.  (Up to 64 rows,
+// as 32 x 64 tiles, the fragments of the smaller operand out of L2 are the limit: 8192 x 4096 x 64 took
+// 26 us, as split 128 x 128 tiles 16 and 3 for the join.)
 bool streams(const GemmArgs &a, size_t es) {
-  return (a.M <= 64 || a.N <= 64) && a.K % (int)(16 / es) == 0 && a.K <= (1 << 22) && on_line(a.A, 16) &&
+  return (a.M <= 16 || a.N <= 16) && a.K % (int)(16 / es) == 0 && a.K <= (1 << 22) && on_line(a.A, 16) &&
          on_line(a.B, 16);
 }
 
@@ -953,9 +1063,7 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
         });
         return hipGetLastError();
       }
-      if (a.M <= 16 || a.N <= 16) return run_stream<T, To, 1, 1, 16, 4>(a, act, st);
-      if (a.M <= a.N) return run_stream<T, To, 4, 2, 8, 2>(a, act, st);
-      return run_stream<T, To, 2, 4, 8, 2>(a, act, st);
+      return run_stream<T, To, 1, 1, 16, 4>(a, act, st);
     }
   }
   a.vec = a.N % 8 == 0 && on_line(a.out, 16) && on_line(a.res, 16) && on_line(a.bias, 16) &&
@@ -971,9 +1079,7 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
     if (chunks && small && a.K > 0) {
       const Plan pl = plan_of(a.M, a.N, a.K);
       PipeArgs q{a, (uint32_t)ab, (uint32_t)bb, 0, 0, pl.splits, (float *)part};
-      const hipError_t e = pl.shape == 0   ? run_piped<4, 2, 2, 4, AK, BKM, To>(q, act, st)
-                           : pl.shape == 1 ? run_piped<2, 2, 4, 2, AK, BKM, To>(q, act, st)
-                                           : run_piped<2, 1, 2, 4, AK, BKM, To>(q, act, st);
+      const hipError_t e = run_piped<AK, BKM, To>(q, pl.shape, act, st);
       if (e != hipSuccess || pl.splits == 1) return e;
       return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
     }
