@@ -455,7 +455,8 @@ int moe_router_loss_bwd(const float *d_losses, const void *logits, const float *
  *   `dtype`; residual [M, N] or NULL and out [M, N] in `out_dtype`, which may
  *   be the same buffer.  dtype MOE_F32 -> out_dtype MOE_F32; dtype MOE_BF16 ->
  *   MOE_BF16 or MOE_F32.  Element alignment; any sizes (bf16 runs fastest with
- *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0.
+ *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0; K and N are
+ *   at most 2^22.  Tensors of any size (64-bit addresses).
  *   workspace: moe_linear_fwd_workspace_bytes(...) bytes, 256-byte aligned
  *   (may be NULL when that is 0).
  */

@@ -632,6 +632,7 @@ int check_route(int64_t T, int32_t E, int32_t k, int32_t score, int32_t dtype) {
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_OPTION;
   return MOE_OK;
 }
+constexpr int64_t kMaxWidth = 1 << 22;  // linear layer: K and N
 bool scale_ok(float s) { return isfinite(s) && s > 0.f; }
 
 int check_linear(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype, int32_t out_dtype) {
@@ -639,8 +640,8 @@ int check_linear(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype, in
                        : dtype != MOE_BF16 || (out_dtype != MOE_F32 && out_dtype != MOE_BF16))
     return MOE_ERR_DTYPE;
   if (M < 0 || K < 1 || N < 1) return MOE_ERR_SHAPE;
-  // tile indices are 32-bit, with room for a partial tile
-  if (M >= kMax32 - 512 || K >= kMax32 - 512 || N >= kMax32 - 512) return MOE_ERR_LIMIT;
+  // row indices are 32-bit, with room for a partial tile; offsets inside a tile of 128 rows too
+  if (M >= kMax32 - 512 || K > kMaxWidth || N > kMaxWidth) return MOE_ERR_LIMIT;
   if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return MOE_ERR_OPTION;
   return MOE_OK;
 }

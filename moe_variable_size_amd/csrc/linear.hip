@@ -100,6 +100,15 @@ struct GemmArgs {
   bool vec;          // N a multiple of 8; out, z, residual and bias on 16-byte lines
 };
 
+// buffer resource from wave-uniform values, in scalar registers
+MOE_DEV __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return make_rsrc((const void *)(uintptr_t)(((uint64_t)hi << 32) | lo),
+                   __builtin_amdgcn_readfirstlane(bytes));
+}
+
 // ---- epilogue -----------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
@@ -188,15 +197,27 @@ MOE_DEV void stage_at(int i, int &r, int &k) {
   r = KMAJ ? i * 8 + (t >> 5) : t % (64 * S);
   k = KMAJ ? t & 31 : i * (4 / S) + t / (64 * S);
 }
+template <typename T>
+MOE_DEV T buf_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+  else
+    return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+}
+// p: the operand at the tile's first row (column) and the range's reduction element k0; rows: of the
+// operand from there on.  Rows past the end are past the buffer's range; the other direction is checked.
 template <typename T, int S, bool KMAJ>
-MOE_DEV void stage_load(const T *p, int64_t ld, int r0, int rows, int k0, int K, T (&v)[8 * S]) {
+MOE_DEV void stage_load(const T *p, int64_t ld, int rows, int left, T (&v)[8 * S]) {
+  const uint32_t es = sizeof(T);
+  const int n = KMAJ ? min(rows, 64 * S) : min(left, SBK);  // memory rows of the tile
+  const __amdgpu_buffer_rsrc_t r = uniform_rsrc(p, n > 0 ? ((uint32_t)(n - 1) * (uint32_t)ld + (KMAJ ? left : rows)) * es : 0u);
 #pragma unroll
   for (int i = 0; i < 8 * S; ++i) {
-    int r, k;
-    stage_at<S, KMAJ>(i, r, k);
-    const bool ok = r0 + r < rows && k0 + k < K;
-    const int64_t at = KMAJ ? (int64_t)(r0 + r) * ld + k0 + k : (int64_t)(k0 + k) * ld + r0 + r;
-    v[i] = ok ? p[at] : (T)0;
+    int row, k;
+    stage_at<S, KMAJ>(i, row, k);
+    const bool ok = KMAJ ? k < left : row < rows;
+    const uint32_t off = (uint32_t)(KMAJ ? row : k) * (uint32_t)ld + (KMAJ ? k : row);
+    v[i] = buf_load<T>(r, ok ? off * es : kOobOffset);
   }
 }
 template <typename T, int S, bool KMAJ>
@@ -227,17 +248,19 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
   const int ke = min(p.K, (int)((int64_t)steps * (split + 1) / splits) * SBK);
   f32x16 acc[S][S] = {};
   T va[8 * S], vb[8 * S];
-  stage_load<T, S, AK>((const T *)p.A, p.lda, m0, p.M, kb, ke, va);
-  stage_load<T, S, BKM>((const T *)p.B, p.ldb, n0, p.N, kb, ke, vb);
+  auto load = [&](int k0) __attribute__((always_inline)) {
+    const T *a = (const T *)p.A + (AK ? (int64_t)m0 * p.lda + k0 : (int64_t)k0 * p.lda + m0);
+    const T *b = (const T *)p.B + (BKM ? (int64_t)n0 * p.ldb + k0 : (int64_t)k0 * p.ldb + n0);
+    stage_load<T, S, AK>(a, p.lda, p.M - m0, ke - k0, va);
+    stage_load<T, S, BKM>(b, p.ldb, p.N - n0, ke - k0, vb);
+  };
+  load(kb);
   for (int k0 = kb; k0 < ke; k0 += SBK) {
     __syncthreads();
     stage_store<T, S, AK>(As, va);
     stage_store<T, S, BKM>(Bs, vb);
     __syncthreads();
-    if (k0 + SBK < ke) {
-      stage_load<T, S, AK>((const T *)p.A, p.lda, m0, p.M, k0 + SBK, ke, va);
-      stage_load<T, S, BKM>((const T *)p.B, p.ldb, n0, p.N, k0 + SBK, ke, vb);
-    }
+    if (k0 + SBK < ke) load(k0 + SBK);
     const int r = lane & 31, h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -323,13 +346,6 @@ MOE_DEV void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds) {
                :
                : "s"(m0v), "v"(voff), "s"(rsrc)
                : "memory", "m0");
-}
-MOE_DEV __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
-  const uint64_t a = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return make_rsrc((const void *)(uintptr_t)(((uint64_t)hi << 32) | lo),
-                   __builtin_amdgcn_readfirstlane(bytes));
 }
 #define LIN_FENCE() __builtin_amdgcn_sched_barrier(0)
 

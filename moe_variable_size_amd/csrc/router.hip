@@ -51,6 +51,10 @@ template <int CTRL>
 MOE_DEV uint32_t dpp(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
 }
+template <int CTRL>
+MOE_DEV int64_t dpp64(int64_t x) {
+  return (int64_t)(((uint64_t)dpp<CTRL>((uint32_t)((uint64_t)x >> 32)) << 32) | dpp<CTRL>((uint32_t)x));
+}
 template <int LPR, class Op>
 MOE_DEV uint32_t row_reduce(uint32_t v, Op op) {
   v = op(v, dpp<0xB1>(v));
@@ -230,6 +234,7 @@ MOE_DEV int choose_exact(const RouteArgs &p, const T *row, int64_t *lds, int lan
     int64_t gk = kBarred;
     if (lane < p.G) {
       int64_t a = kBarred, b = kBarred;  // the two best
+#pragma unroll 8
       for (int j = 0; j < per; ++j) {
         const int64_t v = keys[lane * per + j];
         if (v > a) { b = a; a = v; } else if (v > b) b = v;
@@ -259,12 +264,15 @@ MOE_DEV int choose_exact(const RouteArgs &p, const T *row, int64_t *lds, int lan
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (key[i] > best) { best = key[i]; at = i * 64 + lane; }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const int64_t ok = __shfl_xor(best, d, kWave);
-      const int oa = __shfl_xor(at, d, kWave);
+    auto take = [&](int64_t ok, int oa) __attribute__((always_inline)) {
       if (ok > best || (ok == best && oa < at)) { best = ok; at = oa; }
-    }
+    };
+    take(dpp64<0xB1>(best), (int)dpp<0xB1>(at));
+    take(dpp64<0x4E>(best), (int)dpp<0x4E>(at));
+    take(dpp64<0x141>(best), (int)dpp<0x141>(at));
+    take(dpp64<0x140>(best), (int)dpp<0x140>(at));
+    take(__shfl_xor(best, 16, kWave), __shfl_xor(at, 16, kWave));
+    take(__shfl_xor(best, 32, kWave), __shfl_xor(at, 32, kWave));
     if (best == kBarred) break;
     if (lane == j) id = at;
 #pragma unroll
@@ -534,7 +542,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       uint32_t next = __shfl_down(won, 1, LPR);
       if (sub == p.k - 1) next = left;
       const float hi = key32_value(won), lo = key32_value(next);
-      doubt |= sub < p.k && next > kBarred32 && !(hi - lo > err + (fabsf(hi) + fabsf(lo)) * 0x1p-23f);
+      doubt |= sub < p.k && next > kBarred32 && !(hi - lo > err + (fabsf(hi) + fabsf(lo)) * 0x1p-24f);
     }
     // every lane of a row has the same doubt
     doubt = row_umax<LPR>(doubt) != 0u;
@@ -632,7 +640,7 @@ __global__ __launch_bounds__(NT) void route_bwd_kernel(RouteBwdArgs p) {
 // Forward: every block sums its rows' probabilities and counts its ids per
 // expert, and its rows' squared log-sum-exps; one block joins the partial sums in
 // a fixed order.  Workspace: [blocks][2 E + 2] words: sums, counts, z, rows.
-constexpr int kLossBlocks = 128;   // partial sums that one workgroup then reads (E = 128: 132 KB)
+constexpr int kLossBlocks = 256;   // partial sums that one workgroup then reads (E = 128: 264 KB)
 constexpr int LT = 1024, LW = LT / kWave;
 
 struct LossArgs {

@@ -164,7 +164,8 @@ def test_linear_refuses(lib):
         return lib.moe_linear_fwd(x, W, b, r, out, z, M, K, N, act, dt, odt, ws, nb, None)
     for kw, code in ((dict(x=None), NULL), (dict(W=None), NULL), (dict(out=None), NULL),
                      (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(N=0), SHAPE),
-                     (dict(M=1 << 31), LIMIT), (dict(act=5), OPTION), (dict(act=-1), OPTION),
+                     (dict(M=1 << 31), LIMIT), (dict(K=(1 << 22) + 1), LIMIT),
+                     (dict(N=(1 << 22) + 1), LIMIT), (dict(act=5), OPTION), (dict(act=-1), OPTION),
                      (dict(dt=0, odt=1), DTYPE), (dict(dt=2), DTYPE), (dict(odt=2), DTYPE),
                      (dict(x=ODD), ALIGN), (dict(b=ODD), ALIGN), (dict(r=ODD), ALIGN),
                      (dict(z=ODD), ALIGN), (dict(out=ODD), ALIGN), (dict(M=0, x=None, out=None), 0)):
