@@ -465,7 +465,7 @@ def _launch(t: torch.Tensor, stream=None):
     index = t.get_device()
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
-        return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(index)), raw
+        return (_HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)), raw
     if stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return torch.cuda.stream(stream), stream.cuda_stream

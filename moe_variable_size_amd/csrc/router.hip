@@ -639,7 +639,8 @@ __global__ __launch_bounds__(NT) void route_bwd_kernel(RouteBwdArgs p) {
 // ---- losses --------------------------------------------------------------------
 // Forward: every block sums its rows' probabilities and counts its ids per
 // expert, and its rows' squared log-sum-exps; one block joins the partial sums in
-// a fixed order.  Workspace: [blocks][2 E + 2] words: sums, counts, z, rows.
+// a fixed order.  Workspace: [blocks][sums, counts], E of each padded to a multiple of 4, then
+// [blocks][sum of squared log-sum-exps, rows].
 constexpr int kLossBlocks = 256;   // partial sums that one workgroup then reads (E = 128: 264 KB)
 constexpr int LT = 1024, LW = LT / kWave;
 
@@ -743,80 +744,104 @@ __global__ __launch_bounds__(LT) void loss_fwd_kernel(LossArgs p) {
   }
   if (lane == 0) { zs[wid] = z; rs[wid] = rows; }
   __syncthreads();
-  float *part = p.part + (size_t)blockIdx.x * (2 * p.E + 2);
-  for (int e = threadIdx.x; e < p.E; e += LT) {
+  // this block's part: sums, then counts, each padded to a multiple of 4
+  const int pad = (p.E + 3) & ~3;
+  float *part = p.part + (size_t)blockIdx.x * 2 * pad;
+  for (int e = threadIdx.x; e < pad; e += LT) {
     float v = 0.f;
+    if (e < p.E)
 #pragma unroll
-    for (int w = 0; w < LW; ++w) v += psum[w][e];
+      for (int w = 0; w < LW; ++w) v += psum[w][e];
     part[e] = v;
-    part[p.E + e] = __int_as_float(cnt[e]);
+    part[pad + e] = __int_as_float(e < p.E ? cnt[e] : 0);
   }
   if (threadIdx.x == 0) {
     float v = 0.f;
     int r = 0;
     for (int w = 0; w < LW; ++w) { v += zs[w]; r += rs[w]; }
-    part[2 * p.E] = v;
-    part[2 * p.E + 1] = __int_as_float(r);
+    float *tail = p.part + (size_t)gridDim.x * 2 * pad + 2 * blockIdx.x;
+    tail[0] = v;
+    tail[1] = __int_as_float(r);
   }
 }
 
-// Sum over the block of a value per thread, in a fixed order.
-template <typename S>
-MOE_DEV S block_sum(S v, S *red) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, kWave);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+// Sums over the block of two values per thread, in a fixed order.
+MOE_DEV void block_sums(double &x, double &y, double *red) {
+  x = wave_sum(x);
+  y = wave_sum(y);
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (lane == 0) {
+    red[w] = x;
+    red[LW + w] = y;
+  }
   __syncthreads();
-  S s = red[0];
+  x = red[lane & (LW - 1)];
+  y = red[LW + (lane & (LW - 1))];
 #pragma unroll
-  for (int w = 1; w < LW; ++w) s += red[w];
+  for (int d = LW / 2; d; d >>= 1) {
+    x += __shfl_xor(x, d, kWave);
+    y += __shfl_xor(y, d, kWave);
+  }
   __syncthreads();
-  return s;
 }
 
-// One workgroup joins the blocks' parts: W = the power of two from E up (at least 64) threads side by
-// side per expert, the LT / W others of a column take every (LT / W)-th part.
+// One workgroup joins the blocks' parts, 16 bytes per load: W threads (the power of two from a part's
+// words / 4 up) side by side on a part, the LT / W others take every (LT / W)-th part; then a tree over
+// those.  In 64 bits (the counts too, which it holds exactly).
 __global__ __launch_bounds__(LT) void loss_join_kernel(LossArgs p) {
-  __shared__ double psum[LT];
-  __shared__ int csum[LT];
-  __shared__ double dred[LW];
-  __shared__ long long ired[LW];
-  const int tid = threadIdx.x, pitch = 2 * p.E + 2;
-  int W = 64;
-  while (W < p.E) W <<= 1;
-  const int e = tid & (W - 1), q = tid / W, Q = LT / W;
-  double P = 0.0, z = 0.0;
-  int c = 0;
-  long long r = 0;
-  if (e < p.E) {
-#pragma unroll 8
-    for (int b = q; b < p.blocks; b += Q) {
-      P += p.part[(size_t)b * pitch + e];
-      c += __float_as_int(p.part[(size_t)b * pitch + p.E + e]);
+  typedef double f64x4 __attribute__((ext_vector_type(4)));
+  __shared__ f64x4 sums[LT];
+  __shared__ double red[2 * LW];
+  const int tid = threadIdx.x, pad = (p.E + 3) & ~3, words = pad / 2;  // 16-byte words of a part
+  int W = 1;
+  while (W < words) W <<= 1;
+  const int c = tid & (W - 1), q = tid / W, Q = LT / W;
+  f64x4 acc = {};
+  if (c < words) {
+    const f32x4 *src = (const f32x4 *)p.part + c;
+    // 8 loads in flight (past the last part: the last one again, not added)
+    for (int b0 = q; b0 < p.blocks; b0 += 8 * Q) {
+      f32x4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = src[(size_t)min(b0 + j * Q, p.blocks - 1) * words];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double x = c < pad / 4 ? (double)v[j][i] : (double)__float_as_int(v[j][i]);
+          acc[i] += b0 + j * Q < p.blocks ? x : 0.0;
+        }
     }
   }
+  double z = 0.0, r = 0.0;
   if (tid < p.blocks) {
-    z = p.part[(size_t)tid * pitch + 2 * p.E];
-    r = __float_as_int(p.part[(size_t)tid * pitch + 2 * p.E + 1]);
+    const float *tail = p.part + (size_t)p.blocks * 2 * pad + 2 * tid;
+    z = tail[0];
+    r = (double)__float_as_int(tail[1]);
   }
-  psum[tid] = P;
-  csum[tid] = c;
-  __syncthreads();
-  if (q == 0)
-    for (int i = 1; i < Q; ++i) {
-      P += psum[i * W + e];
-      c += csum[i * W + e];
+  sums[tid] = acc;
+  for (int d = Q / 2; d; d >>= 1) {
+    __syncthreads();
+    if (q < d) {
+      acc += sums[tid + d * W];
+      sums[tid] = acc;
     }
-  const bool mine = q == 0 && e < p.E;
-  const long long C = block_sum<long long>(mine ? c : 0, ired), N = block_sum<long long>(r, ired);
-  const double inv = N > 0 ? 1.0 / (double)N : 0.0;
-  const float f = C > 0 ? (float)((double)p.E * (double)c / (double)C) : 0.f;
-  if (mine) p.stats[e] = f;
-  const double bal = block_sum<double>(mine ? (double)f * P : 0.0, dred), zz = block_sum<double>(z, dred);
+  }
+  __syncthreads();
+  const double *flat = (const double *)sums;  // [pad] sums, [pad] counts
+  const bool mine = tid < p.E;
+  const double P = mine ? flat[tid] : 0.0, n = mine ? flat[pad + tid] : 0.0;
+  double C = n;
+  block_sums(C, r, red);
+  const double inv = r > 0.0 ? 1.0 / r : 0.0;
+  const float f = C > 0.0 ? (float)((double)p.E * n / C) : 0.f;
+  if (mine) p.stats[tid] = f;
+  double bal = (double)f * P;
+  block_sums(bal, z, red);
   if (tid == 0) {
     p.stats[p.E] = (float)inv;
     p.losses[0] = (float)(bal * inv);
-    p.losses[1] = (float)(zz * inv);
+    p.losses[1] = (float)(z * inv);
   }
 }
 static_assert(kLossBlocks <= LT, "a thread per part");
@@ -928,7 +953,7 @@ static int loss_blocks(int64_t T, int E) {
 }
 
 size_t loss_workspace_bytes(int64_t T, int E) {
-  return (size_t)loss_blocks(T, E) * (2 * (size_t)E + 2) * sizeof(float);
+  return (size_t)loss_blocks(T, E) * (2 * (size_t)((E + 3) & ~3) + 2) * sizeof(float);
 }
 
 hipError_t launch_loss_fwd(const void *logits, const int32_t *ids, int64_t T, int E, int k,
