@@ -288,3 +288,54 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, w in zip(got, want):
             assert torch.equal(a, w)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_sweep(seed):
+    """Sizes around the rules that pick a kernel, both directions."""
+    rng = np.random.default_rng(500 + seed)
+    M = int(rng.choice([1, 3, 4, 5, 15, 16, 17, 63, 65, 120, 257, 400, 1100]))
+    N = int(rng.choice([1, 8, 15, 16, 24, 64, 100, 128, 250, 256, 520, 1096]))
+    K = int(rng.choice([1, 8, 30, 64, 72, 127, 192, 500, 1032, 2056]))
+    dtype = ["bf16", "f32"][seed % 4 == 3]
+    out = "f32" if dtype == "f32" or rng.random() < 0.4 else "bf16"
+    act = ACTS[int(rng.integers(5))]
+    _check_fwd(M, K, N, dtype, out, act=act, bias=bool(rng.integers(2)), residual=bool(rng.integers(2)), seed=seed)
+    _check_bwd(M, K, N, dtype, out, act=act, seed=seed)
+
+
+def _rows_close(got, x, W, rows):
+    xf = x[rows].double().cpu().numpy()
+    ref = xf @ W.double().cpu().numpy().T
+    t = _sum_tol(xf, W.double().cpu().numpy().T, x.shape[1])
+    ok = np.abs(host(got[rows]) - ref) <= t + U * np.abs(ref)
+    assert ok.all()
+
+
+def test_output_past_four_gigabytes():
+    M, K, N = 66000, 64, 16384 + 8
+    x = torch.randn((M, K), device="cuda").bfloat16()
+    W = (torch.randn((N, K), device="cuda") * 0.1).bfloat16()
+    o = api.moe_linear_fwd(x, W, out_dtype=torch.float32)
+    assert o.numel() * 4 > 1 << 32
+    _rows_close(o, x, W, [0, 1, 33000, M - 257, M - 1])
+
+
+@pytest.mark.parametrize("N", [8, 72])
+def test_input_past_two_gigabytes(N):
+    """x of more than 2^31 bytes: streamed (N = 8) and staged (N = 72); and its backward,
+    where it is the operand read across its rows."""
+    M, K = 270000, 4096
+    x = torch.empty((M, K), device="cuda", dtype=torch.bfloat16).normal_()
+    assert x.numel() * 2 > 1 << 31
+    W = (torch.randn((N, K), device="cuda") / 64).bfloat16()
+    o = api.moe_linear_fwd(x, W, out_dtype=torch.float32)
+    _rows_close(o, x, W, [0, 1000, M - 130, M - 1])
+    d = torch.zeros((M, N), device="cuda", dtype=torch.bfloat16)
+    d[-3:] = 1.0
+    dX, dW, db = api.moe_linear_bwd(d, x, W)
+    ref = x[-3:].double().sum(0)
+    assert (dW.double() - ref).abs().max() <= V * ref.abs().max() + 1e-5
+    assert bool((db == 3).all()) and not bool(dX[: M - 3].any())
+    want = W.double().sum(0)
+    assert (dX[-1].double() - want).abs().max() <= V * want.abs().max() + 1e-5

@@ -399,3 +399,135 @@ def test_graph_replays_match_eager():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E,k", [(20, 64, 64), (11, 100, 40), (33, 200, 17), (6, 513, 16), (40, 17, 16),
+                                   (9, 256, 16), (5, 300, 32), (7, 300, 33)])
+def test_route_many_slots(T, E, k):
+    """More slots than the lanes that share a row, as many, and every expert chosen."""
+    l = _logits(T, E, "f32", T + k)
+    bias = np.random.default_rng(k).standard_normal(E).astype(np.float32) * 0.2
+    for score in ("softmax", "sigmoid"):
+        _check_route(l, k, "many", score=score)
+        _check_route(l, k, "many, bias", score=score, bias=bias)
+
+
+def test_bias_of_nan_and_infinity():
+    l = _logits(9, 48, "f32", 2)
+    bias = np.zeros(48, np.float32)
+    bias[[3, 30]] = np.nan
+    bias[7] = np.inf
+    bias[[0, 1, 47]] = -np.inf
+    for o in (dict(), dict(score="sigmoid"), dict(groups=6, topk_groups=3, group_score="top2"),
+              dict(score="sigmoid", groups=4, topk_groups=2)):
+        _check_route(l, 5, "bias", bias=bias, **o)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_route_sweep(seed):
+    rng = np.random.default_rng(1000 + seed)
+    E = int(rng.integers(2, 600))
+    groups = int(rng.choice([1, 1, 2, 3, 4, 8, 16]))
+    E = max(2, E // groups) * groups
+    keep = int(rng.integers(1, groups + 1))
+    k = int(rng.integers(1, min(64, keep * (E // groups)) + 1))
+    T = int(rng.integers(1, 90))
+    l = _logits(T, E, ["f32", "bf16"][seed % 2], seed, std=float(rng.choice([0.01, 1.0, 8.0])))
+    l[torch.from_numpy(rng.random((T, E)) < rng.choice([0.0, 0.3, 0.95]))] = -INF
+    bias = rng.standard_normal(E).astype(np.float32) * 0.1 if rng.random() < 0.6 else None
+    _check_route(l, k, f"sweep {seed}", score=str(rng.choice(["softmax", "sigmoid"])), bias=bias, groups=groups,
+                 topk_groups=keep, group_score=str(rng.choice(["max", "top2"])),
+                 renormalize=bool(rng.integers(2)), scale=float(rng.choice([1.0, 2.5])))
+
+
+def test_rows_past_two_gigabytes():
+    """Logits of more than 2^32 bytes: the last rows are routed, and their gradients and
+    losses formed, from their own place."""
+    T, E, k = (1 << 22) + 5, 260, 3
+    l = torch.zeros((T, E), device="cuda")
+    assert l.numel() * 4 > 1 << 32
+    tail = _logits(7, E, "f32", 4)
+    l[-7:] = tail.cuda()
+    ids, w = api.moe_route_fwd(l, k)
+    ri, rw = R.route(tail.numpy(), k)
+    assert np.array_equal(host(ids[-7:]), ri) and np.abs(host(w[-7:]) - rw).max() <= _rel(tail.numpy())
+    assert host(ids[:3]).tolist() == [[0, 1, 2]] * 3
+    g = torch.zeros((T, k), device="cuda")
+    g[-7:] = torch.randn((7, k), generator=torch.Generator().manual_seed(1)).cuda()
+    d = api.moe_route_bwd(g, l, ids, w)
+    ref = R.route_grad(tail.numpy(), ri, host(g[-7:]).astype(np.float64))
+    assert np.abs(host(d[-7:]) - ref).max() <= 4 * _rel(tail.numpy()) * np.abs(host(g[-7:])).max()
+    losses, stats = api.moe_router_loss_fwd(l, ids)
+    api.moe_router_loss_bwd(torch.tensor([0.0, 1.0], device="cuda") * T, l, stats, d_logits=d)
+    p = np.stack([R.softmax(r) for r in tail.numpy()])
+    m = tail.numpy().astype(np.float64).max(1, keepdims=True)
+    lse = m + np.log(np.exp(tail.numpy() - m).sum(1, keepdims=True))
+    assert np.abs(host(d[-7:]) - 2 * lse * p).max() <= 4 * _rel(tail.numpy()) * np.abs(2 * lse * p).max()
+
+
+def test_captured_forward_and_backward_of_the_sublayer():
+    """The differentiable calls captured with torch.autograd.grad, replayed over new
+    inputs, against the eager pass."""
+    T, K, N, E = 96, 64, 72, 8
+    g = torch.Generator().manual_seed(5)
+
+    def r(*s, std=1.0):
+        return (torch.randn(s, generator=g) * std).bfloat16().cuda()
+
+    x = r(T, K)
+    p = [r(E, K, std=K ** -0.5), r(E, std=0.1), r(E, N, K, std=K ** -0.5), r(N, K, std=K ** -0.5)]
+    p = [t.requires_grad_() for t in p]
+    bias = (torch.randn(E, generator=g) * 0.1).cuda()
+
+    def step():
+        y, losses, ids = _sublayer(x, *p, bias)
+        return (y.detach(), losses.detach()) + torch.autograd.grad(y.square().sum() + losses.sum(), p)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (6, 7, 8):
+        x.copy_(torch.randn((T, K), generator=torch.Generator().manual_seed(seed)).bfloat16())
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            # two atomic additions per output commute; sums of the losses are ordered
+            assert torch.allclose(a.float(), b.float(), rtol=2 ** -7, atol=1e-6)
+
+
+def test_refusals_of_the_router_binding():
+    l = torch.zeros((4, 8), device="cuda")
+    ids, w = api.moe_route_fwd(l, 2)
+    for kw in (dict(score="tanh"), dict(group_score="sum"), dict(bias=torch.zeros(7, device="cuda")),
+               dict(bias=torch.zeros(8)), dict(expert_ids=torch.zeros((4, 3), dtype=torch.int32, device="cuda")),
+               dict(topk_weights=torch.zeros((3, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            api.moe_route_fwd(l, 2, **kw)
+    for bad in (l.double(), l.half()):
+        with pytest.raises(TypeError):
+            api.moe_route_fwd(bad, 2)
+    with pytest.raises(ValueError):
+        api.moe_route_fwd(l.t(), 2)
+    for kw in (dict(groups=3), dict(groups=2, topk_groups=3), dict(scale=0.0)):
+        with pytest.raises(api._lib.MoeError):
+            api.moe_route_fwd(l, 2, **kw)
+    with pytest.raises(api._lib.MoeError):
+        api.moe_route_fwd(l, 9)
+    with pytest.raises(ValueError):
+        api.moe_route_bwd(w[:3], l, ids, w)
+    with pytest.raises(TypeError):
+        api.moe_route_bwd(w.bfloat16(), l, ids, w)
+    with pytest.raises(TypeError):
+        api.moe_router_loss_fwd(l, ids.long())
+    with pytest.raises(ValueError):
+        api.moe_router_loss_fwd(l, ids[:3])
+    losses, stats = api.moe_router_loss_fwd(l, ids)
+    with pytest.raises(ValueError):
+        api.moe_router_loss_bwd(losses, l, stats[:8])
