@@ -1,5 +1,6 @@
 /*
- * moe_vs.h -- C ABI of the MI355X (gfx950) MoE variable-size grouped GEMM.
+ * moe_vs.h -- C ABI of the MI355X (gfx950) MoE variable-size grouped GEMM, the
+ * routing that feeds it and the dense layer beside it.
  *
  * One launch computes Y_e = X_e W_e for every expert e, where K and N are shared
  * and the row count m_e of each expert is data-dependent, may be zero, and sums
@@ -362,6 +363,12 @@ size_t moe_fused_bwd_workspace_bytes(const moe_schedule *sched, int64_t K, int64
 int moe_fused_bwd(const void *dY, const void *x, const void *W, const moe_schedule *sched,
                   float *dX, void *dW, float *d_topk, int64_t K, int64_t N, int32_t dtype,
                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- routing, router losses, dense linear layer ----------------------------
+ * T and M may be 0 in these calls.  A workspace serves one call at a time:
+ * calls that overlap (on other streams, or in graphs replayed together) each
+ * need their own.
+ */
 
 /*
  * Routing to experts: from the router's logits to the expert_ids and

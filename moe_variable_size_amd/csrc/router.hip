@@ -5,7 +5,10 @@
 // it is the work per row.  LPR = 16 lanes (E <= 256; 32 up to 512, 64 up to 1024)
 // share a row, V values each in registers, so a wave works on 64 / LPR rows and
 // row-wide sums and maxima are 4 steps inside 16 lanes (data-parallel moves, no
-// LDS) instead of 6 across the wave.
+// LDS) instead of 6 across the wave.  A wave per row, which the first kernels
+// took, against this: routing 65536 x 256 with groups and bias 240 against 35 us,
+// the routing gradient of 65536 x 128 27 against 14.3 (5.1 TB/s), the losses there
+// 80 + 69 (join) + 22 against 10.8 + 10 + 15.
 #include <type_traits>
 
 #include "common.hpp"
@@ -334,21 +337,22 @@ __global__ __launch_bounds__(NT) void route_wave_kernel(RouteArgs p) {
   }
 }
 
-// ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= LPR ------------------
+// ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= min(LPR, 32) -----------
 // 32-bit keys that order like the choice value in fp32 (that of -inf: never chosen), in registers and in
 // LDS by expert.  Every lane keeps the best of its V experts.  A round reduces the row's best and
 // its expert over the lanes, strikes it out in LDS, and the lanes look at the struck owner's V
 // values, one each, for the owner's new best: about 36 instructions a round for all rows of the
-// wave, where striking out and searching again in registers takes 80.
+// wave, where striking out and searching again in registers takes 80.  65536 x 256, k = 8: 18.9 us by
+// the logits (3.7 TB/s), 5.5 more for scores and bias, 8 for groups, 3 for rows chosen again.
 //
 // Without a bias the keys are the logits' own order: exact.  With one (and for groups by sums of
 // scores) the values are fp32 approximations, u = 2^-24:
 //   sigmoid: the exponential's argument is rounded once and it is off by 2 u itself, 1 + e by u, the
 //     reciprocal by 2 u: s (1 - s) (|l| + 2) u + 3 s u, which is at most 5 u times the largest score
 //     of the row (times 1 - max l where that is below 0);
-//   softmax: with x the distance from the maximum, two roundings of x, and 28 more of the
-//     exponential, a sum 21 additions deep, the reciprocal and the product; the sum's terms carry
-//     2 x u each, weighted by their share at most 2 ln E = 13 u: e^-x (2 x + 13 + 28) u <= 42 u
+//   softmax: with x the distance from the maximum, two roundings of x, and 30 more of the
+//     exponential, a sum 22 additions deep, the reciprocal and the product; the sum's terms carry
+//     2 x u each, weighted by their share at most 2 ln E = 14 u: e^-x (2 x + 14 + 30) u <= 46 u
 //     times the largest score.
 // Adding the bias rounds once more.  Where two values next to each other in the order are closer than
 // their two errors, the slots' values are compared in 64 bits; where that does not settle it, or the
@@ -448,7 +452,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       key[i] = key32_number(c[i]);
     }
     const float top = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + fexp(-m)) : inv;
-    err = 2.f * top * (p.sigmoid ? 5.f * (1.f + fmaxf(-m, 0.f)) : 42.f) * 0x1p-24f;
+    err = 2.f * top * (p.sigmoid ? 5.f * (1.f + fmaxf(-m, 0.f)) : 46.f) * 0x1p-24f;
     nan = row_sum<LPR>(nan);  // (of -inf and +inf too)
     doubt = nan != nan;
   }
@@ -931,7 +935,7 @@ hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, in
                     ((1u << 20) + E / G - 1) / (E / G)};
   return by_width(E, [&](auto L, auto W) {
     constexpr int LPR = decltype(L)::value, V = decltype(W)::value, VPL = (LPR * V + 63) / 64;
-    if (LPR == 64 || k > LPR || G > LPR) {
+    if (k > LPR || G > (LPR < 32 ? LPR : 32)) {
       const size_t sm = G > 1 ? (size_t)NW * (VPL * 64 + 64) * sizeof(int64_t) : 0;
       const int64_t g = row_grid(T, NW);
       const int grid = (int)(g > (1 << 20) ? (1 << 20) : g);
@@ -939,7 +943,7 @@ hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, in
         route_wave_kernel<float, VPL><<<grid, NT, sm, st>>>(a);
       else
         route_wave_kernel<bf16_t, VPL><<<grid, NT, sm, st>>>(a);
-    } else if constexpr (LPR < 64) {
+    } else {
       const int grid = row_grid(T, NW * (64 / LPR));
       if (dtype == MOE_F32) {
         if (bias) route_kernel<float, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
