@@ -435,7 +435,7 @@ size_t moe_router_loss_workspace_bytes(int64_t T, int32_t E);
  *   assignment); losses [2] float = {balance, z} and stats [E + 1] float
  *   (f, then 1/V: what the backward needs), OVERWRITTEN.  T may be 0.
  *   workspace: moe_router_loss_workspace_bytes(T, E) bytes, 256-byte aligned.
- * Two launches on `stream`; sums are joined in a fixed order (reproducible).
+ * Two or three launches on `stream`; sums are joined in a fixed order (reproducible).
  */
 int moe_router_loss_fwd(const void *logits, const int32_t *expert_ids, int64_t T, int32_t E,
                         int32_t k, int32_t score, float *losses, float *stats, int32_t dtype,

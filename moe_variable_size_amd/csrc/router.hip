@@ -304,40 +304,7 @@ MOE_DEV float chosen_weight(const RouteArgs &p, int id, float lj, float m, float
   return on ? w : 0.f;
 }
 
-// ---- a wave per row: what the kernel below does not take ---------------------------
-template <typename T, int VPL>
-__global__ __launch_bounds__(NT) void route_wave_kernel(RouteArgs p) {
-  extern __shared__ int64_t smem[];  // with groups, per wave: VPL * 64 keys, 64 group values
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  int64_t *lds = smem + (size_t)wid * (VPL * 64 + 64);
-  for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < p.T; t += (int64_t)gridDim.x * NW) {
-    const T *row = (const T *)p.logits + t * p.E;
-    const int id = choose_exact<T, VPL>(p, row, lds, lane);
-    float m = -__builtin_inff(), sum = 0.f, bad = 0.f;
-    if (!p.sigmoid) {
-      float l[VPL];
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = i * 64 + lane;
-        l[i] = e < p.E ? ldf(row + e) : -__builtin_inff();
-        m = fmaxf(m, l[i]);
-        bad += l[i] != l[i] ? l[i] : 0.f;
-      }
-      m = wave_max(m);
-      bad = wave_sum(bad);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += l[i] == -__builtin_inff() ? 0.f : fexp(l[i] - m);
-      sum = wave_sum(sum);
-    }
-    const float w = chosen_weight<64>(p, id, id >= 0 ? ldf(row + id) : 0.f, m, sum, bad);
-    if (lane < p.k) {
-      p.ids[t * p.k + lane] = id;
-      p.w[t * p.k + lane] = w;
-    }
-  }
-}
-
-// ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= min(LPR, 32) -----------
+// ---- 64 / LPR rows per wave: E <= LPR V, k <= LPR, groups <= LPR ---------------------
 // 32-bit keys that order like the choice value in fp32 (that of -inf: never chosen), in registers and in
 // LDS by expert.  Every lane keeps the best of its V experts.  A round reduces the row's best and
 // its expert over the lanes, strikes it out in LDS, and the lanes look at the struck owner's V
@@ -498,7 +465,8 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       const float mag = row_max<LPR>(g < p.G && a > kBarred32 ? fabsf(fa) + fabsf(fb) : 0.f);
       doubt |= hi > kBarred32 && !(lo - key32_value(hi) > (p.top2 ? 2.f * err + mag * 0x1p-22f : err + mag * 0x1p-23f));
     }
-    const uint32_t mask = (uint32_t)(__ballot(kept && sub < gp) >> (lane & ~(LPR - 1)));
+    using Mask = std::conditional_t<LPR == 64, uint64_t, uint32_t>;
+    const Mask mask = (Mask)(__ballot(kept && sub < gp) >> (lane & ~(LPR - 1)));
     if (M::C == 4 && per % 4 == 0) {
 #pragma unroll
       for (int q = 0; q < (V + 3) / 4; ++q) {
@@ -812,10 +780,41 @@ MOE_DEV void block_sums(double &x, double &y, double *red) {
   __syncthreads();
 }
 
+// Sums runs of the blocks' parts into kLossParts parts of the same form: workgroup (x, y) 64 of the 16-byte
+// words (4 threads each) of the y-th run.  Taken where one workgroup would read more than 256 KB: E = 1024
+// at 16384 rows 55 -> 26 us for the forward, E = 512 at 32768 38 -> 26, E = 256 at 65536 30 -> 27.5; E = 128 gains
+// nothing.
+constexpr int kLossParts = 8;
+__global__ __launch_bounds__(256) void loss_sum_kernel(LossArgs p, float *out) {
+  __shared__ f32x4 red[4][64];
+  const int pad = (p.E + 3) & ~3, words = pad / 2;
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const int lo = p.blocks * blockIdx.y / kLossParts, hi = p.blocks * (blockIdx.y + 1) / kLossParts;
+  const bool counts = c >= pad / 4;
+  f32x4 acc = {};
+  auto add = [&](f32x4 a, f32x4 b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = counts ? __int_as_float(__float_as_int(a[i]) + __float_as_int(b[i])) : a[i] + b[i];
+    return a;
+  };
+  if (c < words)
+#pragma unroll 8
+    for (int b = lo + q; b < hi; b += 4) acc = add(acc, ((const f32x4 *)p.part)[(size_t)b * words + c]);
+  red[q][threadIdx.x & 63] = acc;
+  __syncthreads();
+  if (q == 0 && c < words) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) acc = add(acc, red[i][threadIdx.x & 63]);
+    ((f32x4 *)out)[(size_t)blockIdx.y * words + c] = acc;
+  }
+}
+
 // One workgroup joins the blocks' parts, 16 bytes per load: W threads (the power of two from a part's
 // words / 4 up) side by side on a part, the LT / W others take every (LT / W)-th part; then a tree over
 // those.  In 64 bits (the counts too, which it holds exactly).
-__global__ __launch_bounds__(LT) void loss_join_kernel(LossArgs p) {
+// sums: `parts` parts of sums and counts (the blocks' own, or loss_sum_kernel's).
+__global__ __launch_bounds__(LT) void loss_join_kernel(LossArgs p, const float *sums_in, int parts) {
   typedef double f64x4 __attribute__((ext_vector_type(4)));
   __shared__ f64x4 sums[LT];
   __shared__ double red[2 * LW];
@@ -825,18 +824,18 @@ __global__ __launch_bounds__(LT) void loss_join_kernel(LossArgs p) {
   const int c = tid & (W - 1), q = tid / W, Q = LT / W;
   f64x4 acc = {};
   if (c < words) {
-    const f32x4 *src = (const f32x4 *)p.part + c;
+    const f32x4 *src = (const f32x4 *)sums_in + c;
     // 8 loads in flight (past the last part: the last one again, not added)
-    for (int b0 = q; b0 < p.blocks; b0 += 8 * Q) {
+    for (int b0 = q; b0 < parts; b0 += 8 * Q) {
       f32x4 v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = src[(size_t)min(b0 + j * Q, p.blocks - 1) * words];
+      for (int j = 0; j < 8; ++j) v[j] = src[(size_t)min(b0 + j * Q, parts - 1) * words];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const double x = c < pad / 4 ? (double)v[j][i] : (double)__float_as_int(v[j][i]);
-          acc[i] += b0 + j * Q < p.blocks ? x : 0.0;
+          acc[i] += b0 + j * Q < parts ? x : 0.0;
         }
     }
   }
@@ -901,16 +900,29 @@ __global__ __launch_bounds__(NT) void loss_bwd_kernel(LossArgs p) {
   }
 }
 
-// f(integral_constant<LPR>, integral_constant<V>) for E experts
+// f(integral_constant<LPR>, integral_constant<V>) for E experts and at least `lanes` lanes a row
+template <int LPR, class F>
+void by_values(int E, F &&f) {
+  using std::integral_constant;
+  const integral_constant<int, LPR> l;
+  if (E <= LPR) f(l, integral_constant<int, 1>());
+  else if (E <= 2 * LPR) f(l, integral_constant<int, 2>());
+  else if (E <= 4 * LPR) f(l, integral_constant<int, 4>());
+  else if (E <= 8 * LPR) f(l, integral_constant<int, 8>());
+  else f(l, integral_constant<int, 16>());
+}
+template <class F>
+hipError_t by_width(int E, int lanes, F &&f) {
+  if (E <= 256 && lanes <= 16) by_values<16>(E, f);
+  else if (E <= 512 && lanes <= 32) by_values<32>(E, f);
+  else by_values<64>(E, f);
+  return hipGetLastError();
+}
+// the same where any number of lanes does
 template <class F>
 hipError_t by_width(int E, F &&f) {
   using std::integral_constant;
-  const auto l16 = integral_constant<int, 16>();
-  if (E <= 16) f(l16, integral_constant<int, 1>());
-  else if (E <= 32) f(l16, integral_constant<int, 2>());
-  else if (E <= 64) f(l16, integral_constant<int, 4>());
-  else if (E <= 128) f(l16, integral_constant<int, 8>());
-  else if (E <= 256) f(l16, integral_constant<int, 16>());
+  if (E <= 256) by_values<16>(E, f);
   else if (E <= 512) f(integral_constant<int, 32>(), integral_constant<int, 16>());
   else f(integral_constant<int, 64>(), integral_constant<int, 16>());
   return hipGetLastError();
@@ -933,28 +945,17 @@ hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, in
   const RouteArgs a{logits, bias, ids, w, T, E, k, G, keep, sigmoid, top2, renorm, scale,
                     rows_on_lines(logits, E, dtype), bias && rows_on_lines(bias, E, MOE_F32),
                     ((1u << 20) + E / G - 1) / (E / G)};
-  return by_width(E, [&](auto L, auto W) {
-    constexpr int LPR = decltype(L)::value, V = decltype(W)::value, VPL = (LPR * V + 63) / 64;
-    if (k > LPR || G > (LPR < 32 ? LPR : 32)) {
-      const size_t sm = G > 1 ? (size_t)NW * (VPL * 64 + 64) * sizeof(int64_t) : 0;
-      const int64_t g = row_grid(T, NW);
-      const int grid = (int)(g > (1 << 20) ? (1 << 20) : g);
-      if (dtype == MOE_F32)
-        route_wave_kernel<float, VPL><<<grid, NT, sm, st>>>(a);
-      else
-        route_wave_kernel<bf16_t, VPL><<<grid, NT, sm, st>>>(a);
-    } else {
-      const int grid = row_grid(T, NW * (64 / LPR));
-      if (dtype == MOE_F32) {
-        if (bias) route_kernel<float, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
-        else if (G > 1 && top2) route_kernel<float, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
-        else route_kernel<float, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
-      } else {
-        if (bias) route_kernel<bf16_t, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
-        else if (G > 1 && top2) route_kernel<bf16_t, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
-        else route_kernel<bf16_t, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
-      }
-    }
+  return by_width(E, k > G ? k : G, [&](auto L, auto W) {
+    constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
+    const int grid = row_grid(T, NW * (64 / LPR));
+    auto run = [&](auto t) {
+      using X = decltype(t);
+      if (bias) route_kernel<X, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
+      else if (G > 1 && top2) route_kernel<X, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
+      else route_kernel<X, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
+    };
+    if (dtype == MOE_F32) run(0.f);
+    else run((bf16_t)0);
   });
 }
 
@@ -979,8 +980,15 @@ static int loss_blocks(int64_t T, int E) {
   return (int)(g > kLossBlocks ? kLossBlocks : g);
 }
 
+// words of a part (sums and counts) and of all parts and tails, on a 16-byte line; whether the parts are
+// summed by several workgroups first
+static size_t part_words(int E) { return 2 * (size_t)((E + 3) & ~3); }
+static size_t all_words(int blocks, int E) { return blocks * part_words(E) + 2 * ((blocks + 1) & ~1); }
+static bool sums_first(int blocks, int E) { return blocks * part_words(E) > 65536 + 4096; }
+
 size_t loss_workspace_bytes(int64_t T, int E) {
-  return (size_t)loss_blocks(T, E) * (2 * (size_t)((E + 3) & ~3) + 2) * sizeof(float);
+  const int blocks = loss_blocks(T, E);
+  return (all_words(blocks, E) + (sums_first(blocks, E) ? kLossParts * part_words(E) : 0)) * sizeof(float);
 }
 
 hipError_t launch_loss_fwd(const void *logits, const int32_t *ids, int64_t T, int E, int k,
@@ -998,7 +1006,17 @@ hipError_t launch_loss_fwd(const void *logits, const int32_t *ids, int64_t T, in
         loss_fwd_kernel<bf16_t, LPR, V><<<a.blocks, LT, 0, st>>>(a);
     });
   if (e != hipSuccess) return e;
-  loss_join_kernel<<<1, LT, 0, st>>>(a);
+  const float *sums = a.part;
+  int parts = a.blocks;
+  if (sums_first(a.blocks, E)) {
+    float *out = a.part + all_words(a.blocks, E);
+    loss_sum_kernel<<<dim3((unsigned)(part_words(E) / 4 + 63) / 64, kLossParts), 256, 0, st>>>(a, out);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    sums = out;
+    parts = kLossParts;
+  }
+  loss_join_kernel<<<1, LT, 0, st>>>(a, sums, parts);
   return hipGetLastError();
 }
 

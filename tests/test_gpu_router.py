@@ -227,7 +227,8 @@ def _loss_case(T, E, k, score, dtype, seed):
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (7, 3, 2), (300, 60, 6), (1025, 128, 8),
-                                   (65, 257, 3), (50, 512, 8), (33, 1024, 64), (2100, 8, 2)])
+                                   (65, 257, 3), (50, 512, 8), (33, 1024, 64), (2100, 8, 2), (700, 1024, 8),
+                                   (4500, 600, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_losses(T, E, k, score, dtype):
