@@ -339,3 +339,25 @@ def test_input_past_two_gigabytes(N):
     assert bool((db == 3).all()) and not bool(dX[: M - 3].any())
     want = W.double().sum(0)
     assert (dX[-1].double() - want).abs().max() <= V * want.abs().max() + 1e-5
+
+
+def _off(t):
+    """The same values in a dense view that begins one element into its storage."""
+    s = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    v = s[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 128, 264), (40, 1024, 128), (3, 256, 64), (9, 128, 96), (100, 64, 8)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_epilogue_operands_off_their_lines(M, K, N, dtype, out):
+    """Bias, residual, z and out between 16-byte lines, with x and W on them."""
+    x, W, b, r = (t.cuda() for t in _inputs(M, K, N, dtype, out, True, True, 5))
+    kw = dict(act="gelu", out_dtype=DT[out])
+    want, wz = api.moe_linear_fwd(x, W, bias=b, residual=r, save_z=True, **kw)
+    got, gz = api.moe_linear_fwd(x, W, bias=_off(b), residual=_off(r), out=_off(want), z=_off(wz), **kw)
+    assert torch.equal(got, want) and torch.equal(gz, wz)
+    d = torch.randn((M, N), device="cuda").to(DT[out])
+    for a, c in zip(api.moe_linear_bwd(d, x, W, act="gelu", z=wz), api.moe_linear_bwd(_off(d), x, W, act="gelu", z=_off(wz))):
+        assert torch.equal(a, c)

@@ -532,3 +532,33 @@ def test_refusals_of_the_router_binding():
     losses, stats = api.moe_router_loss_fwd(l, ids)
     with pytest.raises(ValueError):
         api.moe_router_loss_bwd(losses, l, stats[:8])
+
+
+def _off(t):
+    """The same values in a dense view that begins one element into its storage."""
+    s = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    v = s[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_off_their_lines(dtype):
+    """Logits, bias, outputs and gradients that begin between lines of four elements."""
+    T, E, k = 50, 64, 6
+    l = _logits(T, E, dtype, 3)
+    bias = (torch.randn(E, generator=torch.Generator().manual_seed(1)) * 0.1)
+    lc, bc = l.cuda(), bias.cuda()
+    ids, w = api.moe_route_fwd(lc, k, bias=bc, groups=4, topk_groups=2, group_score="top2")
+    ids2, w2 = api.moe_route_fwd(_off(lc), k, bias=_off(bc), groups=4, topk_groups=2, group_score="top2",
+                                 expert_ids=_off(ids), topk_weights=_off(w))
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    g = torch.randn((T, k), device="cuda")
+    for renorm in (True, False):
+        d = api.moe_route_bwd(g, lc, ids, w, renormalize=renorm)
+        assert torch.equal(d, api.moe_route_bwd(_off(g), _off(lc), ids2, w2, renormalize=renorm, d_logits=_off(d)))
+    losses, stats = api.moe_router_loss_fwd(lc, ids)
+    l2, s2 = api.moe_router_loss_fwd(_off(lc), ids2)
+    assert torch.equal(losses, l2) and torch.equal(stats, s2)
+    d = api.moe_router_loss_bwd(losses, lc, stats)
+    assert torch.equal(d, api.moe_router_loss_bwd(losses, _off(lc), stats, d_logits=_off(d)))
