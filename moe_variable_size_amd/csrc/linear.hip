@@ -182,51 +182,86 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 // 64 S x 64 S outputs per 4 waves (2 x 2, S x S blocks of 32 x 32 each), 32 reduction elements per
 // step through registers into LDS, element loads with bounds checks.  fp32 multiplies on the
 // matrix cores' fp32 instructions (exact products, fp32 sums; 64 clocks per 2 reduction elements of
-// a block, so the loads hide behind them); a reduction may be cut into ranges as below.
+// a block, so the loads hide behind them); a reduction may be cut into ranges as below.  fp32 4096^3:
+// 1216 us (113 TFLOP/s of the instructions' 157); loads of one element each 1277.
 constexpr int SBK = 32, SNT = 256;
 
-template <typename T>
-struct Pitch {  // LDS row pitch in elements: rows 16-byte aligned, spread over the banks
-  static constexpr int v = sizeof(T) == 2 ? SBK + 8 : SBK + 1;
+// LDS layout of a 64 S x 32 operand tile: [row][reduction], 16-byte rows whose 16-byte reads spread over
+// the banks; fp32 that is MN-major in memory [reduction][row], so that its loads are stored as they
+// come (scattered, 16 lanes met on one bank: the backward of 4096^3 took 2508 us instead of 2236), with a pitch
+// that puts the two halves of a wave, four reduction elements apart, on different banks.
+template <typename T, int S, bool KMAJ>
+struct Tile {
+  static constexpr bool BYK = sizeof(T) == 4 && !KMAJ;
+  static constexpr int PITCH = BYK ? 64 * S + 8 : sizeof(T) == 2 ? SBK + 8 : SBK + 4;
+  static constexpr int SIZE = PITCH * (BYK ? SBK : 64 * S);
+  MOE_DEV static int at(int r, int k) { return BYK ? k * PITCH + r : r * PITCH + k; }
 };
 
-// a 64 S x 32 tile of an operand: element (r, k) to lds[r][k]; thread t brings 8 S elements
-template <int S, bool KMAJ>
+// Thread t brings 8 S elements of the tile, in runs of E that are contiguous in memory (E = 4 where rows
+// are on lines of four elements, else 1; bf16 that is MN-major always 1): the first element of run i
+template <int S, int E, bool KMAJ>
 MOE_DEV void stage_at(int i, int &r, int &k) {
-  const int t = threadIdx.x;
-  r = KMAJ ? i * 8 + (t >> 5) : t % (64 * S);
-  k = KMAJ ? t & 31 : i * (4 / S) + t / (64 * S);
+  constexpr int RUNS = (KMAJ ? SBK : 64 * S) / E;  // per memory row
+  const int t = threadIdx.x, c = t % RUNS * E, o = i * (SNT / RUNS) + t / RUNS;
+  r = KMAJ ? o : c;
+  k = KMAJ ? c : o;
 }
-template <typename T>
-MOE_DEV T buf_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  if constexpr (sizeof(T) == 4)
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-  else
-    return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+template <typename T, int E>
+MOE_DEV void buf_load(__amdgpu_buffer_rsrc_t r, uint32_t off, T *v) {
+  if constexpr (sizeof(T) * E == 16) {
+    const f32x4 x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[i];
+  } else if constexpr (sizeof(T) * E == 8) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (T)(x[i / 2] >> (16 * (i & 1)));
+  } else if constexpr (sizeof(T) == 4) {
+    *v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+  } else {
+    *v = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+  }
 }
 // p: the operand at the tile's first row (column) and the range's reduction element k0; rows: of the
 // operand from there on.  Rows past the end are past the buffer's range; the other direction is checked.
-template <typename T, int S, bool KMAJ>
+template <typename T, int S, int E, bool KMAJ>
 MOE_DEV void stage_load(const T *p, int64_t ld, int rows, int left, T (&v)[8 * S]) {
   const uint32_t es = sizeof(T);
   const int n = KMAJ ? min(rows, 64 * S) : min(left, SBK);  // memory rows of the tile
   const __amdgpu_buffer_rsrc_t r = uniform_rsrc(p, n > 0 ? ((uint32_t)(n - 1) * (uint32_t)ld + (KMAJ ? left : rows)) * es : 0u);
 #pragma unroll
-  for (int i = 0; i < 8 * S; ++i) {
+  for (int i = 0; i < 8 * S / E; ++i) {
     int row, k;
-    stage_at<S, KMAJ>(i, row, k);
+    stage_at<S, E, KMAJ>(i, row, k);
     const bool ok = KMAJ ? k < left : row < rows;
     const uint32_t off = (uint32_t)(KMAJ ? row : k) * (uint32_t)ld + (KMAJ ? k : row);
-    v[i] = buf_load<T>(r, ok ? off * es : kOobOffset);
+    buf_load<T, E>(r, ok ? off * es : kOobOffset, v + i * E);
   }
 }
-template <typename T, int S, bool KMAJ>
+template <typename T, int S, int E, bool KMAJ>
 MOE_DEV void stage_store(T *lds, const T (&v)[8 * S]) {
+  using L = Tile<T, S, KMAJ>;
+  typedef T run_t __attribute__((ext_vector_type(E)));
 #pragma unroll
-  for (int i = 0; i < 8 * S; ++i) {
+  for (int i = 0; i < 8 * S / E; ++i) {
     int r, k;
-    stage_at<S, KMAJ>(i, r, k);
-    lds[r * Pitch<T>::v + k] = v[i];
+    stage_at<S, E, KMAJ>(i, r, k);
+    if constexpr (E == 4)  // (KMAJ or BYK: the run is contiguous in LDS too)
+      *(run_t *)&lds[L::at(r, k)] = run_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    else
+      lds[L::at(r, k)] = v[i];
+  }
+}
+// elements k .. k + 3 of row r (fp32)
+template <int S, bool KMAJ>
+MOE_DEV f32x4 stage_four(const float *lds, int r, int k) {
+  using L = Tile<float, S, KMAJ>;
+  if constexpr (L::BYK) {
+    return f32x4{lds[L::at(r, k)], lds[L::at(r, k + 1)], lds[L::at(r, k + 2)], lds[L::at(r, k + 3)]};
+  } else {
+    return *(const f32x4 *)&lds[L::at(r, k)];
   }
 }
 
@@ -234,10 +269,12 @@ MOE_DEV void stage_store(T *lds, const T (&v)[8 * S]) {
 MOE_DEV int acc_row(int i, int lane) { return ((i >> 2) << 3) + ((lane >> 5) << 2) + (i & 3); }
 
 // splits > 1: range blockIdx / tiles of the reduction, fp32 products to part [splits][M][N]
-template <typename T, typename To, int S, bool AK, bool BKM, int ACT>
+template <typename T, typename To, int S, int E, bool AK, bool BKM, int ACT>
 __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part) {
-  constexpr int P = Pitch<T>::v, TS = 64 * S;
-  __shared__ __align__(16) T As[TS * P], Bs[TS * P];
+  using LA = Tile<T, S, AK>;
+  using LB = Tile<T, S, BKM>;
+  constexpr int TS = 64 * S, EA = sizeof(T) == 4 || AK ? E : 1, EB = sizeof(T) == 4 || BKM ? E : 1;
+  __shared__ __align__(16) T As[LA::SIZE], Bs[LB::SIZE];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int wm = (wid >> 1) * 32 * S, wn = (wid & 1) * 32 * S;
   const int tn = (p.N + TS - 1) / TS, tiles = tn * ((p.M + TS - 1) / TS);
@@ -251,14 +288,14 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
   auto load = [&](int k0) __attribute__((always_inline)) {
     const T *a = (const T *)p.A + (AK ? (int64_t)m0 * p.lda + k0 : (int64_t)k0 * p.lda + m0);
     const T *b = (const T *)p.B + (BKM ? (int64_t)n0 * p.ldb + k0 : (int64_t)k0 * p.ldb + n0);
-    stage_load<T, S, AK>(a, p.lda, p.M - m0, ke - k0, va);
-    stage_load<T, S, BKM>(b, p.ldb, p.N - n0, ke - k0, vb);
+    stage_load<T, S, EA, AK>(a, p.lda, p.M - m0, ke - k0, va);
+    stage_load<T, S, EB, BKM>(b, p.ldb, p.N - n0, ke - k0, vb);
   };
   load(kb);
   for (int k0 = kb; k0 < ke; k0 += SBK) {
     __syncthreads();
-    stage_store<T, S, AK>(As, va);
-    stage_store<T, S, BKM>(Bs, vb);
+    stage_store<T, S, EA, AK>(As, va);
+    stage_store<T, S, EB, BKM>(Bs, vb);
     __syncthreads();
     if (k0 + SBK < ke) load(k0 + SBK);
     const int r = lane & 31, h = lane >> 5;
@@ -268,8 +305,8 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
         bf16x8_t a[S], b[S];
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          a[i] = *(const bf16x8_t *)&As[(wm + i * 32 + r) * P + s * 16 + h * 8];
-          b[i] = *(const bf16x8_t *)&Bs[(wn + i * 32 + r) * P + s * 16 + h * 8];
+          a[i] = *(const bf16x8_t *)&As[LA::at(wm + i * 32 + r, s * 16 + h * 8)];
+          b[i] = *(const bf16x8_t *)&Bs[LB::at(wn + i * 32 + r, s * 16 + h * 8)];
         }
 #pragma unroll
         for (int i = 0; i < S; ++i)
@@ -278,19 +315,23 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
       }
     } else {
+      // four reduction elements per lane and read: element e of both halves of the wave is one
+      // 32 x 32 x 2 product (the same two reduction indices in both operands)
 #pragma unroll
-      for (int s = 0; s < SBK / 2; ++s) {
-        float a[S], b[S];
+      for (int s = 0; s < SBK / 8; ++s) {
+        f32x4 a[S], b[S];
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          a[i] = As[(wm + i * 32 + r) * P + s * 2 + h];
-          b[i] = Bs[(wn + i * 32 + r) * P + s * 2 + h];
+          a[i] = stage_four<S, AK>(As, wm + i * 32 + r, s * 8 + h * 4);
+          b[i] = stage_four<S, BKM>(Bs, wn + i * 32 + r, s * 8 + h * 4);
         }
 #pragma unroll
-        for (int i = 0; i < S; ++i)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int j = 0; j < S; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[j], acc[i][j], 0, 0, 0);
+          for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
       }
     }
   }
@@ -1106,13 +1147,19 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
   }
   const Plan pl = staged_plan(a.M, a.N, a.K);
   const int ts = 64 * pl.shape;
+  // memory rows (of lda, ldb elements, their whole length) on lines of four elements
+  const bool fours = a.lda % 4 == 0 && a.ldb % 4 == 0 && on_line(a.A, 4 * sizeof(T)) && on_line(a.B, 4 * sizeof(T));
   const int grid = ((a.N + ts - 1) / ts) * ((a.M + ts - 1) / ts) * pl.splits;
   by_act_of<AK && BKM>(act, [&](auto A) {
     constexpr int ACT = decltype(A)::value;
-    if (pl.shape == 2)
-      staged_gemm<T, To, 2, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part);
-    else
-      staged_gemm<T, To, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part);
+    float *const out = (float *)part;
+    if (pl.shape == 2) {
+      if (fours) staged_gemm<T, To, 2, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+      else staged_gemm<T, To, 2, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+    } else {
+      if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+      else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+    }
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.splits == 1) return e;
