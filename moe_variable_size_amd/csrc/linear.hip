@@ -183,12 +183,13 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 // step through registers into LDS, element loads with bounds checks.  fp32 multiplies on the
 // matrix cores' fp32 instructions (exact products, fp32 sums; 64 clocks per 2 reduction elements of
 // a block, so the loads hide behind them); a reduction may be cut into ranges as below.  fp32 4096^3:
-// 1216 us (113 TFLOP/s of the instructions' 157); loads of one element each 1277.
+// 1072 us (128 TFLOP/s of the instructions' 157).
 constexpr int SBK = 32, SNT = 256;
 
 // LDS layout of a 64 S x 32 operand tile: [row][reduction], 16-byte rows whose 16-byte reads spread over
 // the banks; fp32 that is MN-major in memory [reduction][row], so that its loads are stored as they
-// come (scattered, 16 lanes met on one bank: the backward of 4096^3 took 2508 us instead of 2236), with a pitch
+// come (scattered, 16 lanes met on one bank: the backward of 4096^3 in 128 x 128 tiles took 2508
+// us instead of 2236), with a pitch
 // that puts the two halves of a wave, four reduction elements apart, on different banks.
 template <typename T, int S, bool KMAJ>
 struct Tile {
@@ -1064,12 +1065,14 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   }
   return best;
 }
-// The staged kernel's: 128 x 128 (S = 2) where that fills the chip twice; else 64 x 64, with the
-// reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
-// backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us).
-Plan staged_plan(int64_t M, int64_t N, int64_t K) {
+// The staged kernel's: bf16 takes 128 x 128 tiles (S = 2) where they fill the chip twice; else, and in fp32
+// always, 64 x 64 (fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
+// products are slow enough that the operands' traffic does not matter, and more waves share the CU), with
+// the reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
+// backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us of products, cut 64 x 64 tiles 41).
+Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   const int64_t t2 = ((M + 127) / 128) * ((N + 127) / 128), t1 = ((M + 63) / 64) * ((N + 63) / 64);
-  if (t2 >= 512) return Plan{2, 1};
+  if (bf16 && t2 >= 512) return Plan{2, 1};
   const int64_t steps = (K + SBK - 1) / SBK;
   int64_t k = t1 > 0 ? 1024 / t1 : 1;
   if (k > steps / 4) k = steps / 4;
@@ -1078,7 +1081,7 @@ Plan staged_plan(int64_t M, int64_t N, int64_t K) {
 }
 // workspace for the partial products of either kernel
 size_t part_bytes(int64_t M, int64_t N, int64_t K, bool bf16) {
-  const int a = staged_plan(M, N, K).splits, b = bf16 ? plan_of(M, N, K).splits : 1;
+  const int a = staged_plan(M, N, K, bf16).splits, b = bf16 ? plan_of(M, N, K).splits : 1;
   const int k = a > b ? a : b;
   return k > 1 ? (size_t)k * M * N * 4 : 0;
 }
@@ -1145,7 +1148,7 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
       return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
     }
   }
-  const Plan pl = staged_plan(a.M, a.N, a.K);
+  const Plan pl = staged_plan(a.M, a.N, a.K, sizeof(T) == 2);
   const int ts = 64 * pl.shape;
   // memory rows (of lda, ldb elements, their whole length) on lines of four elements
   const bool fours = a.lda % 4 == 0 && a.ldb % 4 == 0 && on_line(a.A, 4 * sizeof(T)) && on_line(a.B, 4 * sizeof(T));
@@ -1153,13 +1156,15 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
   by_act_of<AK && BKM>(act, [&](auto A) {
     constexpr int ACT = decltype(A)::value;
     float *const out = (float *)part;
-    if (pl.shape == 2) {
-      if (fours) staged_gemm<T, To, 2, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-      else staged_gemm<T, To, 2, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-    } else {
-      if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-      else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+    if constexpr (sizeof(T) == 2) {
+      if (pl.shape == 2) {
+        if (fours) staged_gemm<T, To, 2, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+        else staged_gemm<T, To, 2, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+        return;
+      }
     }
+    if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
+    else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.splits == 1) return e;
