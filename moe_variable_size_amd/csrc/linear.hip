@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "linear_plan.hpp"
 
 namespace moe {
 namespace {
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 // matrix cores' fp32 instructions (exact products, fp32 sums; 64 clocks per 2 reduction elements of
 // a block, so the loads hide behind them); a reduction may be cut into ranges as below.  fp32 4096^3:
 // 1072 us (128 TFLOP/s of the instructions' 157).
-constexpr int SBK = 32, SNT = 256;
+constexpr int SNT = 256;
 
 // LDS layout of a 64 S x 32 operand tile: [row][reduction], 16-byte rows whose 16-byte reads spread over
 // the banks; fp32 that is MN-major in memory [reduction][row], so that its loads are stored as they
@@ -382,7 +383,6 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 #define LDS_AS __attribute__((address_space(3)))
-constexpr int PBK = 64;
 
 // 16 bytes per lane from rsrc + voff to LDS byte address lds + 16 * lane (lds wave-uniform);
 // zeros where voff is out of the buffer
@@ -988,8 +988,6 @@ void by_act_of(int act, F &&f) {
     f(std::integral_constant<int, MOE_ACT_NONE>());
 }
 
-constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};  // tile shapes
-
 // launch of a kernel with more LDS than the default allows; the attribute is set once per device
 template <auto KERNEL>
 hipError_t launch_lds(int grid, size_t smem, const PipeArgs &q, hipStream_t st) {
@@ -1020,7 +1018,7 @@ hipError_t run_piped(PipeArgs &q, int shape, int act, hipStream_t st) {
       e = launch_lds<piped_gemm<4, 2, 2, 4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
     else if (shape == 1)
       e = launch_lds<piped_gemm<2, 2, 4, 2, AK, BKM, To, ACT>>(grid, 96 << 10, q, st);
-    else if (grid <= device_cu_count())
+    else if (ring_stages(grid, device_cu_count()) == 4)
       e = launch_lds<ring_gemm<4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
     else
       e = launch_lds<ring_gemm<2, AK, BKM, To, ACT>>(grid, 64 << 10, q, st);
@@ -1028,57 +1026,6 @@ hipError_t run_piped(PipeArgs &q, int shape, int act, hipStream_t st) {
   return e;
 }
 
-// Tile shape and number of reduction ranges of a product of M x N outputs.
-struct Plan {
-  int shape, splits;  // shape: 0 = 256 x 256, 1 = 256 x 128, 2 = 128 x 128
-};
-
-// The choice minimises an estimate in us: rounds of workgroups over the chip (256 CUs; two 128 x 128
-// workgroups fit one) times the stages of a range at the shape's measured time per stage, 6 us of
-// launch, first loads and epilogue, and for split reductions the join: a launch, and the partial
-// products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 us, 256 x 128 0.92, 128 x 128 0.5
-// alone on a CU and 1.0 in pairs.  Measured, us (256 x 256 / 256 x 128 / 128 x 128 / the last in two
-// ranges): 8192 x 4096 x 4096 198 / 240 / 252 / 389, 4096 x 2048 x 2048 47 / 35 / 38 / 60, 2048^3 43 / 31 /
-// 24 / 35, 512 x 4096 x 4096 74 / 51 / 33 / 31, 64 x 4096 x 4096 71 / 49 / 30 / 21 (four ranges 15.5).
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
-  const int64_t stages = (K + PBK - 1) / PBK;
-  Plan best{0, 1};
-  double least = 0;
-  for (int sh = 0; sh < 3; ++sh) {
-    const double tiles = (double)((M + kShapeM[sh] - 1) / kShapeM[sh]) * ((N + kShapeN[sh] - 1) / kShapeN[sh]);
-    for (int k : kSplits) {
-      if (k > 1 && (stages < 2 * k || tiles * k > 512)) break;
-      const double wgs = tiles * k, per = (double)((stages + k - 1) / k);
-      double t;
-      if (sh == 2)
-        t = wgs <= 256 ? per * 0.5 : __builtin_ceil(wgs / 512) * per * 1.0;
-      else
-        t = __builtin_ceil(wgs / 256) * per * (sh == 0 ? 1.35 : 0.92);
-      t += 6;
-      if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
-      if (least == 0 || t < least) {
-        least = t;
-        best = Plan{sh, k};
-      }
-    }
-  }
-  return best;
-}
-// The staged kernel's: bf16 takes 128 x 128 tiles (S = 2) where they fill the chip twice; else, and in fp32
-// always, 64 x 64 (fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
-// products are slow enough that the operands' traffic does not matter, and more waves share the CU), with
-// the reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
-// backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us of products, cut 64 x 64 tiles 41).
-Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
-  const int64_t t2 = ((M + 127) / 128) * ((N + 127) / 128), t1 = ((M + 63) / 64) * ((N + 63) / 64);
-  if (bf16 && t2 >= 512) return Plan{2, 1};
-  const int64_t steps = (K + SBK - 1) / SBK;
-  int64_t k = t1 > 0 ? 1024 / t1 : 1;
-  if (k > steps / 4) k = steps / 4;
-  if (k > 16) k = 16;
-  return Plan{1, (int)(k < 1 ? 1 : k)};
-}
 // workspace for the partial products of either kernel
 size_t part_bytes(int64_t M, int64_t N, int64_t K, bool bf16) {
   const int a = staged_plan(M, N, K, bf16).splits, b = bf16 ? plan_of(M, N, K).splits : 1;

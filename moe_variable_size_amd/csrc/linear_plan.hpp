@@ -1,0 +1,66 @@
+// Which tiles a product of the dense linear layer takes, from its sizes alone.  Plain host code, so that
+// the tests can ask the same rule.
+#pragma once
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int PBK = 64;  // reduction elements per stage of the pipelined and ring tiles
+constexpr int SBK = 32;  // per step of the staged tiles
+constexpr int kShapeM[3] = {256, 256, 128}, kShapeN[3] = {256, 128, 128};  // tile shapes
+
+// Tile shape and number of reduction ranges of a product of M x N outputs.
+struct Plan {
+  int shape, splits;  // shape: 0 = 256 x 256, 1 = 256 x 128, 2 = 128 x 128
+};
+
+// The choice minimises an estimate in us: rounds of workgroups over the chip (256 CUs; two 128 x 128
+// workgroups fit one) times the stages of a range at the shape's measured time per stage, 6 us of
+// launch, first loads and epilogue, and for split reductions the join: a launch, and the partial
+// products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 us, 256 x 128 0.92, 128 x 128 0.5
+// alone on a CU and 1.0 in pairs.  Measured, us (256 x 256 / 256 x 128 / 128 x 128 / the last in two
+// ranges): 8192 x 4096 x 4096 198 / 240 / 252 / 389, 4096 x 2048 x 2048 47 / 35 / 38 / 60, 2048^3 43 / 31 /
+// 24 / 35, 512 x 4096 x 4096 74 / 51 / 33 / 31, 64 x 4096 x 4096 71 / 49 / 30 / 21 (four ranges 15.5).
+inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int64_t stages = (K + PBK - 1) / PBK;
+  Plan best{0, 1};
+  double least = 0;
+  for (int sh = 0; sh < 3; ++sh) {
+    const double tiles = (double)((M + kShapeM[sh] - 1) / kShapeM[sh]) * ((N + kShapeN[sh] - 1) / kShapeN[sh]);
+    for (int k : kSplits) {
+      if (k > 1 && (stages < 2 * k || tiles * k > 512)) break;
+      const double wgs = tiles * k, per = (double)((stages + k - 1) / k);
+      double t;
+      if (sh == 2)
+        t = wgs <= 256 ? per * 0.5 : __builtin_ceil(wgs / 512) * per * 1.0;
+      else
+        t = __builtin_ceil(wgs / 256) * per * (sh == 0 ? 1.35 : 0.92);
+      t += 6;
+      if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = Plan{sh, k};
+      }
+    }
+  }
+  return best;
+}
+// The staged kernel's: bf16 takes 128 x 128 tiles (S = 2) where they fill the chip twice; else, and in fp32
+// always, 64 x 64 (fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
+// products are slow enough that the operands' traffic does not matter, and more waves share the CU), with
+// the reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
+// backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us of products, cut 64 x 64 tiles 41).
+inline Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
+  const int64_t t2 = ((M + 127) / 128) * ((N + 127) / 128), t1 = ((M + 63) / 64) * ((N + 63) / 64);
+  if (bf16 && t2 >= 512) return Plan{2, 1};
+  const int64_t steps = (K + SBK - 1) / SBK;
+  int64_t k = t1 > 0 ? 1024 / t1 : 1;
+  if (k > steps / 4) k = steps / 4;
+  if (k > 16) k = 16;
+  return Plan{1, (int)(k < 1 ? 1 : k)};
+}
+// Stages of the ring of 128 x 128 tiles (ring_gemm's NST)
+inline int ring_stages(int64_t workgroups, int cus) { return workgroups <= cus ? 4 : 2; }
+
+}  // namespace moe
