@@ -873,11 +873,12 @@ def router_loss(logits, expert_ids, *, score="softmax"):
 
 class LinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, bias, act, residual, out_dtype):
+    def forward(ctx, x, W, bias, act, residual, out_dtype, recorded):
         x, W = x.detach().contiguous(), W.detach().contiguous()
         b = None if bias is None else bias.detach().contiguous()
         r = None if residual is None else residual.detach().contiguous()
-        keep = act != "none" and any(ctx.needs_input_grad[:3])
+        # needs_input_grad holds under no_grad too
+        keep = recorded and act != "none" and any(ctx.needs_input_grad[:3])
         y = moe_linear_fwd(x, W, bias=b, act=act, residual=r, out_dtype=out_dtype, save_z=keep)
         y, z = y if keep else (y, None)
         ctx.save_for_backward(x, W, z)
@@ -888,14 +889,14 @@ class LinearFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, gy):
         x, W, z = ctx.saved_tensors
-        nx, nw, nb, _, nr, _ = ctx.needs_input_grad
+        nx, nw, nb, _, nr = ctx.needs_input_grad[:5]
         dX = dW = db = None
         if nx or nw or nb:
             dX, dW, db = moe_linear_bwd(gy.contiguous(), x, W, act=ctx.act, z=z, dx=nx, dw=nw, dbias=nb)
-        return dX, dW, db, None, gy if nr else None, None
+        return dX, dW, db, None, gy if nr else None, None, None
 
 
 def linear(x, W, bias=None, *, act="none", residual=None, out_dtype=None):
     """Differentiable dense layer act(x W^T + bias) + residual of
     ``moe_linear_fwd``; gradients reach x, W, bias and residual."""
-    return LinearFunction.apply(x, W, bias, act, residual, out_dtype)
+    return LinearFunction.apply(x, W, bias, act, residual, out_dtype, torch.is_grad_enabled())
