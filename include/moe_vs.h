@@ -391,6 +391,7 @@ int moe_fused_bwd(const void *dY, const void *x, const void *W, const moe_schedu
  *            NaN logit makes its row's softmax weights NaN.
  *   logits [T, E] in `dtype`; bias [E] float or NULL; expert_ids [T, k] int32
  *   and topk_weights [T, k] float, OVERWRITTEN.  T may be 0.
+ *   T * k < 2^31 (one launch up to 2^25 rows, several above).
  *   1 <= k <= min(64, E), E <= 1024, groups <= 64 a divisor of E (E / groups
  *   >= 2 for MOE_GROUP_TOP2), 1 <= topk_groups <= groups, k <= topk_groups *
  *   E / groups, scale finite and > 0 (MOE_ERR_OPTION).
@@ -462,8 +463,10 @@ int moe_router_loss_bwd(const float *d_losses, const void *logits, const float *
  *   `dtype`; residual [M, N] or NULL and out [M, N] in `out_dtype`, which may
  *   be the same buffer.  dtype MOE_F32 -> out_dtype MOE_F32; dtype MOE_BF16 ->
  *   MOE_BF16 or MOE_F32.  Element alignment; any sizes (bf16 runs fastest with
- *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0; K and N are
- *   at most 2^22.  Tensors of any size (64-bit addresses).
+ *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0 and is
+ *   below 2^31 - 512 (several launches where one cannot hold the rows); K and N
+ *   are at most 2^22.  Tensors of any size (64-bit addresses; bf16 operands of
+ *   2 GiB and more take the kernel for any alignment, about 3 times slower).
  *   workspace: moe_linear_fwd_workspace_bytes(...) bytes, 256-byte aligned
  *   (may be NULL when that is 0).
  */

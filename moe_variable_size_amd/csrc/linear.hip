@@ -1065,6 +1065,23 @@ hipError_t run_stream(const GemmArgs &a, int act, hipStream_t st) {
 
 template <bool AK, bool BKM, typename T, typename To>
 hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
+  if constexpr (AK) {
+    // in runs of rows where one launch could not hold them (no sizes in memory make dW's do)
+    const int64_t run = launch_rows(a.M, a.N);
+    if (run < a.M) {
+      for (int64_t m0 = 0; m0 < a.M; m0 += run) {
+        GemmArgs b = a;
+        b.M = (int)(a.M - m0 < run ? a.M - m0 : run);
+        b.A = (const T *)a.A + m0 * a.lda;
+        b.out = (To *)a.out + m0 * a.N;
+        if (a.res) b.res = (const To *)a.res + m0 * a.N;
+        if (a.z) b.z = (T *)a.z + m0 * a.N;
+        const hipError_t e = gemm<AK, BKM, T, To>(b, act, part, st);
+        if (e != hipSuccess) return e;
+      }
+      return hipSuccess;
+    }
+  }
   if constexpr (AK && BKM) {
     if (streams(a, sizeof(T))) {
       if (a.M <= 4) {

@@ -60,6 +60,17 @@ inline Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   if (k > 16) k = 16;
   return Plan{1, (int)(k < 1 ? 1 : k)};
 }
+// Rows of one launch, at most M of them.  A dispatch holds fewer than 2^32 work-items: the streamed
+// products take 64 per row of x (at most 16 columns), the smallest tiles 256 per 64 x 64 outputs.  Both are
+// kept at 2^31; a product of more is cut into runs of equally many rows (whole runs of 64, so that
+// alignments stay), each of over 2^17 small tiles, so none of them splits its reduction.
+inline int64_t launch_rows(int64_t M, int64_t N) {
+  int64_t most = ((int64_t)1 << 29) / ((N + 63) / 64);
+  if (most > 1 << 25) most = 1 << 25;
+  if (M <= most) return M;
+  const int64_t runs = (M + most - 1) / most, per = (M + runs - 1) / runs;
+  return (per + 63) / 64 * 64;
+}
 // Stages of the ring of 128 x 128 tiles (ring_gemm's NST)
 inline int ring_stages(int64_t workgroups, int cus) { return workgroups <= cus ? 4 : 2; }
 

@@ -928,6 +928,22 @@ hipError_t by_width(int E, F &&f) {
   return hipGetLastError();
 }
 
+// A dispatch holds fewer than 2^32 work-items, and a row takes up to 64: calls of more rows than this
+// (of a launch, 2^31 work-items at most) take several launches.  f(first row, rows)
+constexpr int64_t kLaunchRows = 1 << 25;
+template <class F>
+hipError_t by_rows(int64_t T, F &&f) {
+  for (int64_t t0 = 0; t0 < T; t0 += kLaunchRows) {
+    const hipError_t e = f(t0, T - t0 < kLaunchRows ? T - t0 : kLaunchRows);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+template <class P>
+P *at_row(P *p, int64_t row, int64_t bytes) {
+  return (P *)((const char *)p + row * bytes);
+}
+
 // blocks of `rows` rows each
 int row_grid(int64_t T, int rows) { return (int)((T + rows - 1) / rows); }
 
@@ -942,35 +958,43 @@ bool rows_on_lines(const void *p, int E, int dtype) {
 hipError_t launch_route_fwd(const void *logits, const float *bias, int64_t T, int E, int k,
                             bool sigmoid, int G, int keep, bool top2, bool renorm, float scale,
                             int32_t *ids, float *w, int dtype, hipStream_t st) {
-  const RouteArgs a{logits, bias, ids, w, T, E, k, G, keep, sigmoid, top2, renorm, scale,
-                    rows_on_lines(logits, E, dtype), bias && rows_on_lines(bias, E, MOE_F32),
-                    ((1u << 20) + E / G - 1) / (E / G)};
-  return by_width(E, k > G ? k : G, [&](auto L, auto W) {
-    constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
-    const int grid = row_grid(T, NW * (64 / LPR));
-    auto run = [&](auto t) {
-      using X = decltype(t);
-      if (bias) route_kernel<X, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
-      else if (G > 1 && top2) route_kernel<X, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
-      else route_kernel<X, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
-    };
-    if (dtype == MOE_F32) run(0.f);
-    else run((bf16_t)0);
+  const int64_t row = (int64_t)E * (dtype == MOE_F32 ? 4 : 2), slots = (int64_t)k * 4;
+  return by_rows(T, [&](int64_t t0, int64_t n) {
+    const RouteArgs a{at_row(logits, t0, row), bias, at_row(ids, t0, slots), at_row(w, t0, slots), n, E, k, G,
+                      keep, sigmoid, top2, renorm, scale,
+                      rows_on_lines(logits, E, dtype), bias && rows_on_lines(bias, E, MOE_F32),
+                      ((1u << 20) + E / G - 1) / (E / G)};
+    return by_width(E, k > G ? k : G, [&](auto L, auto W) {
+      constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
+      const int grid = row_grid(n, NW * (64 / LPR));
+      auto run = [&](auto t) {
+        using X = decltype(t);
+        if (bias) route_kernel<X, LPR, V, BY_BIASED><<<grid, NT, 0, st>>>(a);
+        else if (G > 1 && top2) route_kernel<X, LPR, V, GROUPS_BY_SCORE><<<grid, NT, 0, st>>>(a);
+        else route_kernel<X, LPR, V, BY_LOGIT><<<grid, NT, 0, st>>>(a);
+      };
+      if (dtype == MOE_F32) run(0.f);
+      else run((bf16_t)0);
+    });
   });
 }
 
 hipError_t launch_route_bwd(const float *g, const void *logits, const int32_t *ids, const float *w,
                             int64_t T, int E, int k, bool sigmoid, bool renorm, float scale,
                             void *d, int dtype, hipStream_t st) {
-  const RouteBwdArgs a{g, logits, ids, w, d, T, E, k, sigmoid, renorm, scale,
-                       rows_on_lines(logits, E, dtype) && rows_on_lines(d, E, dtype)};
-  return by_width(E, [&](auto L, auto W) {
-    constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
-    const int grid = row_grid(T, NW * (64 / LPR));
-    if (dtype == MOE_F32)
-      route_bwd_kernel<float, LPR, V><<<grid, NT, 0, st>>>(a);
-    else
-      route_bwd_kernel<bf16_t, LPR, V><<<grid, NT, 0, st>>>(a);
+  const int64_t row = (int64_t)E * (dtype == MOE_F32 ? 4 : 2), slots = (int64_t)k * 4;
+  return by_rows(T, [&](int64_t t0, int64_t n) {
+    const RouteBwdArgs a{at_row(g, t0, slots), at_row(logits, t0, row), at_row(ids, t0, slots),
+                         at_row(w, t0, slots), at_row(d, t0, row), n, E, k, sigmoid, renorm, scale,
+                         rows_on_lines(logits, E, dtype) && rows_on_lines(d, E, dtype)};
+    return by_width(E, [&](auto L, auto W) {
+      constexpr int LPR = decltype(L)::value, V = decltype(W)::value;
+      const int grid = row_grid(n, NW * (64 / LPR));
+      if (dtype == MOE_F32)
+        route_bwd_kernel<float, LPR, V><<<grid, NT, 0, st>>>(a);
+      else
+        route_bwd_kernel<bf16_t, LPR, V><<<grid, NT, 0, st>>>(a);
+    });
   });
 }
 
