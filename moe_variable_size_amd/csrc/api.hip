@@ -628,7 +628,7 @@ namespace {
 int check_route(int64_t T, int32_t E, int32_t k, int32_t score, int32_t dtype) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (T < 0 || E < 1 || k < 1 || k > 64 || k > E) return MOE_ERR_SHAPE;
-  if (E > kMaxExperts || T * k >= kMax32) return MOE_ERR_LIMIT;
+  if (E > kMaxExperts || T >= kMax32 || T * k >= kMax32) return MOE_ERR_LIMIT;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_OPTION;
   return MOE_OK;
 }
@@ -694,7 +694,7 @@ int moe_route_bwd(const float *d_weights, const void *logits, const int32_t *exp
 }
 
 size_t moe_router_loss_workspace_bytes(int64_t T, int32_t E) {
-  if (T < 0 || E < 1 || E > kMaxExperts) return 0;
+  if (T < 0 || T >= kMax32 || E < 1 || E > kMaxExperts) return 0;
   return align256(loss_workspace_bytes(T, E));
 }
 
