@@ -826,7 +826,8 @@ class RouteFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale):
         logits = logits.detach().contiguous()
-        ids, w = moe_route_fwd(logits, k, score=score, bias=None if bias is None else bias.detach(),
+        b = None if bias is None else bias.detach().contiguous()
+        ids, w = moe_route_fwd(logits, k, score=score, bias=b,
                                groups=groups, topk_groups=topk_groups, group_score=group_score,
                                renormalize=renormalize, scale=scale)
         ctx.mark_non_differentiable(ids)
@@ -854,7 +855,7 @@ class RouterLossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, expert_ids, score):
         logits = logits.detach().contiguous()
-        losses, stats = moe_router_loss_fwd(logits, expert_ids, score=score)
+        losses, stats = moe_router_loss_fwd(logits, expert_ids.contiguous(), score=score)
         ctx.save_for_backward(logits, stats)
         ctx.score = score
         return losses
