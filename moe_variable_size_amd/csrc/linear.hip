@@ -900,6 +900,13 @@ __global__ __launch_bounds__(512) void row_gemm(GemmArgs p) {
 }
 
 // ---- dz and the bias gradient ---------------------------------------------------
+// dz is rounded once, to nearest, to the operands' type, from fp32: the matrix instructions take both
+// operands of a product in bf16.  That is an independent error of half a step in each term, as large in
+// norm as the rounding of the outputs: 8192 x 4096 x 2048 with silu, dX and dW are off by 2.34e-3, by
+// 1.66e-3 with their own rounding alone.  dz as two bf16 halves would halve the rate (twice the products), fp32
+// products would take a tenth of it (275 GFLOP at 154 TFLOP/s: 1.8 ms against 0.23).  The bias gradient
+// sums the unrounded values.
+//
 // Block (bx, by): 32 V columns from 32 V bx, rows from a contiguous range, 8 at a time; V columns
 // (16 bytes of bf16 for V = 8) per thread.  Each block's column sums go to part[by][N]; bias_join
 // adds them in order.  V = 8 where rows are on 16-byte lines.

@@ -149,3 +149,21 @@ def test_large_training_backward_repeats():
         api.moe_linear_fwd(x[: 64 + 501 * i], W, act="silu")
         for a, b in zip(api.moe_linear_bwd(d, x, W, act="silu", z=z), first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("M,K,N", [(2437, 2488, 328), (261, 2968, 2896), (300, 40, 48), (77, 33, 50)])
+def test_dz_is_rounded_once_to_the_nearest(act, M, K, N):
+    """With a derivative of 0 or 1 dz is d_out itself, so an fp32 d_out shows its one rounding to bf16: the
+    two products are those of the rounded values, the bias gradient the sum of the unrounded ones."""
+    log(f"dz {M} {K} {N} {act}")
+    x, W = _randn((M, K), 31), _randn((N, K), 32, K ** -0.5)
+    d, z = _randn((M, N), 33, dtype=F32), _randn((M, N), 34)
+    dX, dW, db = api.moe_linear_bwd(d, x, W, act=act, z=None if act == "none" else z)
+    torch.cuda.synchronize()
+    exact = d * (z > 0) if act == "relu" else d
+    dz = exact.bfloat16().double()
+    for got, A, B, name in ((dX, dz, W.double(), "dX"), (dW, dz.t().contiguous(), x.double(), "dW")):
+        _close(got, A @ B, _sum_tol(A, B), name)
+    one = torch.ones((1, M), dtype=torch.float64, device="cuda")
+    _close(db, exact.double().sum(0), _sum_tol(one, exact.double())[0], "db")
