@@ -156,7 +156,8 @@ MOE_DEV void store_row(T *row, int E, int sub, bool vec, const float (&d)[V]) {
     if (e < E) stf(row + e, d[i]);
   }
 }
-// exp through the hardware's exp2: x log2(e) rounded once, relative error (|x| + 2) 2^-24
+// exp through the hardware's exp2: log2(e) is off by 0.23 2^-24, its product with x is rounded once, and the
+// instruction adds 2: relative error (1.23 |x| + 2) 2^-24
 MOE_DEV float fexp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 struct RouteArgs {
@@ -314,13 +315,13 @@ MOE_DEV float chosen_weight(const RouteArgs &p, int id, float lj, float m, float
 //
 // Without a bias the keys are the logits' own order: exact.  With one (and for groups by sums of
 // scores) the values are fp32 approximations, u = 2^-24:
-//   sigmoid: the exponential's argument is rounded once and it is off by 2 u itself, 1 + e by u, the
-//     reciprocal by 2 u: s (1 - s) (|l| + 2) u + 3 s u, which is at most 5 u times the largest score
-//     of the row (times 1 - max l where that is below 0);
-//   softmax: with x the distance from the maximum, two roundings of x, and 30 more of the
-//     exponential, a sum 22 additions deep, the reciprocal and the product; the sum's terms carry
-//     2 x u each, weighted by their share at most 2 ln E = 14 u: e^-x (2 x + 14 + 30) u <= 46 u
-//     times the largest score.
+//   sigmoid: the exponential e is off by (1.23 |l| + 2) u, 1 + e by u, the reciprocal by 2 u:
+//     s (1 - s) (1.23 |l| + 2) u + 3 s u, which is at most 5 u times the largest score of the row (times
+//     1 - max l where that is below 0);
+//   softmax: with x the distance from the maximum, its own rounding and the exponential's 2.23 x, and 30
+//     more of the exponential, a sum 22 additions deep, the reciprocal and the product; the sum's terms
+//     carry 2.23 x u each, weighted by their share at most 2.23 ln E = 15.5 u: e^-x (2.23 x + 15.5 + 30) u
+//     <= 46 u times the largest score.
 // Adding the bias rounds once more.  Where two values next to each other in the order are closer than
 // their two errors, the slots' values are compared in 64 bits; where that does not settle it, or the
 // groups on both sides of the cut are that close, or the row holds a NaN, the wave chooses that row
@@ -781,9 +782,9 @@ MOE_DEV void block_sums(double &x, double &y, double *red) {
 }
 
 // Sums runs of the blocks' parts into kLossParts parts of the same form: workgroup (x, y) 64 of the 16-byte
-// words (4 threads each) of the y-th run.  Taken where one workgroup would read more than 256 KB: E = 1024
-// at 16384 rows 55 -> 26 us for the forward, E = 512 at 32768 38 -> 26, E = 256 at 65536 30 -> 27.5; E = 128 gains
-// nothing.
+// words (4 threads each) of the y-th run.  Taken where one workgroup would read more than 272 KB: E = 1024
+// at 16384 rows 55 -> 26 us for the forward, E = 512 at 32768 38 -> 26, E = 256 at 65536 30 -> 27.5; E = 128 (256 KB)
+// gains nothing.
 constexpr int kLossParts = 8;
 __global__ __launch_bounds__(256) void loss_sum_kernel(LossArgs p, float *out) {
   __shared__ f32x4 red[4][64];
@@ -1008,7 +1009,7 @@ static int loss_blocks(int64_t T, int E) {
 // summed by several workgroups first
 static size_t part_words(int E) { return 2 * (size_t)((E + 3) & ~3); }
 static size_t all_words(int blocks, int E) { return blocks * part_words(E) + 2 * ((blocks + 1) & ~1); }
-static bool sums_first(int blocks, int E) { return blocks * part_words(E) > 65536 + 4096; }
+static bool sums_first(int blocks, int E) { return blocks * part_words(E) > 272 * 1024 / sizeof(float); }
 
 size_t loss_workspace_bytes(int64_t T, int E) {
   const int blocks = loss_blocks(T, E);
