@@ -466,7 +466,7 @@ int moe_router_loss_bwd(const float *d_losses, const void *logits, const float *
  *   K a multiple of 8 and 16-byte aligned x and W).  M may be 0 and is
  *   below 2^31 - 512 (several launches where one cannot hold the rows); K and N
  *   are at most 2^22.  Tensors of any size (64-bit addresses; bf16 operands of
- *   2 GiB and more take the kernel for any alignment, about 3 times slower).
+ *   2 GiB and more take the kernel for any alignment, 2 to 3.3 times slower).
  *   workspace: moe_linear_fwd_workspace_bytes(...) bytes, 256-byte aligned
  *   (may be NULL when that is 0).
  */

@@ -187,7 +187,8 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 // step through registers into LDS, element loads with bounds checks.  fp32 multiplies on the
 // matrix cores' fp32 instructions (exact products, fp32 sums; 64 clocks per 2 reduction elements of
 // a block, so the loads hide behind them); a reduction may be cut into ranges as below.  fp32 4096^3:
-// 1072 us (128 TFLOP/s of the instructions' 157).
+// 1068 us (129 TFLOP/s of the instructions' 157).  bf16 4096 x 4095 x 4095, element by element: 282 us (487
+// TFLOP/s), 4096 x 4100 x 4096, four by four: 241 (571).
 constexpr int SNT = 256;
 
 // LDS layout of a 64 S x 32 operand tile: [row][reduction], 16-byte rows whose 16-byte reads spread over
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
 // first read, when four younger ones are in flight.  (Reads waited for in the memory part instead
 // allow one quarter more of lead: the same time within 2 %.)
 //
-// Measured: 8192^3 723-748 us (1470-1520 TFLOP/s), 8192 x 4096 x 4096 198 us (1390).  Without the loads
+// Measured: 8192^3 723-789 us by card (1390-1520 TFLOP/s), 8192 x 4096 x 4096 198 us (1390).  Without the loads
 // (timing only) 8192^3 takes 629 us, without the operand reads 695: the loads, and a clock near
 // 1.9 GHz under this load, are the bound; touching coming stages' lines ahead made it slower.
 typedef short i16x4 __attribute__((ext_vector_type(4)));

@@ -20,7 +20,10 @@ struct Plan {
 // products written and read at 4 TB/s.  Per stage: 256 x 256 1.35 us, 256 x 128 0.92, 128 x 128 0.5
 // alone on a CU and 1.0 in pairs.  Measured, us (256 x 256 / 256 x 128 / 128 x 128 / the last in two
 // ranges): 8192 x 4096 x 4096 198 / 240 / 252 / 389, 4096 x 2048 x 2048 47 / 35 / 38 / 60, 2048^3 43 / 31 /
-// 24 / 35, 512 x 4096 x 4096 74 / 51 / 33 / 31, 64 x 4096 x 4096 71 / 49 / 30 / 21 (four ranges 15.5).
+// 24 / 35, 512 x 4096 x 4096 74 / 51 / 33 / 31, 64 x 4096 x 4096 71 / 49 / 30 / 21.  Few rows, 128 x 128 in 4 / 6 /
+// 8 / 12 / 16 ranges (the rule's in brackets): 32 x 4096 x 4096 13.9 / 13.0 / [12.9] / 14.7 / 14.9, 64 x 4096 x
+// 4096 14.4 / 14.2 / [14.6] / 16.9 / 18.1, 128 x 4096 x 4096 16.4 / [17.5] / 18.2 / 21.0 / 23.6, 128 x 7168 x 2048
+// 20.5 / 17.3 / [16.6] / 17.8 / 19.2, 8192 x 4096 x 64 [18.7] / 20.9 / 21.6 / 27.5 / 31.2.
 inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t stages = (K + PBK - 1) / PBK;
@@ -47,7 +50,7 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 // The staged kernel's: bf16 takes 128 x 128 tiles (S = 2) where they fill the chip twice; else, and in fp32
-// always, 64 x 64 (fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
+// always, 64 x 64 (timed in turn, fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
 // products are slow enough that the operands' traffic does not matter, and more waves share the CU), with
 // the reduction cut until there are about four workgroups per CU, of at least 4 steps each (fp32
 // backward of 1237 x 1001 x 499: 128 x 128 tiles uncut 180 us of products, cut 64 x 64 tiles 41).
