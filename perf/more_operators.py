@@ -127,12 +127,12 @@ def _mix(h):
 
 
 def _dither(sizes, seed, t, device):
-    """Two uniform numbers of 16 bits for every element of tensors that lie in whole blocks behind each other."""
+    """Two uniform numbers, of 16 bits and a half, for every element of tensors that lie in whole blocks behind each other."""
     n = torch.tensor([-(-int(v) // BLOCK) * BLOCK for v in sizes.split(",")], device=device)
     keys = _mix((_mix((seed + 0x9E3779B9 * t) & 0xFFFFFFFF) + torch.arange(n.numel(), device=device)) & 0xFFFFFFFF)
     index = torch.arange(int(n.sum()), device=device) - torch.repeat_interleave(n.cumsum(0) - n, n)
     h = _mix(index ^ torch.repeat_interleave(keys, n))
-    return (h & 0xFFFF).float() * 2.0 ** -16, (h >> 16).float() * 2.0 ** -16
+    return ((h & 0xFFFF).float() + 0.5) * 2.0 ** -16, ((h >> 16).float() + 0.5) * 2.0 ** -16
 
 
 def _pack8(a, u):
@@ -444,7 +444,7 @@ def exact(case, seed):
                 q = a.abs() / torch.where(scale > 0, scale, torch.ones_like(scale))[:, None]
                 # the step between neighbours: an eighth of the power of two below, 2^-9 at least
                 step = torch.exp2(torch.floor(torch.log2(q.clamp(min=2.0 ** -6))) - 3)
-                q = (torch.floor(q / step + bits.view(blocks, BLOCK).to(f64) / 65536) * step).clamp(max=448.0)
+                q = (torch.floor(q / step + (2 * bits.view(blocks, BLOCK).to(f64) + 1) / 131072) * step).clamp(max=448.0)
                 q = (q * a.sign()).view(-1)
                 out[key][span] = torch.where(tail, flat[key][span].to(f64), q)
                 out[key + "_scale"][rows] = scale
