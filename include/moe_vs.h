@@ -501,6 +501,56 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
                    int32_t dtype, int32_t out_dtype, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ---- the optimizer's step ---------------------------------------------------- */
+
+/* One tensor of moe_adamw_step: `n` elements, dense, any alignment of their type
+ * (16-byte lines run fastest).  n may be 0 (its pointers are then not looked at). */
+typedef struct moe_adamw_tensor {
+  void *param;       /* [n] param_dtype, updated                                   */
+  const void *grad;  /* [n] grad_dtype                                             */
+  void *m, *v;       /* [n] states, updated: float, or 8-bit codes                 */
+  float *m_scale;    /* [ceil(n / 256)] 8-bit states' scales, updated; else NULL   */
+  float *v_scale;
+  float *master;     /* [n] fp32 copy that the step is taken on, `param` then being
+                        its rounding; NULL: the step is taken on `param`           */
+  int64_t n;         /* <= 2^34                                                    */
+  int64_t number;    /* 8-bit states: tells the tensors' roundings apart           */
+} moe_adamw_tensor;
+
+/*
+ * AdamW over any number of tensors (one launch per 48; none for count 0):
+ *   g' = s g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   w = w (1 - lr weight_decay)
+ *       - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps),
+ * in fp32, w being the master copy where there is one; `param` is rounded to
+ * nearest.
+ *   tensors [count] HOST array (not kept); no two of them may overlap.
+ *   state_bits 32: m and v are float.  8: codes of the E4M3 format (see
+ *   moe_fused_fwd_fp8) in which element i stands for
+ *       m_i = q(m[i]) m_scale[i / 256],   v_i = (q(v[i]) v_scale[i / 256])^2.
+ *   The scale is the block's largest |m| (sqrt v) / 448, or 0 with codes of 0
+ *   where that largest value is below 2^-100.  With y = |value| 448 / largest and d
+ *   the distance of y's two neighbours in the format, the code is d floor(y / d +
+ *   u): rounded up with the remainder's probability, so that states move by less
+ *   than a code's distance on average.  u is (half + 1/2) / 2^16 with the
+ *   low (m) or high (v) half of h = mix(i ^ mix(mix(seed + 0x9E3779B9 t) + number)) in 32 bits (number +
+ *   0x9E3779B9 (i >> 32) for long tensors), with
+ *       mix(h): h = (h ^ h >> 16) 0x6A09E667, h = (h ^ h >> 15) 0xBB67AE85, h ^ h >> 16.
+ *   A block that holds a value that is not finite becomes NaN.
+ *   lr, step: the learning rate and t >= 1, or device pointers lr_dev and step_dev
+ *   ([1] each, NULL: the numbers) that are read when the launch runs, for graphs
+ *   that are replayed; step is then not looked at.
+ *   grad_scale [1] (device, NULL for 1): s; where it is not finite, nothing is
+ *   changed.
+ *   0 <= beta < 1, 0 <= eps, lr and weight_decay finite (MOE_ERR_OPTION).
+ *   param_dtype and grad_dtype MOE_F32 or MOE_BF16 each; a master copy needs
+ *   MOE_BF16 parameters (MOE_ERR_DTYPE).
+ */
+int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
+                   double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                   const int32_t *step_dev, const float *grad_scale, uint32_t seed,
+                   int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream);
+
 /*
  * Export the flat tile space the grouped kernels walk for an output of N
  * columns with tiles of BM x BN ([GG] "Problem descriptors and the tile

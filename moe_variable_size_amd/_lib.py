@@ -59,10 +59,28 @@ class MoeSchedule(ctypes.Structure):
     ]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    """Mirror of ``struct moe_adamw_tensor``."""
+
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("number", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_U32 = ctypes.c_uint32
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _SZ = ctypes.c_size_t
 _SCHED_P = ctypes.POINTER(MoeSchedule)
 
@@ -92,6 +110,8 @@ SIGNATURES = {
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32, _I32]),
     "moe_linear_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
                                       _P, _SZ, _P]),
+    "moe_adamw_step": (ctypes.c_int, [_P, _I32, _F64, _P, _F64, _F64, _F64, _F64, _I64, _P, _P, _U32, _I32,
+                                      _I32, _I32, _P]),
     "moe_tile_map": (ctypes.c_int, [_SCHED_P, _I64, _I32, _I32, _P, _P, _P, _I64, _P]),
     "moe_set_tile_rows": (ctypes.c_int, [_I32]),
     "moe_set_combine": (ctypes.c_int, [_I32]),

@@ -11,6 +11,7 @@ Pages the operations follow:
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -708,6 +709,187 @@ def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act
                                 _ptr(db), M, K, N, a, code, ocode, _ptr(ws), nbytes, raw)
     _lib.check("moe_linear_bwd", st)
     return dX, dW, db
+
+
+# ---- the optimizer's step -----------------------------------------------------------------------
+
+def _tensors(ts, name: str, count: int, dtypes, sizes, index: int) -> list:
+    """Addresses of a list of dense device tensors of these dtypes (all alike) and element counts."""
+    ts = list(ts)
+    if len(ts) != count:
+        raise ValueError(f"{name} must have {count} tensors, got {len(ts)}")
+    for i, (t, n) in enumerate(zip(ts, sizes)):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
+            _require(t, f"{name}[{i}]")
+            raise TypeError(f"{name}[{i}] must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name}[{i}] must have {n} elements, got {t.numel()}")
+        if t.get_device() != index:
+            raise ValueError(f"{name}[{i}] must be on cuda:{index}, got {t.device}")
+    if len({t.dtype for t in ts}) > 1:
+        raise TypeError(f"{name} must be all of one dtype")
+    return [t.data_ptr() for t in ts]
+
+
+def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+                   weight_decay: float = 0.01, masters=None, m_scales=None, v_scales=None,
+                   grad_scale: Optional[torch.Tensor] = None, seed: int = 0, numbers=None, stream=None) -> None:
+    """One AdamW step on lists of tensors, in place, in one launch per 48 of
+    them: params (float32 or bfloat16), grads (float32 or bfloat16) and the
+    states exp_avgs and exp_avg_sqs, float32, or float8_e4m3fn codes of m and
+    of sqrt(v) with ``m_scales`` and ``v_scales`` (float32, one for every 256
+    elements of a tensor), rounded by ``seed``, the step's number and the
+    tensor's (its place in the list, or ``numbers``).  ``masters``: float32
+    copies of bfloat16 params, on which the step is then taken.  ``step`` (from
+    1 on) and ``lr`` are numbers, or tensors of one element (int32, float32) on
+    the device, which a captured graph reads anew at each replay.
+    ``grad_scale`` [1] float32 multiplies the gradients; where it is not finite
+    nothing is changed.  No two tensors may overlap."""
+    lib = _lib.load()
+    params = list(params)
+    count = len(params)
+    if not count:
+        return
+    _require(params[0], "params[0]", contiguous=False)
+    index, dev = params[0].get_device(), params[0].device
+    sizes = [p.numel() if isinstance(p, torch.Tensor) else -1 for p in params]
+    real = tuple(_DTYPES)
+    p = _tensors(params, "params", count, real, sizes, index)
+    if len(set(p)) != count and len({a for a, n in zip(p, sizes) if n}) != sum(n > 0 for n in sizes):
+        raise ValueError("params must not hold a tensor twice")
+    grads = list(grads)
+    g = _tensors(grads, "grads", count, real, sizes, index)
+    exp_avgs = list(exp_avgs)
+    eight = bool(exp_avgs) and isinstance(exp_avgs[0], torch.Tensor) and exp_avgs[0].dtype == torch.float8_e4m3fn
+    kind = (torch.float8_e4m3fn,) if eight else (torch.float32,)
+    m = _tensors(exp_avgs, "exp_avgs", count, kind, sizes, index)
+    v = _tensors(exp_avg_sqs, "exp_avg_sqs", count, kind, sizes, index)
+    none = [0] * count
+    ms = vs = w = none
+    if eight:
+        if m_scales is None or v_scales is None:
+            raise ValueError("states in 8 bits need m_scales and v_scales")
+        blocks = [-(-n // 256) for n in sizes]
+        ms = _tensors(m_scales, "m_scales", count, (torch.float32,), blocks, index)
+        vs = _tensors(v_scales, "v_scales", count, (torch.float32,), blocks, index)
+    elif m_scales is not None or v_scales is not None:
+        raise ValueError("m_scales and v_scales go with states in 8 bits")
+    if masters is not None:
+        if params[0].dtype != torch.bfloat16:
+            raise TypeError("masters go with bfloat16 params")
+        w = _tensors(masters, "masters", count, (torch.float32,), sizes, index)
+    numbers = range(count) if numbers is None else list(numbers)
+    if len(numbers) != count:
+        raise ValueError(f"numbers must have {count} entries")
+    for t, name, dt in ((step, "step", torch.int32), (lr, "lr", torch.float32), (grad_scale, "grad_scale", torch.float32)):
+        if isinstance(t, torch.Tensor):
+            _require(t, name, dt)
+            if t.numel() != 1 or t.get_device() != index:
+                raise ValueError(f"{name} must be one number on {dev}")
+    on_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
+    table = array.array("q", [a for row in zip(p, g, m, v, ms, vs, w, sizes, numbers) for a in row])
+    ctx, raw = _launch(params[0], stream)
+    with ctx:
+        st = lib.moe_adamw_step(table.buffer_info()[0], count, 0.0 if on_dev[1] else lr, _ptr(lr) if on_dev[1] else None,
+                                betas[0], betas[1], eps, weight_decay, 1 if on_dev[0] else step,
+                                _ptr(step) if on_dev[0] else None, _ptr(grad_scale), seed & 0xFFFFFFFF,
+                                _DTYPES[params[0].dtype], _DTYPES[grads[0].dtype], 8 if eight else 32, raw)
+    _lib.check("moe_adamw_step", st)
+
+
+class AdamW:
+    """AdamW over a list of parameters, float32 or bfloat16 and dense, by
+    ``moe_adamw_step``: the states in 32 or 8 bits (``state_bits``), with
+    ``master`` a float32 copy of every bfloat16 parameter.  ``step()`` takes
+    each parameter's ``.grad``; those without one are left as they are.
+    ``capturable`` keeps the step's number and ``lr`` on the device, so that a
+    step captured in a graph counts on and follows ``set_lr`` when replayed."""
+
+    def __init__(self, params, *, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 32, master: bool = False, seed: int = 0,
+                 capturable: bool = False):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params is empty")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        for i, p in enumerate(self.params):
+            _require(p, f"params[{i}]")
+            _dtype_code(p)
+            if p.device != self.params[0].device:
+                raise ValueError(f"params[{i}] must be on {self.params[0].device}, got {p.device}")
+        self.betas, self.eps, self.weight_decay = (float(betas[0]), float(betas[1])), float(eps), float(weight_decay)
+        self.state_bits, self.seed, self.capturable = state_bits, int(seed), bool(capturable)
+        dev = self.params[0].device
+        kind = torch.float8_e4m3fn if state_bits == 8 else torch.float32
+
+        def zeros(n, dtype):
+            return torch.zeros(n, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device=dev).view(dtype)
+
+        self.m = [zeros(p.numel(), kind) for p in self.params]
+        self.v = [zeros(p.numel(), kind) for p in self.params]
+        eight = state_bits == 8
+        self.m_scale = [zeros(-(-p.numel() // 256), torch.float32) for p in self.params] if eight else None
+        self.v_scale = [zeros(-(-p.numel() // 256), torch.float32) for p in self.params] if eight else None
+        self.masters = [p.detach().float() if p.dtype == torch.bfloat16 else None
+                        for p in self.params] if master else None
+        self.t = torch.zeros(1, dtype=torch.int32, device=dev) if capturable else 0
+        self.lr = torch.full((1,), float(lr), device=dev) if capturable else float(lr)
+
+    def set_lr(self, lr: float) -> None:
+        if self.capturable:
+            self.lr.fill_(float(lr))
+        else:
+            self.lr = float(lr)
+
+    def zero_grad(self) -> None:
+        for p in self.params:
+            p.grad = None
+
+    @torch.no_grad()
+    def step(self, grad_scale: Optional[torch.Tensor] = None) -> None:
+        self.t += 1
+        sets = {}
+        for i, p in enumerate(self.params):
+            if p.grad is not None:
+                sets.setdefault((p.dtype, p.grad.dtype), []).append(i)
+        for (dtype, _), at in sets.items():
+            def of(a, at=at):
+                return None if a is None else [a[i] for i in at]
+            params = of(self.params)
+            moe_adamw_step([p.detach() for p in params], [p.grad.contiguous() for p in params], of(self.m), of(self.v),
+                           step=self.t, lr=self.lr, betas=self.betas, eps=self.eps, weight_decay=self.weight_decay,
+                           masters=of(self.masters) if dtype == torch.bfloat16 else None, m_scales=of(self.m_scale),
+                           v_scales=of(self.v_scale), grad_scale=grad_scale, seed=self.seed, numbers=at)
+            torch.autograd.graph.increment_version(params)
+
+    _LISTS = ("m", "v", "m_scale", "v_scale", "masters")
+
+    def state_dict(self) -> dict:
+        """The states themselves (not copies), the step's number and the learning rate."""
+        return {"t": int(self.t), "lr": float(self.lr), "state_bits": self.state_bits, "seed": self.seed,
+                **{k: getattr(self, k) for k in self._LISTS}}
+
+    @torch.no_grad()
+    def load_state_dict(self, d: dict) -> None:
+        if d["state_bits"] != self.state_bits:
+            raise ValueError(f"states are in {d['state_bits']} bits, here in {self.state_bits}")
+        pairs = []
+        for k in self._LISTS:
+            a, b = getattr(self, k), d[k]
+            if (a is None) != (b is None) or (a is not None and (len(a) != len(b) or any(
+                    (x is None) != (y is None) or (x is not None and (x.shape != y.shape or x.dtype != y.dtype))
+                    for x, y in zip(a, b)))):
+                raise ValueError(f"{k} does not fit these parameters")
+            pairs += [(x, y) for x, y in zip(a or (), b or ()) if x is not None]
+        for x, y in pairs:
+            x.view(torch.uint8).copy_(y.view(torch.uint8)) if x.dtype == torch.float8_e4m3fn else x.copy_(y)
+        self.seed = int(d["seed"])
+        if self.capturable:
+            self.t.fill_(int(d["t"]))
+        else:
+            self.t = int(d["t"])
+        self.set_lr(d["lr"])
 
 
 def moe_tile_map(sched: Schedule, N: int, BM: int, BN: int, owner_capacity: Optional[int] = None,

@@ -170,7 +170,7 @@ const char *const kFamilies[] = {"build_schedule", "fill_zero", "grouped_gemm", 
                                  "fused_fwd_fp8", "gated_bwd_dw_down", "gated_bwd_dh",
                                  "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx", "route_fwd",
                                  "route_bwd", "router_loss_fwd", "router_loss_bwd", "linear_fwd",
-                                 "linear_bwd"};
+                                 "linear_bwd", "adamw"};
 constexpr int kNumFamilies = sizeof(kFamilies) / sizeof(kFamilies[0]);
 
 struct Timing {
@@ -216,7 +216,7 @@ hipError_t timed(int fam, hipStream_t st, F &&f) {
 
 enum { F_SCHED = 0, F_FILL, F_BARE, F_FWD, F_DX, F_DW, F_TILEMAP, F_GATED_UP, F_GATED_DOWN,
        F_FWD_FP8, F_GB_DWD, F_GB_DH, F_GB_DX, F_GB_DWGU, F_FWD_MX, F_ROUTE_FWD, F_ROUTE_BWD,
-       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD };
+       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD, F_ADAMW };
 
 }  // namespace
 }  // namespace moe
@@ -782,6 +782,40 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
   return hip_status(timed(F_LIN_BWD, st, [&] {
     return launch_linear_bwd(d_out, x, W, z, dX, dW, d_bias, (int)M, (int)K, (int)N, act, dtype,
                              out_dtype, workspace, st);
+  }));
+}
+
+int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
+                   double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                   const int32_t *step_dev, const float *grad_scale, uint32_t seed,
+                   int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
+  if ((param_dtype != MOE_F32 && param_dtype != MOE_BF16) ||
+      (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16))
+    return MOE_ERR_DTYPE;
+  if (count < 0) return MOE_ERR_SHAPE;
+  if (state_bits != 8 && state_bits != 32) return MOE_ERR_OPTION;
+  if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0) || !isfinite(eps) ||
+      !isfinite(lr) || !isfinite(weight_decay) || (!step_dev && (step < 1 || step >= kMax32)))
+    return MOE_ERR_OPTION;
+  if (count > 0 && !tensors) return MOE_ERR_NULL;
+  if (!aligned(lr_dev, 4) || !aligned(step_dev, 4) || !aligned(grad_scale, 4)) return MOE_ERR_ALIGN;
+  const size_t ep = esize(param_dtype), eg = esize(grad_dtype), es = state_bits == 8 ? 1 : 4;
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor &t = tensors[i];
+    if (t.n < 0) return MOE_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (t.n > ((int64_t)1 << 34)) return MOE_ERR_LIMIT;
+    if (t.master && param_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
+      return MOE_ERR_NULL;
+    if (!aligned(t.param, ep) || !aligned(t.grad, eg) || !aligned(t.m, es) || !aligned(t.v, es) ||
+        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4) || !aligned(t.master, 4))
+      return MOE_ERR_ALIGN;
+  }
+  hipStream_t st = (hipStream_t)stream;
+  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev, grad_scale, seed};
+  return hip_status(timed(F_ADAMW, st, [&] {
+    return launch_adamw(tensors, count, o, param_dtype, grad_dtype, state_bits, st);
   }));
 }
 

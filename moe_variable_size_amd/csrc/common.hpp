@@ -189,6 +189,18 @@ hipError_t launch_linear_fwd(const void *x, const void *W, const void *bias, con
 hipError_t launch_linear_bwd(const void *dout, const void *x, const void *W, const void *z,
                              void *dX, void *dW, void *db, int M, int K, int N, int act, int dtype,
                              int out_dtype, void *ws, hipStream_t st);
+
+// optimizer step
+struct AdamwOptions {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const float *lr_dev;
+  const int32_t *step_dev;
+  const float *grad_scale;
+  uint32_t seed;
+};
+hipError_t launch_adamw(const moe_adamw_tensor *tensors, int count, const AdamwOptions &o, int param_dtype,
+                        int grad_dtype, int bits, hipStream_t st);
 }  // namespace moe
 
 namespace moe {
