@@ -501,6 +501,53 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
                    int32_t dtype, int32_t out_dtype, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ---- loss of a model's output layer ------------------------------------------- */
+
+/*
+ * Cross entropy of logits l = x W^T that are not kept:
+ *   lse_m = log sum_v exp(l_mv),   loss_m = lse_m - l_m,t + z_weight lse_m^2,
+ * t = targets[m].  A row whose target is outside [0, V) (a prompt's or the
+ * padding's token) does not count: its loss is 0.
+ *   x [M, K], W [V, K] in `dtype` (MOE_BF16 or MOE_F32); targets [M] int32 or
+ *   int64 (target_bits 32 or 64); loss [M], lse [M] float, OVERWRITTEN;
+ *   total [3] float or NULL: {sum of loss, rows that count, sum / rows (0 for no
+ *   rows)}, OVERWRITTEN.
+ *   Element alignment, any sizes (bf16 runs fastest with K a multiple of 8 and
+ *   16-byte aligned x and W); M may be 0; M <= 2^24, K and V <= 2^22.
+ *   workspace: moe_linear_ce_fwd_workspace_bytes(...) bytes, 256-byte aligned:
+ *   at most two numbers per row and 128 columns of the vocabulary, or a piece of
+ *   256 MB (or 1024 columns) of logits where the tiles cannot join them.
+ * Sums are fp32 per row and run of columns, joined in a fixed order (reproducible).
+ * A logit of +inf or NaN makes its row's loss NaN.
+ */
+#define MOE_REDUCE_NONE 0
+#define MOE_REDUCE_SUM 1
+#define MOE_REDUCE_MEAN 2
+size_t moe_linear_ce_fwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype);
+int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t target_bits,
+                      int64_t M, int64_t K, int64_t V, float z_weight, float *loss, float *lse,
+                      float *total, int32_t dtype, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * Gradient of sum_m g_m loss_m, with g = d_loss [M] (MOE_REDUCE_NONE), d_loss[0]
+ * for every row (_SUM) or d_loss[0] / total[1] (_MEAN):
+ *   dl = g_m ((1 + 2 z_weight lse_m) exp(l - lse_m) - [v = t]), 0 in rows that do
+ *   not count, rounded to `dtype` for the two products;
+ *   dX = dl W [M, K],  dW = dl^T x [V, K], in `dtype`: each OVERWRITTEN, or NULL to
+ *   skip.
+ *   x, W, targets, z_weight as in the forward, lse [M] and total [3] from it (total
+ *   for _MEAN alone).  M may be 0 (dW is then zeros).
+ *   workspace: moe_linear_ce_bwd_workspace_bytes(...) bytes, 256-byte aligned: dl
+ *   of a piece of the vocabulary (256 MB, or 256 columns), dX's sum in fp32, and
+ *   the products'.
+ */
+size_t moe_linear_ce_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype);
+int moe_linear_ce_bwd(const float *d_loss, int32_t reduction, const float *total, const void *x,
+                      const void *W, const void *targets, int32_t target_bits, const float *lse,
+                      int64_t M, int64_t K, int64_t V, float z_weight, void *dX, void *dW,
+                      int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- the optimizer's step ---------------------------------------------------- */
 
 /* One tensor of moe_adamw_step: `n` elements, dense, any alignment of their type

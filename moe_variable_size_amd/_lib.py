@@ -24,6 +24,7 @@ MOE_COMBINE_ATOMIC = 1
 MOE_COMBINE_RANKED = 2
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 MOE_GROUP_SCORES = {"max": 0, "top2": 1}
+MOE_REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 MOE_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
@@ -110,6 +111,11 @@ SIGNATURES = {
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32, _I32]),
     "moe_linear_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
                                       _P, _SZ, _P]),
+    "moe_linear_ce_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "moe_linear_ce_fwd": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _F32, _P, _P, _P, _I32, _P, _SZ, _P]),
+    "moe_linear_ce_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "moe_linear_ce_bwd": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _F32, _P, _P, _I32,
+                                         _P, _SZ, _P]),
     "moe_adamw_step": (ctypes.c_int, [_P, _I32, _F64, _P, _F64, _F64, _F64, _F64, _I64, _P, _P, _U32, _I32,
                                       _I32, _I32, _P]),
     "moe_tile_map": (ctypes.c_int, [_SCHED_P, _I64, _I32, _I32, _P, _P, _P, _I64, _P]),

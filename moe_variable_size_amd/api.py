@@ -23,7 +23,7 @@ import torch
 from . import _lib
 from ._lib import MOE_BF16, MOE_F32, MOE_LAYOUT_CONTIGUOUS, MOE_LAYOUT_MASKED, BM_VALUES
 from ._lib import MOE_COMBINE_AUTO, MOE_COMBINE_ATOMIC, MOE_COMBINE_RANKED
-from ._lib import MOE_ACTS, MOE_GROUP_SCORES, MOE_SCORES
+from ._lib import MOE_ACTS, MOE_GROUP_SCORES, MOE_REDUCTIONS, MOE_SCORES
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -497,6 +497,16 @@ def _linear_bwd_workspace(M, K, N, act, code, out_code):
     return int(_lib.load().moe_linear_bwd_workspace_bytes(M, K, N, act, code, out_code))
 
 
+@functools.lru_cache(maxsize=4096)
+def _ce_fwd_workspace(M, K, V, code):
+    return int(_lib.load().moe_linear_ce_fwd_workspace_bytes(M, K, V, code))
+
+
+@functools.lru_cache(maxsize=4096)
+def _ce_bwd_workspace(M, K, V, code):
+    return int(_lib.load().moe_linear_ce_bwd_workspace_bytes(M, K, V, code))
+
+
 def _option(table: dict, value, name: str) -> int:
     if value not in table:
         raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
@@ -709,6 +719,82 @@ def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act
                                 _ptr(db), M, K, N, a, code, ocode, _ptr(ws), nbytes, raw)
     _lib.check("moe_linear_bwd", st)
     return dX, dW, db
+
+
+# ---- loss of a model's output layer -------------------------------------------------------------
+
+def _ce_operands(x, W, targets):
+    """(dtype code, device index, M, K, V, bits of a target)"""
+    _need(x, "x", None, 2, -1)
+    code, index = _dtype_code(x), x.get_device()
+    _need(W, "W", x.dtype, 2, index)
+    M, K = x.shape
+    if W.shape[1] != K:
+        raise ValueError("shape mismatch between x [M, K] and W [V, K]")
+    _need(targets, "targets", None, 1, index)
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"targets must be int32 or int64, got {targets.dtype}")
+    if targets.numel() != M:
+        raise ValueError(f"targets must have {M} entries, got {targets.numel()}")
+    return code, index, M, K, W.shape[0], 64 if targets.dtype == torch.int64 else 32
+
+
+def moe_linear_ce_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, z_weight: float = 0.0,
+                      total: Optional[torch.Tensor] = None, stream=None):
+    """Cross entropy of the logits x W^T, which are not kept: x [M, K] and W
+    [V, K] bfloat16 or float32, targets [M] int32 or int64.  Returns (loss [M],
+    lse [M]) float32, loss = lse - logit of the target + z_weight lse^2, 0 in
+    rows whose target is outside [0, V); into ``total`` [3] float32, if given,
+    the sum of the losses, the number of rows that count, and their quotient."""
+    lib = _lib.load()
+    code, _, M, K, V, bits = _ce_operands(x, W, targets)
+    dev = x.device
+    if total is not None:
+        _require_out(total, "total", torch.float32, (3,), dev)
+    ctx, raw = _launch(x, stream)
+    with ctx:
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
+        nbytes = _ce_fwd_workspace(M, K, V, code)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        st = lib.moe_linear_ce_fwd(_ptr(x), _ptr(W), _ptr(targets), bits, M, K, V, z_weight, _ptr(loss), _ptr(lse),
+                                   _ptr(total), code, _ptr(ws), nbytes, raw)
+    _lib.check("moe_linear_ce_fwd", st)
+    return loss, lse
+
+
+def moe_linear_ce_bwd(d_loss: torch.Tensor, x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
+                      lse: torch.Tensor, *, z_weight: float = 0.0, reduction: str = "none",
+                      total: Optional[torch.Tensor] = None, dx: bool = True, dw: bool = True, stream=None):
+    """Gradients (dX [M, K] | None, dW [V, K] | None), in x's dtype, of
+    ``moe_linear_ce_fwd``'s losses from d_loss float32: [M], or one number, the
+    gradient of their sum or (with the forward's ``total``) of their mean."""
+    lib = _lib.load()
+    code, index, M, K, V, bits = _ce_operands(x, W, targets)
+    dev = x.device
+    red = _option(MOE_REDUCTIONS, reduction, "reduction")
+    _require_out(lse, "lse", torch.float32, (M,), dev)
+    if red:
+        _require(d_loss, "d_loss", torch.float32)
+        if d_loss.numel() != 1 or d_loss.get_device() != index:
+            raise ValueError(f"d_loss must be one number on {dev}")
+    else:
+        _require_out(d_loss, "d_loss", torch.float32, (M,), dev)
+    if reduction == "mean":
+        if total is None:
+            raise ValueError("the mean's gradient needs the total its forward gave")
+        _require_out(total, "total", torch.float32, (3,), dev)
+    ctx, raw = _launch(x, stream)
+    with ctx:
+        dX = torch.empty((M, K), dtype=x.dtype, device=dev) if dx else None
+        dW = torch.empty((V, K), dtype=x.dtype, device=dev) if dw else None
+        nbytes = _ce_bwd_workspace(M, K, V, code)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        st = lib.moe_linear_ce_bwd(_ptr(d_loss), red, _ptr(total) if reduction == "mean" else None, _ptr(x), _ptr(W),
+                                   _ptr(targets), bits, _ptr(lse), M, K, V, z_weight, _ptr(dX), _ptr(dW), code,
+                                   _ptr(ws), nbytes, raw)
+    _lib.check("moe_linear_ce_bwd", st)
+    return dX, dW
 
 
 # ---- the optimizer's step -----------------------------------------------------------------------
@@ -1083,3 +1169,31 @@ def linear(x, W, bias=None, *, act="none", residual=None, out_dtype=None):
     """Differentiable dense layer act(x W^T + bias) + residual of
     ``moe_linear_fwd``; gradients reach x, W, bias and residual."""
     return LinearFunction.apply(x, W, bias, act, residual, out_dtype, torch.is_grad_enabled())
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, targets, z_weight, reduction):
+        x, W, targets = x.detach().contiguous(), W.detach().contiguous(), targets.contiguous()
+        total = None if reduction == "none" else torch.empty(3, dtype=torch.float32, device=x.device)
+        loss, lse = moe_linear_ce_fwd(x, W, targets, z_weight=z_weight, total=total)
+        ctx.save_for_backward(x, W, targets, lse, total)
+        ctx.opts = dict(z_weight=z_weight, reduction=reduction)
+        # (a copy: the number is saved for the backward)
+        return loss if total is None else total[0 if reduction == "sum" else 2].clone()
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        x, W, targets, lse, total = ctx.saved_tensors
+        nx, nw = ctx.needs_input_grad[:2]
+        dX, dW = moe_linear_ce_bwd(g.contiguous(), x, W, targets, lse, total=total, dx=nx, dw=nw, **ctx.opts)
+        return dX, dW, None, None, None
+
+
+def linear_cross_entropy(x, W, targets, *, z_weight=0.0, reduction="mean"):
+    """Differentiable cross entropy of the logits x W^T (``moe_linear_ce_fwd``),
+    which are not kept: float32 losses [M] ("none"), their sum or their mean over
+    the rows whose target is in [0, V).  Gradients reach x and W."""
+    _option(MOE_REDUCTIONS, reduction, "reduction")
+    return LinearCrossEntropyFunction.apply(x, W, targets, z_weight, reduction)

@@ -170,7 +170,7 @@ const char *const kFamilies[] = {"build_schedule", "fill_zero", "grouped_gemm", 
                                  "fused_fwd_fp8", "gated_bwd_dw_down", "gated_bwd_dh",
                                  "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx", "route_fwd",
                                  "route_bwd", "router_loss_fwd", "router_loss_bwd", "linear_fwd",
-                                 "linear_bwd", "adamw"};
+                                 "linear_bwd", "linear_ce_fwd", "linear_ce_bwd", "adamw"};
 constexpr int kNumFamilies = sizeof(kFamilies) / sizeof(kFamilies[0]);
 
 struct Timing {
@@ -216,7 +216,7 @@ hipError_t timed(int fam, hipStream_t st, F &&f) {
 
 enum { F_SCHED = 0, F_FILL, F_BARE, F_FWD, F_DX, F_DW, F_TILEMAP, F_GATED_UP, F_GATED_DOWN,
        F_FWD_FP8, F_GB_DWD, F_GB_DH, F_GB_DX, F_GB_DWGU, F_FWD_MX, F_ROUTE_FWD, F_ROUTE_BWD,
-       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD, F_ADAMW };
+       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD, F_CE_FWD, F_CE_BWD, F_ADAMW };
 
 }  // namespace
 }  // namespace moe
@@ -645,6 +645,15 @@ int check_linear(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype, in
   if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return MOE_ERR_OPTION;
   return MOE_OK;
 }
+
+int check_ce(int64_t M, int64_t K, int64_t V, float z, int32_t target_bits, int32_t dtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (target_bits != 32 && target_bits != 64) return MOE_ERR_DTYPE;
+  if (M < 0 || K < 1 || V < 1) return MOE_ERR_SHAPE;
+  if (M > (1 << 24) || K > kMaxWidth || V > kMaxWidth) return MOE_ERR_LIMIT;
+  if (!isfinite(z)) return MOE_ERR_OPTION;
+  return MOE_OK;
+}
 }  // namespace
 }  // namespace moe
 
@@ -782,6 +791,58 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
   return hip_status(timed(F_LIN_BWD, st, [&] {
     return launch_linear_bwd(d_out, x, W, z, dX, dW, d_bias, (int)M, (int)K, (int)N, act, dtype,
                              out_dtype, workspace, st);
+  }));
+}
+
+size_t moe_linear_ce_fwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype) {
+  if (M == 0 || check_ce(M, K, V, 0.f, 32, dtype)) return 0;
+  return align256(linear_ce_fwd_workspace(M, K, V, dtype));
+}
+
+int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t target_bits,
+                      int64_t M, int64_t K, int64_t V, float z_weight, float *loss, float *lse,
+                      float *total, int32_t dtype, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+  int rc = check_ce(M, K, V, z_weight, target_bits, dtype);
+  if (rc) return rc;
+  if (M > 0 && (!x || !W || !targets || !loss || !lse)) return MOE_ERR_NULL;
+  const size_t need = moe_linear_ce_fwd_workspace_bytes(M, K, V, dtype), es = esize(dtype);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned(x, es) || !aligned(W, es) || !aligned(targets, target_bits / 8) || !aligned(loss, 4) ||
+      !aligned(lse, 4) || !aligned(total, 4) || (need && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_CE_FWD, st, [&] {
+    return launch_linear_ce_fwd(x, W, targets, target_bits == 64, M, K, V, z_weight, loss, lse, total, dtype,
+                                workspace, st);
+  }));
+}
+
+size_t moe_linear_ce_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype) {
+  if (M == 0 || check_ce(M, K, V, 0.f, 32, dtype)) return 0;
+  return align256(linear_ce_bwd_workspace(M, K, V, dtype));
+}
+
+int moe_linear_ce_bwd(const float *d_loss, int32_t reduction, const float *total, const void *x,
+                      const void *W, const void *targets, int32_t target_bits, const float *lse,
+                      int64_t M, int64_t K, int64_t V, float z_weight, void *dX, void *dW,
+                      int32_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_ce(M, K, V, z_weight, target_bits, dtype);
+  if (rc) return rc;
+  if (reduction < MOE_REDUCE_NONE || reduction > MOE_REDUCE_MEAN) return MOE_ERR_OPTION;
+  if (!dX && !dW) return MOE_OK;
+  if (M > 0 && (!d_loss || !x || !W || !targets || !lse || (reduction == MOE_REDUCE_MEAN && !total)))
+    return MOE_ERR_NULL;
+  const size_t need = moe_linear_ce_bwd_workspace_bytes(M, K, V, dtype), es = esize(dtype);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned(x, es) || !aligned(W, es) || !aligned(targets, target_bits / 8) || !aligned(d_loss, 4) ||
+      !aligned(lse, 4) || !aligned(total, 4) || !aligned(dX, es) || !aligned(dW, es) ||
+      (need && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_CE_BWD, st, [&] {
+    return launch_linear_ce_bwd(d_loss, reduction, total, x, W, targets, target_bits == 64, lse, M, K, V, z_weight,
+                                dX, dW, dtype, workspace, st);
   }));
 }
 

@@ -190,6 +190,15 @@ hipError_t launch_linear_bwd(const void *dout, const void *x, const void *W, con
                              void *dX, void *dW, void *db, int M, int K, int N, int act, int dtype,
                              int out_dtype, void *ws, hipStream_t st);
 
+// cross entropy of x W^T (wide: 64-bit targets)
+size_t linear_ce_fwd_workspace(int64_t M, int64_t K, int64_t V, int dtype);
+size_t linear_ce_bwd_workspace(int64_t M, int64_t K, int64_t V, int dtype);
+hipError_t launch_linear_ce_fwd(const void *x, const void *W, const void *targets, bool wide, int64_t M, int64_t K, int64_t V,
+                                float z, float *loss, float *lse, float *total, int dtype, void *ws, hipStream_t st);
+hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float *total, const void *x, const void *W,
+                                const void *targets, bool wide, const float *lse, int64_t M, int64_t K, int64_t V, float z,
+                                void *dX, void *dW, int dtype, void *ws, hipStream_t st);
+
 // optimizer step
 struct AdamwOptions {
   double lr, beta1, beta2, eps, weight_decay;

@@ -1,0 +1,363 @@
+// Cross entropy of the logits l = x W^T over a large vocabulary, and its gradient, without keeping them:
+//   lse_m = log sum_v exp l_mv,   loss_m = lse_m - l_m,t + z lse_m^2,
+//   dl_mv = g_m ((1 + 2 z lse_m) exp(l_mv - lse_m) - [v = t_m]),   dX = dl W,   dW = dl^T x.
+//
+// Forward: the product's tiles keep their logits in registers and leave per row the largest and the sum of
+// exp(l - largest) of their columns (linear.hip, ce_stats); the parts of a row are joined here.  Backward:
+// the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
+// logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
+// fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it.
+// What cannot take those tiles (fp32, rows off 16-byte lines, few rows, short vocabularies whose reduction is
+// better split) writes a piece's logits in fp32 to the workspace and reads them back.
+#include "cross_entropy.hpp"
+
+namespace moe {
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+bool on_line(const void *p) { return (uintptr_t)p % 16 == 0; }
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+MOE_DEV void st(float *p, float v) { *p = v; }
+MOE_DEV void st(bf16_t *p, float v) { *p = __builtin_bit_cast(bf16_t, (__bf16)v); }
+
+// ---- logits in memory ---------------------------------------------------------
+constexpr int CHUNK = 2048;  // columns of a row that a workgroup takes
+constexpr int kGrid = 1 << 16;
+
+// part[chunk][m] of a piece of n columns; pieces after the first are joined to what is there
+__global__ __launch_bounds__(256) void stats_kernel(const float *__restrict__ l, CeArgs a, int64_t M, int n, int chunks) {
+  __shared__ float2 red[4];
+  const int64_t total = M * chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int64_t m = b / chunks;
+    const int c = (int)(b - m * chunks), hi = min(n, (c + 1) * CHUNK);
+    float v[CHUNK / 256], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < CHUNK / 256; ++i) {
+      const int col = c * CHUNK + i * 256 + threadIdx.x;
+      v[i] = col < hi ? l[m * n + col] : -INFINITY;
+      top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const float base = ce_base(top);
+#pragma unroll
+    for (int i = 0; i < CHUNK / 256; ++i) sum += expf(v[i] - base);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = float2{top, sum};
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float2 r = ce_join(ce_join(red[0], red[1]), ce_join(red[2], red[3]));
+      float2 *at = a.part + (int64_t)c * M + m;
+      *at = a.col0 ? ce_join(*at, r) : r;
+      const int t = ce_target(a, m);
+      if (t >= c * CHUNK && t < hi) a.target_logit[m] = l[m * n + t];
+    }
+    __syncthreads();
+  }
+}
+
+// dl of a piece, zeros behind it up to its row length; fp32 takes the exact exponential (the hardware's is off by some 2^-21 at |l - lse| = 10)
+template <typename T>
+__global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, CeArgs a, T *__restrict__ dl, int64_t M,
+                                                 int n, int chunks) {
+  const int64_t total = M * chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int64_t m = b / chunks;
+    const int c = (int)(b - m * chunks), hi = min(n, (c + 1) * CHUNK);
+    const CeRow r = a.rows[m];
+    if (hi == n && threadIdx.x < a.ld - n) st(dl + m * a.ld + n + threadIdx.x, 0.f);
+#pragma unroll
+    for (int i = 0; i < CHUNK / 256; ++i) {
+      const int col = c * CHUNK + i * 256 + threadIdx.x;
+      if (col >= hi) break;
+      float d = 0.f;
+      if constexpr (sizeof(T) == 2) {
+        d = ce_dl(r, l[m * n + col], a.col0 + col);
+      } else if (r.target >= 0) {
+        d = r.scale * expf(l[m * n + col] - r.lse);
+        if (a.col0 + col == r.target) d -= r.g;
+      }
+      st(dl + m * a.ld + col, d);
+    }
+  }
+}
+
+// ---- rows -------------------------------------------------------------------------
+// loss and lse from a row's parts.  LANES = 64: a wave per row, 4 rows per workgroup; 4: a workgroup takes
+// 64 rows, whose parts lie side by side, 4 threads each (from M = 2048 on: lines are then read whole).
+template <int LANES>
+__global__ __launch_bounds__(256) void join_kernel(CeArgs a, int64_t M, int parts, float z, float *loss, float *lse) {
+  __shared__ float2 red[4][64];
+  const int lane = LANES == 64 ? threadIdx.x & 63 : threadIdx.x >> 6;
+  const int64_t m = LANES == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  float2 r{-INFINITY, 0.f};
+  if (m < M)
+    for (int p = lane; p < parts; p += LANES) r = ce_join(r, a.part[(int64_t)p * M + m]);
+  if constexpr (LANES == 64) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) r = ce_join(r, float2{__shfl_xor(r.x, d, 64), __shfl_xor(r.y, d, 64)});
+  } else {
+    red[lane][threadIdx.x & 63] = r;
+    __syncthreads();
+    r = ce_join(ce_join(red[0][threadIdx.x & 63], red[1][threadIdx.x & 63]),
+                ce_join(red[2][threadIdx.x & 63], red[3][threadIdx.x & 63]));
+  }
+  if (lane || m >= M) return;
+  const float v = r.x + logf(r.y);
+  lse[m] = v;
+  loss[m] = ce_target_id(a, m) < 0 ? 0.f : v - a.target_logit[m] + z * v * v;
+}
+
+// {sum of loss, rows that count, sum / rows}; sums in 64 bits, in a fixed order
+__global__ __launch_bounds__(1024) void total_kernel(CeArgs a, int64_t M, const float *__restrict__ loss, float *total) {
+  __shared__ double s[16];
+  __shared__ int64_t c[16];
+  double sum = 0;
+  int64_t count = 0;
+  for (int64_t m = threadIdx.x; m < M; m += 1024) {
+    if (ce_target_id(a, m) < 0) continue;
+    sum += loss[m];
+    ++count;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    sum += __shfl_xor(sum, d, 64);
+    count += __shfl_xor((long long)count, d, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    s[threadIdx.x >> 6] = sum;
+    c[threadIdx.x >> 6] = count;
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) {
+    sum += s[i];
+    count += c[i];
+  }
+  total[0] = (float)sum;
+  total[1] = (float)count;
+  total[2] = count ? (float)(sum / (double)count) : 0.f;
+}
+
+__global__ __launch_bounds__(256) void rows_kernel(CeArgs a, int64_t M, const float *d_loss, const float *lse,
+                                                   const float *total, int reduction, float z, CeRow *rows) {
+  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (m >= M) return;
+  const int64_t t = ce_target_id(a, m);
+  float g = d_loss[reduction == MOE_REDUCE_NONE ? m : 0];
+  if (reduction == MOE_REDUCE_MEAN) g /= total[1];
+  const float v = lse[m];
+  rows[m] = CeRow{v, g * (1.f + 2.f * z * v), g, (int)t};
+}
+
+__global__ __launch_bounds__(256) void round_kernel(const float *__restrict__ x, bf16_t *__restrict__ y, int64_t n, bool wide) {
+  const int64_t step = (int64_t)gridDim.x * 1024;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += step) {
+    if (wide && i + 4 <= n) {
+      const f32x4 v = *(const f32x4 *)(x + i);
+      *(bf16x4 *)(y + i) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    } else {
+      for (int e = 0; e < 4 && i + e < n; ++e) st(y + i + e, x[i + e]);
+    }
+  }
+}
+
+// ---- pieces and workspaces, from the sizes alone -----------------------------------
+int64_t even_piece(int64_t V, int64_t most) {  // equal pieces of whole tiles, of at most `most` columns (>= 256)
+  if (V <= most) return V;
+  const int64_t count = (V + most - 1) / most;
+  const int64_t p = ((V + count - 1) / count + 255) / 256 * 256;
+  return p <= most ? p : most / 256 * 256;
+}
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t greatest(int64_t a, int64_t b) { return a > b ? a : b; }
+int64_t weight_piece(int64_t K) { return greatest(256, least(((int64_t)1 << 30) / K - 1, 1 << 20) / 256 * 256); }
+
+struct Fwd {
+  bool tiles;
+  int64_t piece;
+  int parts;
+  size_t part, logits, gemm, total;  // offsets of the parts (after the targets' logits), ...
+};
+Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, bool tiles, bool spare) {
+  Fwd f;
+  f.tiles = tiles;
+  f.part = up256((size_t)M * 4);
+  if (tiles) {
+    f.piece = even_piece(V, weight_piece(K));
+    f.parts = 0;
+    const int bn = ce_tile_columns(M, K, f.piece);
+    for (int64_t v = 0; v < V; v += f.piece) f.parts += (int)((least(f.piece, V - v) + bn - 1) / bn);
+    f.logits = f.gemm = f.total = f.part + up256((size_t)f.parts * M * 8);
+    return f;
+  }
+  // 256 MB of logits; 1024 columns where only operands off their lines come here
+  f.piece = even_piece(V, spare ? 1024 : greatest(1024, ((int64_t)1 << 26) / M / 256 * 256));
+  f.parts = (int)((f.piece + CHUNK - 1) / CHUNK);
+  f.logits = f.part + up256((size_t)f.parts * M * 8);
+  f.gemm = f.logits + up256((size_t)M * f.piece * 4);
+  size_t g = 0;
+  for (int64_t n : {f.piece, V % f.piece}) {
+    if (!n) continue;
+    const size_t b = ce_part_bytes(M, n, K, dtype);
+    g = b > g ? b : g;
+  }
+  f.total = f.gemm + up256(g);
+  return f;
+}
+bool fwd_tiles(int64_t M, int64_t K, int64_t V, int dtype) {
+  return dtype == MOE_BF16 && ce_tiles(M, K, even_piece(V, weight_piece(K)));
+}
+
+struct Bwd {
+  bool tiles;
+  int64_t piece;
+  size_t dl, sum, logits, gemm, total;  // offsets after the rows
+};
+// 256 MB of dl in bf16
+int64_t bwd_piece(int64_t M, int64_t K, int64_t V) {
+  const int64_t most = greatest(256, ((int64_t)1 << 27) / M / 256 * 256);
+  return even_piece(V, least(most, weight_piece(K)));
+}
+int64_t bwd_ld(int64_t piece) { return (piece + 7) / 8 * 8; }
+// Whether dl's rows may be filled up to 16-byte lines: the products that read it then take chunked loads, which
+// look at no column past the end but those zeros (the loads of four elements of other tiles would pass the buffer's)
+bool bwd_lines(int64_t M, int64_t K, int64_t V, int dtype) {
+  const int64_t p = bwd_ld(bwd_piece(M, K, V)), most = (int64_t)1 << 30;
+  return dtype == MOE_BF16 && K % 8 == 0 && K <= (1 << 20) && p <= (1 << 20) && M * p < most && M * K < most && p * K < most;
+}
+bool bwd_tiles(int64_t M, int64_t K, int64_t V, int dtype) {
+  return bwd_lines(M, K, V, dtype) && ce_tiles(M, K, bwd_piece(M, K, V));
+}
+Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, bool tiles, bool spare) {
+  const size_t es = dtype == MOE_F32 ? 4 : 2;
+  Bwd w;
+  w.tiles = tiles;
+  w.piece = spare ? even_piece(V, 1024) : bwd_piece(M, K, V);
+  w.dl = up256((size_t)M * sizeof(CeRow));
+  w.sum = w.dl + up256((size_t)M * bwd_ld(w.piece) * es);
+  w.logits = w.sum + (w.piece < V && dtype == MOE_BF16 ? up256((size_t)M * K * 4) : 0);
+  w.gemm = w.logits + (tiles ? 0 : up256((size_t)M * w.piece * 4));
+  size_t g = 0;
+  for (int64_t n : {w.piece, V % w.piece}) {
+    if (!n) continue;
+    for (size_t b : {tiles ? 0 : ce_part_bytes(M, n, K, dtype), ce_part_bytes(M, K, n, dtype), ce_part_bytes(n, K, M, dtype)})
+      g = b > g ? b : g;
+  }
+  w.total = w.gemm + up256(g);
+  return w;
+}
+
+int chunk_grid(int64_t M, int chunks) { return (int)least(M * chunks, kGrid); }
+
+}  // namespace
+
+size_t linear_ce_fwd_workspace(int64_t M, int64_t K, int64_t V, int dtype) {
+  const bool t = fwd_tiles(M, K, V, dtype);
+  const size_t a = fwd_space(M, K, V, dtype, false, t).total, b = t ? fwd_space(M, K, V, dtype, true, false).total : 0;
+  return a > b ? a : b;
+}
+size_t linear_ce_bwd_workspace(int64_t M, int64_t K, int64_t V, int dtype) {
+  const bool t = bwd_tiles(M, K, V, dtype);
+  const size_t a = bwd_space(M, K, V, dtype, false, t).total, b = t ? bwd_space(M, K, V, dtype, true, false).total : 0;
+  return a > b ? a : b;
+}
+
+hipError_t launch_linear_ce_fwd(const void *x, const void *W, const void *targets, bool wide, int64_t M, int64_t K, int64_t V,
+                                float z, float *loss, float *lse, float *total, int dtype, void *ws, hipStream_t st) {
+  CeArgs a{};
+  a.targets = targets;
+  a.wide = wide;
+  a.V = V;
+  hipError_t e = hipSuccess;
+  if (M > 0) {
+    const bool sized = fwd_tiles(M, K, V, dtype), tiles = sized && on_line(x) && on_line(W);
+    const Fwd f = fwd_space(M, K, V, dtype, tiles, sized && !tiles);
+    const size_t es = dtype == MOE_F32 ? 4 : 2;
+    a.target_logit = (float *)ws;
+    a.part = (float2 *)((char *)ws + f.part);
+    float *logits = (float *)((char *)ws + f.logits);
+    const int bn = tiles ? ce_tile_columns(M, K, f.piece) : 1;
+    for (int64_t v = 0; v < V && e == hipSuccess; v += f.piece) {
+      const int n = (int)least(f.piece, V - v);
+      const char *w = (const char *)W + (size_t)v * K * es;
+      a.col0 = v;
+      if (tiles) {
+        e = launch_ce_tiles(x, w, nullptr, a, (int)M, (int)K, n, (int)f.piece, st);
+        a.part0 += (n + bn - 1) / bn;
+        continue;
+      }
+      e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32,
+                            (char *)ws + f.gemm, st);
+      if (e != hipSuccess) break;
+      const int chunks = (n + CHUNK - 1) / CHUNK;
+      stats_kernel<<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, M, n, chunks);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+    a.col0 = 0;
+    if (M < 2048) join_kernel<64><<<(int)((M + 3) / 4), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
+    else join_kernel<4><<<(int)((M + 63) / 64), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && total) {
+    total_kernel<<<1, 1024, 0, st>>>(a, M, loss, total);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float *total, const void *x, const void *W,
+                                const void *targets, bool wide, const float *lse, int64_t M, int64_t K, int64_t V, float z,
+                                void *dX, void *dW, int dtype, void *ws, hipStream_t st) {
+  const size_t es = dtype == MOE_F32 ? 4 : 2;
+  if (M == 0) return dW ? launch_fill_zero(dW, (size_t)V * K * es, nullptr, 0, st) : hipSuccess;
+  const bool on = on_line(x) && on_line(W), sized = bwd_tiles(M, K, V, dtype), tiles = sized && on;
+  const bool lines = on && bwd_lines(M, K, V, dtype);
+  const Bwd b = bwd_space(M, K, V, dtype, tiles, sized && !tiles);
+  CeArgs a{};
+  a.targets = targets;
+  a.wide = wide;
+  a.V = V;
+  a.rows = (const CeRow *)ws;
+  void *dl = (char *)ws + b.dl;
+  float *sum = dtype == MOE_F32 ? (float *)dX : (float *)((char *)ws + b.sum);
+  float *logits = (float *)((char *)ws + b.logits);
+  void *part = (char *)ws + b.gemm;
+  rows_kernel<<<(int)((M + 255) / 256), 256, 0, st>>>(a, M, d_loss, lse, total, reduction, z, (CeRow *)ws);
+  hipError_t e = hipGetLastError();
+  const bool once = b.piece >= V;
+  for (int64_t v = 0; v < V && e == hipSuccess; v += b.piece) {
+    const int n = (int)least(b.piece, V - v);
+    const char *w = (const char *)W + (size_t)v * K * es;
+    a.col0 = v;
+    a.ld = lines ? bwd_ld(n) : n;
+    if (tiles) {
+      e = launch_ce_tiles(x, w, dl, a, (int)M, (int)K, n, (int)b.piece, st);
+    } else {
+      e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32, part, st);
+      if (e != hipSuccess) break;
+      const int chunks = (n + CHUNK - 1) / CHUNK;
+      if (dtype == MOE_F32) dl_kernel<float><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);
+      else dl_kernel<bf16_t><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && dW)
+      e = launch_ce_dw(dl, a.ld, x, (char *)dW + (size_t)v * K * es, (int)M, (int)K, n, dtype, part, st);
+    if (e == hipSuccess && dX)
+      e = launch_ce_dx(dl, a.ld, w, v ? sum : nullptr, once ? dX : sum, !once, (int)M, (int)K, n, dtype, part, st);
+  }
+  if (e == hipSuccess && dX && !once && dtype == MOE_BF16) {
+    const int64_t n = M * K;
+    round_kernel<<<(int)least((n + 1023) / 1024, 8192), 256, 0, st>>>(sum, (bf16_t *)dX, n, (uintptr_t)dX % 8 == 0);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace moe

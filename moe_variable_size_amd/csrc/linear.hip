@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "cross_entropy.hpp"
 #include "linear_plan.hpp"
 
 namespace moe {
@@ -478,6 +479,7 @@ struct PipeArgs {
   uint32_t a_bytes, b_bytes;
   int tm, tn, splits;  // tiles; reduction ranges (> 1: fp32 partial products to part)
   float *part;         // [splits][M][N]
+  CeArgs ce;           // the cross entropy's epilogues alone
 };
 
 // Epilogue of a workgroup's tile, half the rows at a time through LDS as fp32 [WA][BN], so that each
@@ -545,6 +547,112 @@ MOE_DEV void tile_epilogue(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2
             finish1<bf16_t, To, ACT>(p, v + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
         }
       }
+    }
+  }
+}
+
+// ---- the cross entropy's epilogues (cross_entropy.hip) ----------------------------
+// Logits l = x W^T stay in the accumulators.  The forward leaves the largest value and the sum of
+// exponentials of a tile's columns for each row, and the target's logit; the backward leaves dl.
+constexpr int kCeStats = 16, kCeGrad = 17;  // in the place of an activation
+
+// A lane holds 4 HN columns per half of 2 HM rows: its own maximum and sum first, then the 4 lanes of a row,
+// then the WGN waves through LDS.
+template <int HM, int HN, int WGM, int WGN>
+MOE_DEV void ce_stats(const PipeArgs &q, char *lds, f32x4 (&acc)[2][2][HM][HN], int wm, int wn, int m0, int n0,
+                      int nb) {
+  constexpr int BM = 32 * HM * WGM, WA = BM / 2, WB = 16 * HN * WGN;
+  const GemmArgs &p = q.g;
+  const int lane = threadIdx.x & 63;
+  float2 *red = (float2 *)lds;  // [WGN][BM]
+  __syncthreads();
+#pragma unroll
+  for (int mh = 0; mh < 2; ++mh)
+#pragma unroll
+    for (int i = 0; i < HM; ++i) {
+      const int r = mh * WA + wm * 16 * HM + i * 16 + (lane & 15), m = m0 + r;
+      int t = m < p.M ? ce_target(q.ce, m) : -1;
+      if (t >= p.N) t = -1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int nh = 0; nh < 2; ++nh)
+#pragma unroll
+        for (int j = 0; j < HN; ++j) {
+          const int n = n0 + nh * WB + wn * 16 * HN + j * 16 + 4 * (lane >> 4);
+          f32x4 &a = acc[mh][nh][i][j];
+          if (t >= n && t < n + 4) {
+            const int e = t - n;
+            q.ce.target_logit[m] = e == 0 ? a[0] : e == 1 ? a[1] : e == 2 ? a[2] : a[3];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = n + e < p.N ? a[e] : -INFINITY;
+            top = fmaxf(top, a[e]);
+          }
+        }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float base = ce_base(top);
+      float sum = 0.f;
+#pragma unroll
+      for (int nh = 0; nh < 2; ++nh)
+#pragma unroll
+        for (int j = 0; j < HN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += __expf(acc[mh][nh][i][j][e] - base);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (lane < 16) red[wn * BM + r] = float2{top, sum};
+    }
+  __syncthreads();
+  const int r = threadIdx.x;
+  if (r < BM && m0 + r < p.M) {
+    float2 a = red[r];
+#pragma unroll
+    for (int w = 1; w < WGN; ++w) a = ce_join(a, red[w * BM + r]);
+    q.ce.part[(int64_t)(q.ce.part0 + nb) * p.M + m0 + r] = a;
+  }
+}
+
+// dl in bf16, as the products that follow take it, half the rows at a time through LDS as in tile_epilogue;
+// zeros in the columns that fill up its rows
+template <int HM, int HN, int WGM, int WGN>
+MOE_DEV void ce_grad(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2][HM][HN], int wm, int wn, int m0, int n0) {
+  constexpr int BM = 32 * HM * WGM, BN = 32 * HN * WGN, WA = BM / 2, WB = BN / 2;
+  const GemmArgs &p = q.g;
+  const int lane = threadIdx.x & 63;
+  auto chunk = [&](int r, int c) __attribute__((always_inline)) {
+    return (f32x4 *)(lds + r * (BN * 4) + ((c ^ (r & 15)) << 4));
+  };
+  constexpr int LPR = BN / 8, RPP = 512 / LPR;
+#pragma unroll
+  for (int mh = 0; mh < 2; ++mh) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int nh = 0; nh < 2; ++nh)
+#pragma unroll
+        for (int j = 0; j < HN; ++j)
+          *chunk(wm * 16 * HM + i * 16 + (lane & 15),
+                 (nh * WB + wn * 16 * HN + j * 16) / 4 + (lane >> 4)) = acc[mh][nh][i][j];
+    __syncthreads();
+    const int r0 = threadIdx.x / LPR, c0 = (threadIdx.x % LPR) * 8, n = n0 + c0;
+    if (n >= q.ce.ld) continue;
+#pragma unroll 4
+    for (int r = r0; r < WA; r += RPP) {
+      const int m = m0 + mh * WA + r;
+      if (m >= p.M) break;
+      const CeRow row = q.ce.rows[m];
+      f32x4 v[2] = {*chunk(r, c0 / 4), *chunk(r, c0 / 4 + 1)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = n + 4 * h + e;
+          v[h][e] = col < p.N ? ce_dl(row, v[h][e], q.ce.col0 + col) : 0.f;
+        }
+      put8((bf16_t *)p.out + (int64_t)m * q.ce.ld + n, v);
     }
   }
 }
@@ -661,7 +769,9 @@ __global__ __launch_bounds__(512, 2) void piped_gemm(PipeArgs q) {
   // zeros for stages that are not there, and the last early read, before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 
-  tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
+  if constexpr (ACT == kCeStats) ce_stats<HM, HN, WGM, WGN>(q, lds, acc, wm, wn, m0, n0, nb);
+  else if constexpr (ACT == kCeGrad) ce_grad<HM, HN, WGM, WGN>(q, lds, acc, wm, wn, m0, n0);
+  else tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
 }
 
 // The same product with 128 x 128 tiles for problems whose 256-wide tiles leave CUs idle: 8 waves of
@@ -749,7 +859,9 @@ __global__ __launch_bounds__(512, NST == 2 ? 4 : 2) void ring_gemm(PipeArgs q) {
     multiply(1);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
+  if constexpr (ACT == kCeStats) ce_stats<HM, HN, WGM, WGN>(q, lds, acc, wm, wn, m0, n0, nb);
+  else if constexpr (ACT == kCeGrad) ce_grad<HM, HN, WGM, WGN>(q, lds, acc, wm, wn, m0, n0);
+  else tile_epilogue<HM, HN, WGM, WGN, To, ACT>(q, lds, acc, wm, wn, m0, n0, split);
 }
 
 // ---- streamed products: few rows or few columns --------------------------------
@@ -1023,7 +1135,7 @@ hipError_t run_piped(PipeArgs &q, int shape, int act, hipStream_t st) {
   q.tn = (q.g.N + bn - 1) / bn;
   const int grid = q.tm * q.tn * q.splits;
   hipError_t e = hipSuccess;
-  by_act_of<AK && BKM>(act, [&](auto A) {
+  auto run = [&](auto A) {
     constexpr int ACT = decltype(A)::value;
     if (shape == 0)
       e = launch_lds<piped_gemm<4, 2, 2, 4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
@@ -1033,7 +1145,20 @@ hipError_t run_piped(PipeArgs &q, int shape, int act, hipStream_t st) {
       e = launch_lds<ring_gemm<4, AK, BKM, To, ACT>>(grid, 128 << 10, q, st);
     else
       e = launch_lds<ring_gemm<2, AK, BKM, To, ACT>>(grid, 64 << 10, q, st);
-  });
+  };
+  if constexpr (AK && BKM && sizeof(To) == 2) {
+    if (act == kCeGrad) {
+      run(std::integral_constant<int, kCeGrad>());
+      return e;
+    }
+  }
+  if constexpr (AK && BKM && sizeof(To) == 4) {
+    if (act == kCeStats) {
+      run(std::integral_constant<int, kCeStats>());
+      return e;
+    }
+  }
+  by_act_of<AK && BKM>(act, run);
   return e;
 }
 
@@ -1202,6 +1327,39 @@ hipError_t bwd(const void *dout, const void *x, const void *W, const void *z, vo
 }
 
 }  // namespace
+
+// ---- products of the linear cross entropy ------------------------------------------
+bool ce_tiles(int64_t M, int64_t K, int64_t V) {
+  const int64_t most = (int64_t)kOobOffset / 2;
+  return M > 16 && K % 8 == 0 && K <= (1 << 20) && V <= (1 << 20) && M * K < most && V * K < most &&
+         ((M + 127) / 128) * ((V + 127) / 128) <= (1 << 22) && plan_of(M, V, K).splits == 1;
+}
+int ce_tile_columns(int64_t M, int64_t K, int64_t V) { return kShapeN[unsplit_shape(M, V, K)]; }
+hipError_t launch_ce_tiles(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v,
+                           hipStream_t st) {
+  PipeArgs q{};
+  q.g = GemmArgs{x, W, nullptr, nullptr, dl, nullptr, M, V, K, K, K, false};
+  q.a_bytes = (uint32_t)((int64_t)M * K * 2);
+  q.b_bytes = (uint32_t)((int64_t)V * K * 2);
+  q.splits = 1;
+  q.ce = ce;
+  const int shape = unsplit_shape(M, shape_v, K);
+  return dl ? run_piped<true, true, bf16_t>(q, shape, kCeGrad, st) : run_piped<true, true, float>(q, shape, kCeStats, st);
+}
+size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype) { return part_bytes(M, N, K, dtype == MOE_BF16); }
+hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
+                        int V, int dtype, void *part, hipStream_t st) {
+  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false};
+  if (dtype == MOE_F32) return gemm<true, false, float, float>(a, MOE_ACT_NONE, part, st);
+  if (out_f32) return gemm<true, false, bf16_t, float>(a, MOE_ACT_NONE, part, st);
+  return gemm<true, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
+}
+hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, void *dW, int M, int K, int V, int dtype, void *part,
+                        hipStream_t st) {
+  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false};
+  if (dtype == MOE_F32) return gemm<false, false, float, float>(a, MOE_ACT_NONE, part, st);
+  return gemm<false, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
+}
 
 size_t linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype) {
   return part_bytes(M, N, K, dtype == MOE_BF16);

@@ -49,6 +49,22 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   }
   return best;
 }
+// The shape of the same estimate for a product that cannot split its reduction (its epilogue needs the sums).
+inline int unsplit_shape(int64_t M, int64_t N, int64_t K) {
+  const int64_t stages = (K + PBK - 1) / PBK;
+  int best = 0;
+  double least = 0;
+  for (int sh = 0; sh < 3; ++sh) {
+    const double wgs = (double)((M + kShapeM[sh] - 1) / kShapeM[sh]) * ((N + kShapeN[sh] - 1) / kShapeN[sh]);
+    const double t = sh == 2 ? (wgs <= 256 ? 0.5 : __builtin_ceil(wgs / 512)) * stages
+                             : __builtin_ceil(wgs / 256) * stages * (sh == 0 ? 1.35 : 0.92);
+    if (least == 0 || t < least) {
+      least = t;
+      best = sh;
+    }
+  }
+  return best;
+}
 // The staged kernel's: bf16 takes 128 x 128 tiles (S = 2) where they fill the chip twice; else, and in fp32
 // always, 64 x 64 (timed in turn, fp32 4096^3: 1072 us against 1236, 8192 x 2048 x 2048 510 against 626: the fp32
 // products are slow enough that the operands' traffic does not matter, and more waves share the CU), with

@@ -52,6 +52,51 @@ def test_adamw_rejects_before_launch(lib):
     assert lib.moe_adamw_step(None, 1, 1e-3, None, 0.9, 0.99, 1e-8, 0.0, 1, None, None, 0, 0, 0, 32, None) == 1
 
 
+def test_linear_ce_rejects_before_launch(lib):
+    def fwd(x=P, W=P, t=P, bits=32, M=10, K=8, V=20, z=0.0, loss=P, lse=P, total=None, dt=1, ws=P, nb=1 << 40):
+        return lib.moe_linear_ce_fwd(x, W, t, bits, M, K, V, z, loss, lse, total, dt, ws, nb, None)
+
+    def bwd(g=P, red=0, total=None, x=P, W=P, t=P, bits=64, lse=P, M=10, K=8, V=20, z=0.0, dX=P, dW=P, dt=0, ws=P, nb=1 << 40):
+        return lib.moe_linear_ce_bwd(g, red, total, x, W, t, bits, lse, M, K, V, z, dX, dW, dt, ws, nb, None)
+
+    for call in (fwd, bwd):
+        for name in ("x", "W", "t", "lse"):
+            assert call(**{name: None}) == 1
+            assert call(**{name: ODD}) == 4
+        assert call(K=0) == 2 and call(V=0) == 2 and call(M=-1) == 2
+        assert call(M=(1 << 24) + 1) == 7 and call(K=(1 << 22) + 1) == 7 and call(V=(1 << 22) + 1) == 7
+        assert call(dt=2) == 3 and call(bits=16) == 3
+        assert call(z=float("inf")) == 8
+        assert call(ws=None) == 5 and call(nb=8) == 5 and call(ws=ODD) == 4
+    assert fwd(loss=None) == 1 and fwd(total=ODD) == 4
+    assert bwd(g=None) == 1 and bwd(red=3) == 8 and bwd(red=2) == 1 and bwd(dX=ODD) == 4 and bwd(dW=ODD) == 4
+    assert bwd(dX=None, dW=None) == 0 and fwd(M=0, x=None, W=None, t=None) == 0
+    for q in (lib.moe_linear_ce_fwd_workspace_bytes, lib.moe_linear_ce_bwd_workspace_bytes):
+        assert q(10, 0, 20, 1) == 0 and q(10, 8, 20, 3) == 0 and q(0, 8, 20, 1) == 0
+        assert q(10, 8, 20, 1) > 0 and q(10, 8, 20, 1) % 256 == 0
+    # no logits: 8192 x 65536 of them would be a GiB in bf16
+    assert lib.moe_linear_ce_fwd_workspace_bytes(8192, 4096, 65536, 1) < 1 << 27
+    assert lib.moe_linear_ce_bwd_workspace_bytes(8192, 4096, 65536, 1) < 1 << 29
+
+
+def test_oracle_linear_ce_against_differences_and_torch():
+    rng = np.random.default_rng(0)
+    x, W = rng.standard_normal((7, 5)), rng.standard_normal((11, 5))
+    t, g = np.array([0, 10, -1, 11, 3, 4, 5]), rng.standard_normal(7)
+    loss, lse, total = O.linear_ce(x, W, t, 0.01)
+    assert loss[2] == loss[3] == 0 and total[1] == 5
+    want = torch.nn.functional.cross_entropy(torch.from_numpy(x @ W.T), torch.from_numpy(np.where(t < 11, t, -1)),
+                                             ignore_index=-1, reduction="none").numpy()
+    assert np.allclose(loss, want + np.where((t >= 0) & (t < 11), 0.01 * lse ** 2, 0), rtol=1e-12)
+    dX, dW, _ = O.linear_ce_bwd(g, x, W, t, 0.01)
+    u, v, h = rng.standard_normal(x.shape), rng.standard_normal(W.shape), 1e-5
+
+    def f(s):
+        return (g * O.linear_ce(x + s * h * u, W + s * h * v, t, 0.01)[0]).sum()
+
+    assert abs((f(1) - f(-1)) / (2 * h) - (dX * u).sum() - (dW * v).sum()) < 1e-8
+
+
 def test_oracle_e4m3_is_the_format():
     c = torch.arange(256, dtype=torch.uint8)
     want = c.view(torch.float8_e4m3fn).float().numpy()
