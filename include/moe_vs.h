@@ -501,6 +501,72 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
                    int32_t dtype, int32_t out_dtype, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ---- 4-bit weights ---------------------------------------------------------------- */
+
+/*
+ * Weights of 4 bits: W[e, n, k] = (q[e, n, k] - z[e, g, n]) s[e, g, n], q in 0 .. 15,
+ * g = k / group.  A descriptor (host struct, not kept) of device arrays, the
+ * experts behind each other:
+ *   codes  [E][N][ceil(K / 128) * 64] bytes, 16-byte aligned.  Element k of a row:
+ *          with i = k % 8, nibble i / 2 (even i) or 4 + i / 2 (odd i) of the
+ *          little-endian 32-bit word at byte 64 (k / 128) + 16 (k % 32 / 8) +
+ *          4 (k % 128 / 32) (nibble 0: the lowest bits).
+ *   scales [E][ceil(K / group)][C] bf16, 8-byte aligned, C = N rounded up to 16 (what
+ *          lies behind N enters no result).
+ *   zeros  as scales, uint8 0 .. 15 (any byte), 4-byte aligned; NULL: 8 everywhere.
+ * group 32, 64 or 128; 1 <= E <= 1024; K and N at most 2^22; one expert's codes
+ * below 2^31 bytes and its scales below 2^30 entries (MOE_ERR_LIMIT).
+ */
+typedef struct moe_w4_weight {
+  void *codes, *scales, *zeros;
+  int64_t N, K;
+  int32_t E, group;
+} moe_w4_weight;
+
+/*
+ * Codes, scales and, unless w->zeros is NULL, zero points from W [E, N, K] in
+ * `dtype` (MOE_F32 or MOE_BF16), any K: with lo <= 0 and hi >= 0 the smallest and
+ * largest of a group and 0, s = bf16((hi - lo) / 15), z = round(-lo / s) (without
+ * zeros: s = bf16(max |W| / 7), z = 8), q = round(W / s) + z, each kept within
+ * 0 .. 15; s = 0 where it would be below 2^-126.  For finite W.  Columns of scales
+ * and zeros behind N are not written.
+ */
+int moe_w4_quantize(const void *W, const moe_w4_weight *w, int32_t dtype, void *stream);
+
+/* W [E, N, K] in `dtype`, OVERWRITTEN: (q - z) s, rounded once. */
+int moe_w4_dequantize(const moe_w4_weight *w, void *W, int32_t dtype, void *stream);
+
+/*
+ * out = act(x W^T + bias) + residual for few rows (a decode batch): x [M, K], bias
+ * [N] or NULL in bf16, residual [M, N] or NULL and out [M, N] in `out_dtype` (MOE_BF16
+ * or MOE_F32), which may be the same buffer; w with E = 1; act as moe_linear_fwd.
+ * The weights' values are multiplied unrounded, sums are fp32.
+ *   K a multiple of 8 (MOE_ERR_SHAPE), x 16-byte aligned and below 2^31 bytes
+ *   (MOE_ERR_LIMIT); M may be 0.  The codes are read again for every 64 rows: from
+ *   some hundred rows on moe_w4_dequantize and moe_linear_fwd are faster.
+ */
+int moe_linear_w4_fwd(const void *x, const moe_w4_weight *w, const void *bias, const void *residual,
+                      void *out, int64_t M, int32_t act, int32_t out_dtype, void *stream);
+
+/*
+ * moe_fused_fwd with 4-bit weights: y[t] = sum_j w[t, j] x[t] W[ids[t, j]]^T, either
+ * layout; y [T, N] float, OVERWRITTEN (zeroed by the call, then accumulated
+ * atomically: bitwise reproducible for k <= 2).  x and K as moe_linear_w4_fwd;
+ * w->E = sched->E.  Made for few rows per expert (the codes are read again for
+ * every 16 or 32 of them).
+ */
+int moe_fused_fwd_w4(const void *x, const moe_w4_weight *w, const moe_schedule *sched, float *y,
+                     void *stream);
+
+/*
+ * The same for single tokens, without a schedule: expert_ids [T, k] int32 (outside
+ * [0, E): left out), topk_weights [T, k] float or NULL for 1.  One launch, no
+ * atomics (reproducible).  The codes are read once per assignment, so it is for T k
+ * up to about E; T may be 0, T k < 2^31, k <= 64.
+ */
+int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *expert_ids,
+                     const float *topk_weights, int64_t T, int32_t k, float *y, void *stream);
+
 /* ---- loss of a model's output layer ------------------------------------------- */
 
 /*

@@ -76,6 +76,20 @@ class MoeAdamwTensor(ctypes.Structure):
     ]
 
 
+class MoeW4Weight(ctypes.Structure):
+    """Mirror of ``struct moe_w4_weight``."""
+
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -111,6 +125,11 @@ SIGNATURES = {
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32, _I32]),
     "moe_linear_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
                                       _P, _SZ, _P]),
+    "moe_w4_quantize": (ctypes.c_int, [_P, _P, _I32, _P]),
+    "moe_w4_dequantize": (ctypes.c_int, [_P, _P, _I32, _P]),
+    "moe_linear_w4_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I32, _I32, _P]),
+    "moe_fused_fwd_w4": (ctypes.c_int, [_P, _P, _SCHED_P, _P, _P]),
+    "moe_token_fwd_w4": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _P]),
     "moe_linear_ce_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
     "moe_linear_ce_fwd": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _F32, _P, _P, _P, _I32, _P, _SZ, _P]),
     "moe_linear_ce_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),

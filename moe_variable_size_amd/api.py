@@ -721,6 +721,169 @@ def moe_linear_bwd(d_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, *, act
     return dX, dW, db
 
 
+# ---- 4-bit weights ----------------------------------------------------------------------------
+
+@dataclass
+class W4Weight:
+    """Weights of 4 bits (q - zero point) * scale in groups of ``group`` (32, 64
+    or 128) elements of a row: ``codes`` uint8 [N, ceil(K / 128) * 64], two to a
+    byte in the order of ``struct moe_w4_weight``, ``scales`` bfloat16
+    [ceil(K / group), N rounded up to 16] and ``zeros`` uint8 alike, or None for
+    zero points of 8; for experts all with a leading [E].
+    ``moe_w4_quantize`` makes one."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: Optional[torch.Tensor]
+    N: int
+    K: int
+    group: int = 128
+
+    @property
+    def E(self) -> Optional[int]:
+        """The number of experts, None for one dense weight."""
+        return self.codes.shape[0] if self.codes.dim() == 3 else None
+
+
+def _w4_shapes(lead, N, K, group):
+    return (*lead, N, -(-K // 128) * 64), (*lead, -(-K // group), -(-N // 16) * 16)
+
+
+def _w4_struct(w: W4Weight, index: int, experts: bool):
+    if not isinstance(w, W4Weight):
+        raise TypeError("the weight must be a W4Weight")
+    if w.group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {w.group}")
+    rank = 3 if experts else 2
+    _need(w.codes, "codes", torch.uint8, rank, index)
+    _need(w.scales, "scales", torch.bfloat16, rank, index)
+    codes, scales = _w4_shapes(w.codes.shape[:-2], w.N, w.K, w.group)
+    if tuple(w.codes.shape) != codes or tuple(w.scales.shape) != scales:
+        raise ValueError(f"codes must be {codes} and scales {scales}, got {tuple(w.codes.shape)} and {tuple(w.scales.shape)}")
+    if w.zeros is not None:
+        _need(w.zeros, "zeros", torch.uint8, rank, index)
+        if tuple(w.zeros.shape) != scales:
+            raise ValueError(f"zeros must be {scales}, got {tuple(w.zeros.shape)}")
+    return _lib.MoeW4Weight(_ptr(w.codes), _ptr(w.scales), _ptr(w.zeros), w.N, w.K, w.E or 1, w.group)
+
+
+def moe_w4_quantize(W: torch.Tensor, *, group: int = 128, symmetric: bool = False, stream=None) -> W4Weight:
+    """4-bit codes, scales and (unless ``symmetric``) zero points of W [N, K] or
+    [E, N, K], float32 or bfloat16: per group the range of its values and 0 in
+    15 steps, or their largest magnitude in 7."""
+    lib = _lib.load()
+    _need(W, "W", None, 3 if W.dim() == 3 else 2, -1)
+    code = _dtype_code(W)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    N, K = W.shape[-2:]
+    codes, scales = _w4_shapes(W.shape[:-2], N, K, group)
+    ctx, raw = _launch(W, stream)
+    with ctx:
+        w = W4Weight(torch.empty(codes, dtype=torch.uint8, device=W.device),
+                     torch.zeros(scales, dtype=torch.bfloat16, device=W.device),
+                     None if symmetric else torch.zeros(scales, dtype=torch.uint8, device=W.device), N, K, group)
+        st = lib.moe_w4_quantize(_ptr(W), ctypes.byref(_w4_struct(w, W.get_device(), W.dim() == 3)), code, raw)
+    _lib.check("moe_w4_quantize", st)
+    return w
+
+
+def moe_w4_dequantize(w: W4Weight, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
+    """The weights [N, K] or [E, N, K] that ``w`` stands for, rounded to dtype."""
+    lib = _lib.load()
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    c = _w4_struct(w, w.codes.get_device(), w.E is not None)
+    ctx, raw = _launch(w.codes, stream)
+    with ctx:
+        W = torch.empty((*w.codes.shape[:-1], w.K), dtype=dtype, device=w.codes.device)
+        st = lib.moe_w4_dequantize(ctypes.byref(c), _ptr(W), _DTYPES[dtype], raw)
+    _lib.check("moe_w4_dequantize", st)
+    return W
+
+
+def moe_linear_w4_fwd(x: torch.Tensor, w: W4Weight, *, bias: Optional[torch.Tensor] = None, act: str = "none",
+                      residual: Optional[torch.Tensor] = None, out_dtype=None, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """act(x W^T + bias) + residual for few rows of x [M, K] bfloat16 (K a multiple
+    of 8) with 4-bit weights; bias [N] bfloat16, residual [M, N] in ``out_dtype``
+    (bfloat16, the default, or float32), which may be ``out`` itself.  From some
+    hundred rows on ``moe_w4_dequantize`` and ``moe_linear_fwd`` are faster."""
+    lib = _lib.load()
+    _need(x, "x", torch.bfloat16, 2, -1)
+    c = _w4_struct(w, x.get_device(), False)
+    M, dev = x.shape[0], x.device
+    if x.shape[1] != w.K:
+        raise ValueError(f"x must be [M, {w.K}], got {tuple(x.shape)}")
+    a = _option(MOE_ACTS, act, "act")
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"unsupported out_dtype {out_dtype}; use float32 or bfloat16")
+    if bias is not None:
+        _require_out(bias, "bias", torch.bfloat16, (w.N,), dev)
+    if residual is not None:
+        _require_out(residual, "residual", out_dtype, (M, w.N), dev)
+    ctx, raw = _launch(x, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, w.N), dtype=out_dtype, device=dev)
+        else:
+            _require_out(out, "out", out_dtype, (M, w.N), dev)
+        st = lib.moe_linear_w4_fwd(_ptr(x), ctypes.byref(c), _ptr(bias), _ptr(residual), _ptr(out), M, a,
+                                   _DTYPES[out_dtype], raw)
+    _lib.check("moe_linear_w4_fwd", st)
+    return out
+
+
+def moe_fused_fwd_w4(x: torch.Tensor, w: W4Weight, sched: Schedule, *, y: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """``moe_fused_fwd`` with experts' weights of 4 bits, for few rows per expert:
+    x [T, K] bfloat16 (K a multiple of 8); y [T, N] float32."""
+    lib = _lib.load()
+    _need(x, "x", torch.bfloat16, 2, -1)
+    c = _w4_struct(w, x.get_device(), True)
+    if tuple(x.shape) != (sched.c.T, w.K) or w.E != sched.c.E:
+        raise ValueError("shape mismatch between x [T, K], the weight [E, N, K] and the schedule")
+    ctx, raw = _launch(x, stream)
+    with ctx:
+        if y is None:
+            y = torch.empty((x.shape[0], w.N), dtype=torch.float32, device=x.device)
+        else:
+            _require_out(y, "y", torch.float32, (x.shape[0], w.N), x.device)
+        st = lib.moe_fused_fwd_w4(_ptr(x), ctypes.byref(c), ctypes.byref(sched.c), _ptr(y), raw)
+    _lib.check("moe_fused_fwd_w4", st)
+    return y
+
+
+def moe_token_fwd_w4(x: torch.Tensor, w: W4Weight, expert_ids: torch.Tensor,
+                     topk_weights: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """The same for single tokens, straight from expert_ids [T, k] int32 (outside
+    [0, E): left out) and topk_weights [T, k] float32 (None: 1), without a
+    schedule; the codes are read once for every assignment."""
+    lib = _lib.load()
+    _need(x, "x", torch.bfloat16, 2, -1)
+    index = x.get_device()
+    c = _w4_struct(w, index, True)
+    if x.shape[1] != w.K:
+        raise ValueError(f"x must be [T, {w.K}], got {tuple(x.shape)}")
+    _need(expert_ids, "expert_ids", torch.int32, 2, index)
+    T, k = expert_ids.shape
+    if T != x.shape[0]:
+        raise ValueError("expert_ids and x disagree on T")
+    if topk_weights is not None:
+        _require_out(topk_weights, "topk_weights", torch.float32, (T, k), x.device)
+    ctx, raw = _launch(x, stream)
+    with ctx:
+        if y is None:
+            y = torch.empty((T, w.N), dtype=torch.float32, device=x.device)
+        else:
+            _require_out(y, "y", torch.float32, (T, w.N), x.device)
+        st = lib.moe_token_fwd_w4(_ptr(x), ctypes.byref(c), _ptr(expert_ids), _ptr(topk_weights), T, k, _ptr(y), raw)
+    _lib.check("moe_token_fwd_w4", st)
+    return y
+
+
 # ---- loss of a model's output layer -------------------------------------------------------------
 
 def _ce_operands(x, W, targets):

@@ -170,7 +170,8 @@ const char *const kFamilies[] = {"build_schedule", "fill_zero", "grouped_gemm", 
                                  "fused_fwd_fp8", "gated_bwd_dw_down", "gated_bwd_dh",
                                  "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx", "route_fwd",
                                  "route_bwd", "router_loss_fwd", "router_loss_bwd", "linear_fwd",
-                                 "linear_bwd", "linear_ce_fwd", "linear_ce_bwd", "adamw"};
+                                 "linear_bwd", "linear_ce_fwd", "linear_ce_bwd", "adamw",
+                                 "w4_quantize", "w4_dequantize", "linear_w4", "fused_fwd_w4", "token_fwd_w4"};
 constexpr int kNumFamilies = sizeof(kFamilies) / sizeof(kFamilies[0]);
 
 struct Timing {
@@ -216,7 +217,8 @@ hipError_t timed(int fam, hipStream_t st, F &&f) {
 
 enum { F_SCHED = 0, F_FILL, F_BARE, F_FWD, F_DX, F_DW, F_TILEMAP, F_GATED_UP, F_GATED_DOWN,
        F_FWD_FP8, F_GB_DWD, F_GB_DH, F_GB_DX, F_GB_DWGU, F_FWD_MX, F_ROUTE_FWD, F_ROUTE_BWD,
-       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD, F_CE_FWD, F_CE_BWD, F_ADAMW };
+       F_LOSS_FWD, F_LOSS_BWD, F_LIN_FWD, F_LIN_BWD, F_CE_FWD, F_CE_BWD, F_ADAMW, F_W4_QUANTIZE,
+       F_W4_DEQUANTIZE, F_LIN_W4, F_FWD_W4, F_TOKEN_W4 };
 
 }  // namespace
 }  // namespace moe
@@ -646,6 +648,25 @@ int check_linear(int64_t M, int64_t K, int64_t N, int32_t act, int32_t dtype, in
   return MOE_OK;
 }
 
+int check_w4(const moe_w4_weight *w) {
+  if (!w) return MOE_ERR_NULL;
+  if (w->E < 1 || w->N < 1 || w->K < 1) return MOE_ERR_SHAPE;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_ERR_OPTION;
+  if (w->E > kMaxExperts || w->N > kMaxWidth || w->K > kMaxWidth) return MOE_ERR_LIMIT;
+  const int64_t groups = (w->K + w->group - 1) / w->group;
+  if (w->N * ((w->K + 127) / 128) * 64 >= kMax32 || (w->N + 15) / 16 * 16 * groups >= kMax32 / 2) return MOE_ERR_LIMIT;
+  if (!w->codes || !w->scales) return MOE_ERR_NULL;
+  if (!aligned(w->codes, 16) || !aligned(w->scales, 8) || !aligned(w->zeros, 4)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+// x [rows, K] bf16 of a product with 4-bit weights
+int check_w4_rows(const void *x, int64_t rows, int64_t K) {
+  if (rows < 0 || K % 8) return MOE_ERR_SHAPE;
+  if (!fits(rows, K, MOE_BF16)) return MOE_ERR_LIMIT;
+  if (rows > 0 && !x) return MOE_ERR_NULL;
+  return aligned(x, 16) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
 int check_ce(int64_t M, int64_t K, int64_t V, float z, int32_t target_bits, int32_t dtype) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (target_bits != 32 && target_bits != 64) return MOE_ERR_DTYPE;
@@ -792,6 +813,74 @@ int moe_linear_bwd(const void *d_out, const void *x, const void *W, const void *
     return launch_linear_bwd(d_out, x, W, z, dX, dW, d_bias, (int)M, (int)K, (int)N, act, dtype,
                              out_dtype, workspace, st);
   }));
+}
+
+int moe_w4_quantize(const void *W, const moe_w4_weight *w, int32_t dtype, void *stream) {
+  int rc = check_w4(w);
+  if (rc) return rc;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!W) return MOE_ERR_NULL;
+  if (!aligned(W, esize(dtype))) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_W4_QUANTIZE, st, [&] { return launch_w4_quantize(W, *w, dtype, st); }));
+}
+
+int moe_w4_dequantize(const moe_w4_weight *w, void *W, int32_t dtype, void *stream) {
+  int rc = check_w4(w);
+  if (rc) return rc;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!W) return MOE_ERR_NULL;
+  if (!aligned(W, esize(dtype))) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_W4_DEQUANTIZE, st, [&] { return launch_w4_dequantize(*w, W, dtype, st); }));
+}
+
+int moe_linear_w4_fwd(const void *x, const moe_w4_weight *w, const void *bias, const void *residual,
+                      void *out, int64_t M, int32_t act, int32_t out_dtype, void *stream) {
+  int rc = check_w4(w);
+  if (rc) return rc;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (w->E != 1) return MOE_ERR_SHAPE;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return MOE_ERR_OPTION;
+  rc = check_w4_rows(x, M, w->K);
+  if (rc) return rc;
+  if (M == 0) return MOE_OK;
+  if (!out) return MOE_ERR_NULL;
+  const size_t eo = esize(out_dtype);
+  if (!aligned(bias, 2) || !aligned(residual, eo) || !aligned(out, eo)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_LIN_W4, st, [&] { return launch_linear_w4(x, *w, bias, residual, out, M, act, out_dtype, st); }));
+}
+
+int moe_fused_fwd_w4(const void *x, const moe_w4_weight *w, const moe_schedule *sched, float *y,
+                     void *stream) {
+  int rc = check_sched(sched);
+  if (!rc) rc = check_w4(w);
+  if (rc) return rc;
+  if (w->E != sched->E) return MOE_ERR_SHAPE;
+  rc = check_w4_rows(x, sched->T, w->K);
+  if (rc) return rc;
+  if (!y) return MOE_ERR_NULL;
+  if (!aligned(y, 4)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(F_FILL, st, [&] { return launch_fill_zero(y, (size_t)sched->T * w->N * 4, nullptr, 0, st); });
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  return hip_status(timed(F_FWD_W4, st, [&] { return launch_fused_w4(x, *w, *sched, y, st); }));
+}
+
+int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *expert_ids,
+                     const float *topk_weights, int64_t T, int32_t k, float *y, void *stream) {
+  int rc = check_w4(w);
+  if (rc) return rc;
+  if (k < 1 || k > 64) return MOE_ERR_SHAPE;
+  rc = check_w4_rows(x, T, w->K);
+  if (rc) return rc;
+  if (T * k >= kMax32) return MOE_ERR_LIMIT;
+  if (T == 0) return MOE_OK;
+  if (!expert_ids || !y) return MOE_ERR_NULL;
+  if (!aligned(expert_ids, 4) || !aligned(topk_weights, 4) || !aligned(y, 4)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  return hip_status(timed(F_TOKEN_W4, st, [&] { return launch_token_w4(x, *w, expert_ids, topk_weights, T, k, y, st); }));
 }
 
 size_t moe_linear_ce_fwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype) {

@@ -199,6 +199,16 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
                                 const void *targets, bool wide, const float *lse, int64_t M, int64_t K, int64_t V, float z,
                                 void *dX, void *dW, int dtype, void *ws, hipStream_t st);
 
+// 4-bit weights
+hipError_t launch_w4_quantize(const void *W, const moe_w4_weight &w, int dtype, hipStream_t st);
+hipError_t launch_w4_dequantize(const moe_w4_weight &w, void *W, int dtype, hipStream_t st);
+hipError_t launch_linear_w4(const void *x, const moe_w4_weight &w, const void *bias, const void *res, void *out, int64_t M, int act,
+                            int out_dtype, hipStream_t st);
+// y zeroed
+hipError_t launch_fused_w4(const void *x, const moe_w4_weight &w, const moe_schedule &s, float *y, hipStream_t st);
+hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t *ids, const float *weights, int64_t T, int k, float *y,
+                           hipStream_t st);
+
 // optimizer step
 struct AdamwOptions {
   double lr, beta1, beta2, eps, weight_decay;

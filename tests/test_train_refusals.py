@@ -79,6 +79,56 @@ def test_linear_ce_rejects_before_launch(lib):
     assert lib.moe_linear_ce_bwd_workspace_bytes(8192, 4096, 65536, 1) < 1 << 29
 
 
+def test_w4_rejects_before_launch(lib):
+    def w(**f):
+        return ctypes.byref(_lib.MoeW4Weight(**{**dict(codes=P.value, scales=P.value, zeros=None, N=40, K=136, E=1, group=32), **f}))
+
+    s = _lib.MoeSchedule()
+    for name, kind in _lib.MoeSchedule._fields_:
+        setattr(s, name, P.value if kind is ctypes.c_void_p else 0)
+    s.T, s.S, s.R, s.k, s.E, s.phases = 10, 20, 20, 2, 1, 0
+
+    def lin(x=P, ww=None, bias=None, res=None, out=P, M=10, act=0, od=1):
+        return lib.moe_linear_w4_fwd(x, ww or w(), bias, res, out, M, act, od, None)
+
+    calls = [lambda ww, **k: lin(ww=ww, **k), lambda ww, **k: lib.moe_fused_fwd_w4(k.get("x", P), ww, ctypes.byref(s), P, None),
+             lambda ww, **k: lib.moe_token_fwd_w4(k.get("x", P), ww, P, None, 10, 2, P, None),
+             lambda ww, **k: lib.moe_w4_quantize(P, ww, 0, None), lambda ww, **k: lib.moe_w4_dequantize(ww, P, 0, None)]
+    for call in calls:
+        assert call(w(codes=None)) == 1 and call(w(scales=None)) == 1 and call(None) == 1 or call is calls[0]
+        assert call(w(N=0)) == 2 and call(w(K=0)) == 2 and call(w(E=0)) == 2
+        assert call(w(group=48)) == 8
+        assert call(w(N=(1 << 22) + 1)) == 7 and call(w(K=(1 << 22) + 8)) == 7 and call(w(E=1025)) == 7
+        assert call(w(N=1 << 20, K=4096)) == 7  # 2^31 bytes of codes
+        assert call(w(codes=P.value + 8)) == 4 and call(w(scales=P.value + 2)) == 4 and call(w(zeros=P.value + 1)) == 4
+    for call in calls[:3]:
+        assert call(w(K=132)) == 2
+        assert call(w(), x=None) == 1 and call(w(), x=ctypes.c_void_p(P.value + 8)) == 4
+    assert lin(out=None) == 1 and lin(M=-1) == 2 and lin(M=1 << 23) == 7 and lin(act=5) == 8 and lin(od=2) == 3 and lin(ww=w(E=2)) == 2
+    assert lin(bias=ODD) == 4 and lin(res=ODD) == 4 and lin(out=ODD) == 4 and lin(M=0, x=None, out=None) == 0
+    assert lib.moe_fused_fwd_w4(P, w(E=2), ctypes.byref(s), P, None) == 2
+    assert lib.moe_fused_fwd_w4(P, w(), ctypes.byref(s), None, None) == 1 and lib.moe_fused_fwd_w4(P, w(), None, P, None) == 1
+    tok = lib.moe_token_fwd_w4
+    assert tok(P, w(), None, None, 10, 2, P, None) == 1 and tok(P, w(), P, None, 10, 2, None, None) == 1
+    assert tok(P, w(), P, None, 10, 0, P, None) == 2 and tok(P, w(), P, None, 10, 65, P, None) == 2
+    assert tok(P, w(), ODD, None, 10, 2, P, None) == 4 and tok(P, w(), P, ODD, 10, 2, P, None) == 4
+    assert tok(None, w(), None, None, 0, 2, None, None) == 0
+    assert lib.moe_w4_quantize(None, w(), 0, None) == 1 and lib.moe_w4_quantize(P, w(), 3, None) == 3
+    assert lib.moe_w4_dequantize(w(), None, 0, None) == 1 and lib.moe_w4_dequantize(w(), ODD, 1, None) == 4
+
+
+def test_oracle_w4_places_every_code_once():
+    """256 elements: every nibble of their 128 bytes is one of them; a block alone fills its 64 bytes."""
+    seen = {O.w4_place(k) for k in range(256)}
+    assert seen == {(b, s) for b in range(128) for s in (0, 4)}
+    assert {O.w4_place(k)[0] // 64 for k in range(128)} == {0}
+    W = np.random.default_rng(1).standard_normal((3, 70))
+    for symmetric in (True, False):
+        q, s, z = O.w4_quantize(W, 32, symmetric)
+        g = np.arange(70) // 32
+        assert (abs((q - z[:, g]) * s[:, g] - W) <= s[:, g] * 1.07).all()
+
+
 def test_oracle_linear_ce_against_differences_and_torch():
     rng = np.random.default_rng(0)
     x, W = rng.standard_normal((7, 5)), rng.standard_normal((11, 5))
