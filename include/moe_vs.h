@@ -562,7 +562,7 @@ int moe_fused_fwd_w4(const void *x, const moe_w4_weight *w, const moe_schedule *
  * The same for single tokens, without a schedule: expert_ids [T, k] int32 (outside
  * [0, E): left out), topk_weights [T, k] float or NULL for 1.  One launch, no
  * atomics (reproducible).  The codes are read once per assignment, so it is for T k
- * up to about E; T may be 0, T k < 2^31, k <= 64.
+ * up to about E; T may be 0, T k < 2^31, k <= 64, K <= 32512.
  */
 int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *expert_ids,
                      const float *topk_weights, int64_t T, int32_t k, float *y, void *stream);

@@ -875,7 +875,7 @@ int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *exper
   if (k < 1 || k > 64) return MOE_ERR_SHAPE;
   rc = check_w4_rows(x, T, w->K);
   if (rc) return rc;
-  if (T * k >= kMax32) return MOE_ERR_LIMIT;
+  if (T * k >= kMax32 || w->K > token_w4_width()) return MOE_ERR_LIMIT;
   if (T == 0) return MOE_OK;
   if (!expert_ids || !y) return MOE_ERR_NULL;
   if (!aligned(expert_ids, 4) || !aligned(topk_weights, 4) || !aligned(y, 4)) return MOE_ERR_ALIGN;

@@ -206,6 +206,7 @@ hipError_t launch_linear_w4(const void *x, const moe_w4_weight &w, const void *b
                             int out_dtype, hipStream_t st);
 // y zeroed
 hipError_t launch_fused_w4(const void *x, const moe_w4_weight &w, const moe_schedule &s, float *y, hipStream_t st);
+int64_t token_w4_width();  // its largest K (a row of x in 64 KB of LDS)
 hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t *ids, const float *weights, int64_t T, int k, float *y,
                            hipStream_t st);
 

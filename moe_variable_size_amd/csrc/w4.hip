@@ -11,6 +11,8 @@
 // A 128-element block of a row is 64 bytes, 16 for each quarter q of a wave's lanes: word j holds elements 32 j + 8
 // q .. +7, what lane quarter q feeds into the block's j-th 16 x 16 x 32 product, so that a lane loads 16 bytes at a
 // time and each product lies in one group.
+#include <atomic>
+
 #include "activation.hpp"
 #include "common.hpp"
 
@@ -22,6 +24,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+constexpr int STREAM_LEAST = 256;
 constexpr int BLK = 128;  // reduction elements of a block, 64 bytes of codes
 
 MOE_DEV __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
@@ -33,7 +36,10 @@ MOE_DEV __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
 
 // 16 + q of a word's eight codes, elements 0 .. 7
 MOE_DEV bf16x8 unpack(uint32_t w) {
-  constexpr uint32_t M = 0x00780078u, O = 0x41804180u;
+  // (in registers, so that and and or are one instruction: it takes no literals)
+  uint32_t M = 0x00780078u, O = 0x41804180u;
+  asm("" : "+s"(M));
+  asm("" : "+v"(O));
   const u32x4 v = {((w << 3) & M) | O, ((w >> 1) & M) | O, ((w >> 5) & M) | O, ((w >> 9) & M) | O};
   return __builtin_bit_cast(bf16x8, v);
 }
@@ -48,19 +54,45 @@ struct Weight {
   int blocks, groups;             // of a row
 };
 
-// The sums of 16 TI rows of x and 16 TJ columns over a wave's share of the blocks, those numbered wid, wid + NW, ...
-// acc of lane l: column l & 15, rows 4 (l >> 4) .. +3 (so that a lane needs one scale and one zero point).  GP: groups
-// of a block.  Codes are loaded D blocks ahead, x (out of L2) DX ahead; a block's offset is the loads' scalar one, which
-// no bounds check sees: every lane that loads is inside its row at every block, the others are out of range anyway.
-template <int TI, int TJ, int GP, bool ZEROS, int D, int DX>
+// Buffers of one expert's codes, scales and zero points
+struct Buffers {
+  const void *w, *s, *z;
+  uint32_t wn, sn, zn;  // bytes
+  MOE_DEV static Buffers of(const Weight &p, int64_t e) {
+    return Buffers{p.codes + e * p.per_codes, p.scales + e * p.per_scales, p.zeros + e * p.per_scales,
+                   (uint32_t)p.per_codes, (uint32_t)(2 * p.per_scales), (uint32_t)p.per_scales};
+  }
+};
+
+// One group's products and their sum into acc: v = sum (q - z) x of each row, from part, which holds sum (16 + q) x, or
+// that less 24 sum x where there are no zero points
+template <bool ZEROS>
+MOE_DEV void add_group(f32x4 &acc, f32x4 part, f32x4 sum, float scale, float zero) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = fmaf(scale, ZEROS ? fmaf(-zero, sum[e], part[e]) : part[e], acc[e]);
+}
+MOE_DEV f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+template <bool ZEROS>
+MOE_DEV bf16x8 sum_factor() {  // 1, or -24
+  return all_of(ZEROS ? 0x3F803F80u : 0xC1C0C1C0u);
+}
+
+// ---- some rows: 5 and more -------------------------------------------------------------
+// The sums of 16 TI rows of x and 16 TJ columns over a wave's share of the blocks.  acc of lane l: column l & 15, rows 4
+// (l >> 4) .. +3 (so that a lane needs one scale and one zero point).  GP: groups of a block.  Two blocks are in flight
+// while one is multiplied; loads return in their order, so those of x are issued with the codes'.
+// A block's offset is the loads' scalar one, which no bounds check sees: lanes of rows and columns that exist are inside
+// their row at every whole block, the others out of range anyway, and a block that does not exist is loaded from a buffer
+// of no bytes.
+template <int TI, int TJ, int GP, bool ZEROS>
 struct Wave {
-  static_assert(D % DX == 0, "");
-  u32x4 w[D][TJ], x[DX][4][TI];
+  static constexpr int D = 2;
+  u32x4 w[D][TJ], x[D][4][TI];
   uint32_t s[D][TJ], z[D][TJ];  // lane quarter q: of group q (q % 2, 0) of the block
   f32x4 acc[TI][TJ];
   uint32_t wo[TJ], so[TJ], xo[TI];
 
-  // xo: byte offsets of the rows (l & 15 of each tile) in x, out of range for none
+  // xo: byte offsets in x of the rows (l & 15 of each tile), out of range for none
   MOE_DEV void setup(const Weight &p, int n0) {
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
 #pragma unroll
@@ -76,48 +108,46 @@ struct Wave {
       for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{};
     }
   }
-  MOE_DEV void load_w(int d, const Weight &p, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz, int b) {
-    const bool in = b * GP + (int)((threadIdx.x & 63) >> 4 & (GP - 1)) < p.groups;
+  // whole block b to place d; TAIL: the last block, in which x ends, and the groups may
+  template <bool TAIL>
+  MOE_DEV void load(int d, const Weight &p, const Buffers &f, const void *xp, uint32_t xn, bool on, int b) {
+    const int q = (int)((threadIdx.x & 63) >> 4);
+    const auto rw = uniform_rsrc(f.w, on ? f.wn : 0), rs = uniform_rsrc(f.s, on ? f.sn : 0), rx = uniform_rsrc(xp, on ? xn : 0);
+    const bool group = !TAIL || b * GP + (q & (GP - 1)) < p.groups;
     const uint32_t g = (uint32_t)(b * GP) * (uint32_t)p.cols;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       w[d][j] = __builtin_amdgcn_raw_buffer_load_b128(rw, wo[j], b * 64, 0);
-      s[d][j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in && so[j] < kOobOffset ? 2 * so[j] : kOobOffset, 2 * g, 0);
-      if constexpr (ZEROS) z[d][j] = __builtin_amdgcn_raw_buffer_load_b8(rz, in ? so[j] : kOobOffset, g, 0);
+      const bool in = group && so[j] < kOobOffset;
+      s[d][j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in ? 2 * so[j] : kOobOffset, 2 * g, 0);
+      if constexpr (ZEROS) z[d][j] = __builtin_amdgcn_raw_buffer_load_b8(uniform_rsrc(f.z, on ? f.zn : 0), in ? so[j] : kOobOffset, g, 0);
     }
-  }
-  MOE_DEV void load_x(int d, const Weight &p, __amdgpu_buffer_rsrc_t rx, int b) {
-    const int k = b * BLK + (int)((threadIdx.x & 63) >> 4) * 8;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
-        x[d][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, k + 32 * t < p.K ? xo[i] + 64 * t : kOobOffset, b * 256, 0);
+      for (int i = 0; i < TI; ++i) {
+        const bool in = !TAIL || b * BLK + t * 32 + q * 8 < p.K;
+        x[d][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo[i] + 64 * t : kOobOffset, b * 256, 0);
+      }
   }
-  // weight: of the rows' assignments, 1 where it is applied later
-  MOE_DEV void multiply(int d, int dx, float weight) {
+  MOE_DEV void multiply(int d) {
     constexpr int PER = 4 / GP;  // products of a group
-    // One column tile and group after the other (empty assembly keeps its order): the compiler begins all of them at
-    // once otherwise, and spills their sums
+    // Empty assembly keeps its order, one column tile and group after the other: the compiler begins all of them at once
+    // otherwise, and spills their sums
     constexpr bool ORDER = GP * TI * TJ > 4;
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
-      f32x4 sum[TI], base[TI];  // sum x; what the accumulators begin with
-      float zero_sum = 0.f;
-      if constexpr (ORDER) asm volatile("" : "+v"(zero_sum));
+      f32x4 sum[TI];
+      float none = 0.f;
+      if constexpr (ORDER) asm volatile("" : "+v"(none));
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
-        sum[i] = base[i] = f32x4{zero_sum, zero_sum, zero_sum, zero_sum};
+        sum[i] = f32x4{none, none, none, none};
 #pragma unroll
-        for (int t = 0; t < PER; ++t) {
-          const bf16x8 xv = __builtin_bit_cast(bf16x8, x[dx][g * PER + t][i]);
-          if constexpr (ZEROS)
-            sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, all_of(0x3F803F80u), sum[i], 0, 0, 0);  // 1
-          else
-            base[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, all_of(0xC1C0C1C0u), base[i], 0, 0, 0);  // -24
-        }
-        if constexpr (ZEROS) base[i] = -16.f * sum[i];
+        for (int t = 0; t < PER; ++t)
+          sum[i] = mfma(__builtin_bit_cast(bf16x8, x[d][g * PER + t][i]), sum_factor<ZEROS>(), sum[i]);
       }
+      const int from = ((threadIdx.x & 15) + 16 * g) * 4;  // the quarter that has this group's
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
         f32x4 part[TI];
@@ -125,56 +155,52 @@ struct Wave {
         for (int t = 0; t < PER; ++t) {
           uint32_t word = w[d][j][g * PER + t];
           if constexpr (ORDER) asm volatile("" : "+v"(word));
-          const bf16x8 wv = unpack(word);
+          const bf16x8 v = unpack(word);
 #pragma unroll
           for (int i = 0; i < TI; ++i)
-            part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[dx][g * PER + t][i]), wv,
-                                                              t ? part[i] : base[i], 0, 0, 0);
+            part[i] = mfma(__builtin_bit_cast(bf16x8, x[d][g * PER + t][i]), v, t ? part[i] : ZEROS ? f32x4{} : sum[i]);
         }
         uint32_t sc = s[d][j], zc = ZEROS ? z[d][j] : 0;
-        if constexpr (GP > 1) {  // from the quarter that has this group's
-          const int from = ((threadIdx.x & 15) + 16 * g) * 4;
+        if constexpr (GP > 1) {
           sc = __builtin_amdgcn_ds_bpermute(from, sc);
           if constexpr (ZEROS) zc = __builtin_amdgcn_ds_bpermute(from, zc);
         }
-        const float scale = __uint_as_float(sc << 16) * weight, zero = (float)zc;
+        const float scale = __uint_as_float(sc << 16), zero = 16.f + (float)(zc & 0xffu);
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = ZEROS ? fmaf(-zero, sum[i][e], part[i][e]) : part[i][e];
-            acc[i][j][e] = fmaf(scale, v, acc[i][j][e]);
-          }
-        if constexpr (ORDER) {
-#pragma unroll
-          for (int i = 0; i < TI; ++i) asm volatile("" : "+v"(acc[i][j]));
+        for (int i = 0; i < TI; ++i) {
+          add_group<ZEROS>(acc[i][j], part[i], sum[i], scale, zero);
+          if constexpr (ORDER) asm volatile("" : "+v"(acc[i][j]));
         }
       }
     }
   }
-  // all of the wave's blocks; they begin at another place in each workgroup, since rows are often a power of two
-  // apart and all workgroups on the same block would meet on few channels
+  // all of the wave's blocks; they begin at another place in each workgroup, since rows are often a power of two apart and
+  // all workgroups on the same block would meet on few channels
   template <int NW>
-  MOE_DEV void run(const Weight &p, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz,
-                   __amdgpu_buffer_rsrc_t rx, int n0, uint32_t place) {
+  MOE_DEV void run(const Weight &p, const Buffers &f, const void *x, uint32_t xn, int n0, uint32_t place) {
     setup(p, n0);
-    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rot = (int)(place % (uint32_t)p.blocks);
-    auto block = [&](int u) __attribute__((always_inline)) { return u + rot >= p.blocks ? u + rot - p.blocks : u + rot; };
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), whole = p.K / BLK;
+    const int rot = whole ? (int)(place % (uint32_t)whole) : 0;
+    // No branch around a load (the compiler could not count what is in flight, and would wait for all of it), and none
+    // moved down to its use.
+    auto fetch = [&](int d, int u) __attribute__((always_inline)) {
+      const int b = u + rot;
+      load<false>(d, p, f, x, xn, u < whole, u >= whole ? 0 : b >= whole ? b - whole : b);
+    };
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (wid + d * NW < p.blocks) load_w(d, p, rw, rs, rz, block(wid + d * NW));
-#pragma unroll
-    for (int d = 0; d < DX; ++d)
-      if (wid + d * NW < p.blocks) load_x(d, p, rx, block(wid + d * NW));
-    for (int b = wid; b < p.blocks; b += D * NW) {
+    for (int d = 0; d < D; ++d) fetch(d, wid + d * NW);
+    for (int u = wid; u < whole; u += D * NW) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const int u = b + d * NW;
-        if (u >= p.blocks) break;
-        multiply(d, d % DX, 1.f);
-        if (u + D * NW < p.blocks) load_w(d, p, rw, rs, rz, block(u + D * NW));
-        if (u + DX * NW < p.blocks) load_x(d % DX, p, rx, block(u + DX * NW));
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(d);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(d, u + (D + d) * NW);
       }
+    }
+    if (whole < p.blocks && wid == whole % NW) {
+      load<true>(0, p, f, x, xn, true, whole);
+      multiply(0);
     }
   }
 };
@@ -204,7 +230,6 @@ MOE_DEV void join_waves(float *red, const f32x4 (&acc)[TJ], int rows, F &&f) {
   }
 }
 
-// ---- dense -------------------------------------------------------------------------
 struct DenseArgs {
   Weight w;
   const bf16_t *x, *bias;
@@ -216,8 +241,16 @@ MOE_DEV float ldf(const float *p) { return *p; }
 MOE_DEV float ldf(const bf16_t *p) { return bf16_to_f32(*p); }
 MOE_DEV void stf(float *p, float v) { *p = v; }
 MOE_DEV void stf(bf16_t *p, float v) { *p = __builtin_bit_cast(bf16_t, (__bf16)v); }
+template <typename To>
+MOE_DEV void finish(const DenseArgs &a, int act, int m, int n, float s) {
+  const int64_t at = (int64_t)m * a.w.N + n;
+  if (a.bias) s += bf16_to_f32(a.bias[n]);
+  s = act_fwd_of(act, s);
+  if (a.res) s += ldf((const To *)a.res + at);
+  stf((To *)a.out + at, s);
+}
 
-template <int TI, int TJ, int NW, int GP, bool ZEROS, int D, int DX, typename To>
+template <int TI, int TJ, int NW, int GP, bool ZEROS, typename To>
 __global__ __launch_bounds__(NW * 64) void dense_kernel(DenseArgs a, int act) {
   __shared__ __align__(16) float red[NW * 16 * kPitch<TJ>];
   const int tm = (a.M + 16 * TI - 1) / (16 * TI);
@@ -225,32 +258,24 @@ __global__ __launch_bounds__(NW * 64) void dense_kernel(DenseArgs a, int act) {
   const int m0 = blockIdx.x % tm * (16 * TI), n0 = blockIdx.x / tm * (16 * TJ);
   const int lane = threadIdx.x & 63;
   const Weight &p = a.w;
-  const auto rw = uniform_rsrc(p.codes, (uint32_t)p.per_codes), rs = uniform_rsrc(p.scales, (uint32_t)(2 * p.per_scales));
-  const auto rz = uniform_rsrc(ZEROS ? p.zeros : p.codes, ZEROS ? (uint32_t)p.per_scales : 0u);
-  const auto rx = uniform_rsrc(a.x + (int64_t)m0 * p.K, (uint32_t)min(16 * TI, a.M - m0) * (uint32_t)p.K * 2);
-  Wave<TI, TJ, GP, ZEROS, D, DX> v;
+  Wave<TI, TJ, GP, ZEROS> v;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int r = i * 16 + (lane & 15);
     v.xo[i] = m0 + r < a.M ? (uint32_t)r * (uint32_t)p.K * 2 : kOobOffset;
   }
-  v.template run<NW>(p, rw, rs, rz, rx, n0, blockIdx.x);
+  v.template run<NW>(p, Buffers::of(p, 0), a.x + (int64_t)m0 * p.K, (uint32_t)min(16 * TI, a.M - m0) * (uint32_t)p.K * 2, n0, blockIdx.x);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int rows = a.M - m0 - i * 16;
     if (rows <= 0) break;
     join_waves<TJ, NW>(red, v.acc[i], rows, [&](int r, int c, float s) {
-      if (n0 + c >= p.N) return;
-      const int64_t at = (int64_t)(m0 + i * 16 + r) * p.N + n0 + c;
-      if (a.bias) s += bf16_to_f32(a.bias[n0 + c]);
-      s = act_fwd_of(act, s);
-      if (a.res) s += ldf((const To *)a.res + at);
-      stf((To *)a.out + at, s);
+      if (n0 + c < p.N) finish<To>(a, act, m0 + i * 16 + r, n0 + c, s);
     });
   }
 }
 
-// ---- experts, through a schedule ---------------------------------------------------
+// ---- experts, through a schedule
 struct ExpertArgs {
   Weight w;
   const bf16_t *x;
@@ -260,21 +285,17 @@ struct ExpertArgs {
   int T, layout, capacity, tn, e0;  // e0: first expert of the launch
 };
 
-template <int TI, int TJ, int NW, int GP, bool ZEROS, int D, int DX>
+template <int TI, int TJ, int NW, int GP, bool ZEROS>
 MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row0, int rows) {
   const int lane = threadIdx.x & 63;
   const Weight &p = a.w;
-  const auto rw = uniform_rsrc(p.codes + e * p.per_codes, (uint32_t)p.per_codes);
-  const auto rs = uniform_rsrc(p.scales + e * p.per_scales, (uint32_t)(2 * p.per_scales));
-  const auto rz = uniform_rsrc(ZEROS ? p.zeros + e * p.per_scales : p.codes, ZEROS ? (uint32_t)p.per_scales : 0u);
-  const auto rx = uniform_rsrc(a.x, (uint32_t)a.T * (uint32_t)p.K * 2);
-  Wave<TI, TJ, GP, ZEROS, D, DX> v;
+  Wave<TI, TJ, GP, ZEROS> v;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int r = i * 16 + (lane & 15), t = r < rows ? a.row_to_token[row0 + r] : -1;
     v.xo[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.K * 2 : kOobOffset;
   }
-  v.template run<NW>(p, rw, rs, rz, rx, n0, blockIdx.x);
+  v.template run<NW>(p, Buffers::of(p, e), a.x, (uint32_t)a.T * (uint32_t)p.K * 2, n0, blockIdx.x);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     if (i * 16 >= rows) break;
@@ -289,19 +310,315 @@ MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row
 
 // One workgroup per expert and column tile; an expert's rows 16 TI at a time (the last ones 16 if that will do), its
 // codes then coming out of the caches.
-template <int TI, int TJ, int NW, int GP, bool ZEROS, int D, int DX>
+template <int TI, int TJ, int NW, int GP, bool ZEROS>
 __global__ __launch_bounds__(NW * 64) void expert_kernel(ExpertArgs a) {
   __shared__ __align__(16) float red[NW * 16 * kPitch<TJ>];
   const int e = a.e0 + blockIdx.x / a.tn, n0 = blockIdx.x % a.tn * (16 * TJ);
   const int count = __builtin_amdgcn_readfirstlane(a.counts[e]);
   const int first = a.layout == MOE_LAYOUT_MASKED ? e * a.capacity : __builtin_amdgcn_readfirstlane(a.offsets[e]) - count;
   for (int r = 0; r < count; r += 16 * TI) {
-    if (TI > 1 && count - r <= 16) expert_rows<1, TJ, NW, GP, ZEROS, D, DX>(a, red, e, n0, first + r, count - r);
-    else expert_rows<TI, TJ, NW, GP, ZEROS, D, DX>(a, red, e, n0, first + r, min(count - r, 16 * TI));
+    if (TI > 1 && count - r <= 16) expert_rows<1, TJ, NW, GP, ZEROS>(a, red, e, n0, first + r, count - r);
+    else expert_rows<TI, TJ, NW, GP, ZEROS>(a, red, e, n0, first + r, min(count - r, 16 * TI));
   }
 }
 
-// ---- experts of single tokens --------------------------------------------------------
+// ---- experts, enough of them to fill the chip: no split of the reduction -------------------
+// 16 columns per wave, 128 per workgroup, all waves at the same place of the reduction, whose rows of x they share
+// in LDS (out of L2 they were as many bytes as the codes: 64 experts of 7168 x 2048 with 16 rows took 190 us).  A stage is
+// two blocks of everything, so that codes are whole lines: x's rows, each wave's codes, scales and zero points, all by
+// direct global->LDS loads (a wave waits for exactly the loads it has issued; nothing else is in flight), one stage ahead
+// of the one that is multiplied, two workgroups per CU.
+//
+// One barrier per stage, after the wait for the own loads of the stage about to be read: then every wave's have landed,
+// and every wave has read the stage before, whose place the loads issued next go into.
+//
+// Measured, 64 experts of 7168 x 2048, 6 to 26 rows each, us: groups of 32 125, of 128 110 (477 MB; without the
+// arithmetic, for timing, 98).  Two or three stages ahead with one workgroup per CU 145-154 and 109; 16 waves of 16
+// columns 132 and 111, 8 of 32 columns 136 and 108; stages of one block, half lines of codes, 143 and 137.
+#define LDS_AS __attribute__((address_space(3)))
+MOE_DEV void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(m0v), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
+// the same, for lines that nothing else reads
+MOE_DEV void dma16_nt(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+               :
+               : "s"(m0v), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
+MOE_DEV void dma4(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(m0v), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
+
+constexpr int STREAM_W = 8;  // waves
+template <int TI, int GP, bool ZEROS>
+struct Stream {
+  static constexpr int G2 = 2 * GP;                               // groups of a stage
+  static constexpr int XB = TI * 8192;                            // x: [16 TI][512 bytes]
+  static constexpr int WB = 2048 + 256 + (ZEROS ? 256 : 0);       // a wave's codes, scales [G2][16], zeros [G2][16]
+  static constexpr int STAGE = XB + STREAM_W * WB;
+  static constexpr int XL = TI * 8 / STREAM_W;                    // a wave's loads of x
+};
+
+template <int TI, int GP, bool ZEROS>
+MOE_DEV void stream_rows(const ExpertArgs &a, char *lds, int e, int n0, int row0, int rows) {
+  using S = Stream<TI, GP, ZEROS>;
+  constexpr int PER = 4 / GP;
+  const Weight &p = a.w;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+  const Buffers f = Buffers::of(p, e);
+  const auto rw = uniform_rsrc(f.w, f.wn), rs = uniform_rsrc(f.s, f.sn), rx = uniform_rsrc(a.x, (uint32_t)a.T * (uint32_t)p.K * 2);
+  const auto rz = uniform_rsrc(ZEROS ? f.z : f.s, ZEROS ? f.zn : 0);
+  n0 += wid * 16;
+  // x: 16-byte chunk c of row m at place c ^ (m & 15), so that the 16 rows of an operand read fall on 16 bank groups; a
+  // load fills 2 rows, lane l place l & 31 of row l >> 5
+  uint32_t xo[S::XL];
+  int xk[S::XL];  // first reduction element of the lane's chunk in a stage
+#pragma unroll
+  for (int i = 0; i < S::XL; ++i) {
+    const int m = (wid * S::XL + i) * 2 + (lane >> 5), c = (lane & 31) ^ (m & 15);
+    const int t = m < rows ? a.row_to_token[row0 + m] : -1;
+    xk[i] = c * 8;
+    xo[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.K * 2 + c * 16 : kOobOffset;
+  }
+  // codes: chunk c (of 8) of row n at place c ^ (n >> 1 & 7): the 16 rows of an operand read, two to a line of the
+  // banks, fall on 16 bank groups; a load fills 8 rows, whole lines of memory
+  uint32_t wo[2];
+  const int wc = (lane & 7) ^ (lane >> 4);  // (n >> 1 & 7 of row 8 h + (lane >> 3) is 4 h + (lane >> 4))
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + h * 8 + (lane >> 3);
+    wo[h] = n < p.N ? (uint32_t)n * ((uint32_t)p.blocks * 64) + (wc ^ (4 * h)) * 16 : kOobOffset;
+  }
+  // scales: lane l columns 2 (l & 7) .. of group l >> 3; zero points: columns 4 (l & 3) .. of group l >> 2.  (cols: whole 16s)
+  const int sg = lane >> 3, sn = n0 + 2 * (lane & 7), zg = lane >> 2, zn = n0 + 4 * (lane & 3);
+  const uint32_t so = sg < S::G2 && sn < p.cols ? 2 * ((uint32_t)sg * (uint32_t)p.cols + sn) : kOobOffset;
+  const uint32_t zo = zg < S::G2 && zn < p.cols ? (uint32_t)zg * (uint32_t)p.cols + zn : kOobOffset;
+  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(LDS_AS char *)lds);
+  const int stages = (p.blocks + 1) / 2, rot = (int)(blockIdx.x % (uint32_t)stages);
+  auto issue = [&](int u, int slot) __attribute__((always_inline)) {
+    const bool on = u < stages;
+    const int b = !on ? 0 : u + rot >= stages ? u + rot - stages : u + rot;
+    const uint32_t at = base + (uint32_t)slot * S::STAGE, mine = at + S::XB + wid * S::WB;
+#pragma unroll
+    for (int i = 0; i < S::XL; ++i)
+      dma16(rx, on && b * 256 + xk[i] < p.K ? xo[i] : kOobOffset, b * 512, at + (wid * S::XL + i) * 1024);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // (an odd number of blocks: the last stage has one)
+      dma16_nt(rw, on && 2 * b + ((wc ^ (4 * h)) >> 2) < p.blocks ? wo[h] : kOobOffset, b * 128, mine + h * 1024);
+    dma4(rs, on && b * S::G2 + sg < p.groups ? so : kOobOffset, 2 * b * S::G2 * p.cols, mine + 2048);
+    if constexpr (ZEROS) dma4(rz, on && b * S::G2 + zg < p.groups ? zo : kOobOffset, b * S::G2 * p.cols, mine + 2304);
+  };
+  f32x4 acc[TI] = {};
+  issue(0, 0);
+  for (int u = 0; u < stages; ++u) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(u + 1, (u + 1) & 1);
+    const char *at = lds + (u & 1) * S::STAGE, *mine = at + S::XB + wid * S::WB;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      bf16x8 xv[TI][4];
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) xv[i][t] = *(const bf16x8 *)(at + (i * 16 + r) * 512 + (((b * 16 + t * 4 + q) ^ r) << 4));
+      const u32x4 w = *(const u32x4 *)(mine + r * 128 + (((b * 4 + q) ^ (r >> 1)) << 4));
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        f32x4 sum[TI], part[TI];
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          sum[i] = f32x4{};
+#pragma unroll
+          for (int t = 0; t < PER; ++t) sum[i] = mfma(xv[i][g * PER + t], sum_factor<ZEROS>(), sum[i]);
+        }
+#pragma unroll
+        for (int t = 0; t < PER; ++t) {
+          const bf16x8 v = unpack(w[g * PER + t]);
+#pragma unroll
+          for (int i = 0; i < TI; ++i) part[i] = mfma(xv[i][g * PER + t], v, t ? part[i] : ZEROS ? f32x4{} : sum[i]);
+        }
+        const int of = (b * GP + g) * 16 + r;
+        const float scale = bf16_to_f32(((const bf16_t *)(mine + 2048))[of]);
+        const float zero = ZEROS ? 16.f + (float)((const uint8_t *)(mine + 2304))[of] : 0.f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) add_group<ZEROS>(acc[i], part[i], sum[i], scale, zero);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // loads of stages that are not there end before the LDS is used again, by whomever
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int e2 = 0; e2 < 4; ++e2) {
+      const int m = i * 16 + 4 * q + e2;
+      if (m >= rows) continue;
+      const int t = a.row_to_token[row0 + m];
+      if (t < 0) continue;
+      const float weight = a.row_weight[row0 + m];
+      if (n0 + r < p.N) unsafeAtomicAdd(a.y + (int64_t)t * p.N + n0 + r, acc[i][e2] * weight);
+    }
+}
+
+template <int GP, bool ZEROS>
+__global__ __launch_bounds__(STREAM_W * 64, 4) void stream_kernel(ExpertArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const int e = a.e0 + blockIdx.x / a.tn, n0 = blockIdx.x % a.tn * (16 * STREAM_W);
+  const int count = __builtin_amdgcn_readfirstlane(a.counts[e]);
+  const int first = a.layout == MOE_LAYOUT_MASKED ? e * a.capacity : __builtin_amdgcn_readfirstlane(a.offsets[e]) - count;
+  for (int r = 0; r < count; r += 32) {
+    if (count - r <= 16) stream_rows<1, GP, ZEROS>(a, lds, e, n0, first + r, count - r);
+    else stream_rows<2, GP, ZEROS>(a, lds, e, n0, first + r, min(count - r, 32));
+  }
+}
+
+// ---- at most 4 rows, and single tokens through their experts ----------------------------------
+// Rows of x in LDS, tiles of 8 columns: a load of codes is an operand as it comes, its 16 columns being the 8 of the
+// first and the 8 of the second block of a pair; x's 16 rows are those of both blocks in turn (row r: r >> 1, block r &
+// 1; rows that are not there repeat the first), and of the products' 16 x 16 sums those of one block with itself count.
+// Since the other operand is in LDS, codes can be loaded D pairs ahead.
+template <int TJ, int GP, bool ZEROS, int D>
+struct Few {
+  u32x4 w[D][TJ];
+  uint32_t s[D][TJ], z[D][TJ];  // lane quarter q: of group q (q % 2, 0) of the lane's block
+  f32x4 acc[TJ];
+  uint32_t wo[TJ], so[TJ], xo;
+
+  // x: LDS bytes of this wave's rows, pitch apart
+  MOE_DEV void setup(const Weight &p, int n0, int rows, int pitch) {
+    const int lane = threadIdx.x & 63, hb = lane >> 3 & 1, q = lane >> 4, m = (lane & 15) >> 1;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int n = n0 + j * 8 + (lane & 7);
+      wo[j] = n < p.N ? (uint32_t)n * ((uint32_t)p.blocks * 64) + hb * 64 + q * 16 : kOobOffset;
+      so[j] = n < p.N ? (uint32_t)(hb * GP + (q & (GP - 1))) * (uint32_t)p.cols + n : kOobOffset;
+      acc[j] = f32x4{};
+    }
+    xo = (m < rows ? m : 0) * pitch + (lane & 1) * 256 + q * 16;
+  }
+  template <bool TAIL>
+  MOE_DEV void load(int d, const Weight &p, const Buffers &f, bool on, int u) {
+    const int lane = threadIdx.x & 63, hb = lane >> 3 & 1, q = lane >> 4;
+    const auto rw = uniform_rsrc(f.w, on ? f.wn : 0), rs = uniform_rsrc(f.s, on ? f.sn : 0);
+    const uint32_t g = (uint32_t)(u * 2 * GP) * (uint32_t)p.cols;
+    const bool block = !TAIL || 2 * u + hb < p.blocks, group = !TAIL || (2 * u + hb) * GP + (q & (GP - 1)) < p.groups;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      w[d][j] = __builtin_amdgcn_raw_buffer_load_b128(rw, block ? wo[j] : kOobOffset, u * 128, 0);
+      const bool in = group && so[j] < kOobOffset;
+      s[d][j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in ? 2 * so[j] : kOobOffset, 2 * g, 0);
+      if constexpr (ZEROS) z[d][j] = __builtin_amdgcn_raw_buffer_load_b8(uniform_rsrc(f.z, on ? f.zn : 0), in ? so[j] : kOobOffset, g, 0);
+    }
+  }
+  // weight: of the row's assignment, 1 without
+  MOE_DEV void multiply(int d, const char *x, int u, float weight) {
+    constexpr int PER = 4 / GP;
+    bf16x8 xv[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) xv[t] = *(const bf16x8 *)(x + xo + u * 512 + t * 64);
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      f32x4 sum = {};
+#pragma unroll
+      for (int t = 0; t < PER; ++t) sum = mfma(xv[g * PER + t], sum_factor<ZEROS>(), sum);
+      // (a quarter's sums of x are the same in every column)
+      const int from = ((threadIdx.x & 15) + 16 * g) * 4;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        f32x4 part = ZEROS ? f32x4{} : sum;
+#pragma unroll
+        for (int t = 0; t < PER; ++t) part = mfma(xv[g * PER + t], unpack(w[d][j][g * PER + t]), part);
+        uint32_t sc = s[d][j], zc = ZEROS ? z[d][j] : 0;
+        if constexpr (GP > 1) {  // from the quarter that has this group's
+          sc = __builtin_amdgcn_ds_bpermute(from, sc);
+          if constexpr (ZEROS) zc = __builtin_amdgcn_ds_bpermute(from, zc);
+        }
+        add_group<ZEROS>(acc[j], part, sum, __uint_as_float(sc << 16) * weight, 16.f + (float)(zc & 0xffu));
+      }
+    }
+  }
+};
+
+// The sums of at most 4 rows and 8 TJ columns over the waves' two blocks each, in order; f(row, column, sum)
+template <int TJ, int NW, class F>
+MOE_DEV void join_few(float *red, const f32x4 (&acc)[TJ], int rows, F &&f) {  // red [2 NW][4][8 TJ]
+  constexpr int TN = 8 * TJ;
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, hb = lane >> 3 & 1;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * (lane >> 4) + e, m = r >> 1;
+      if ((r & 1) == hb && m < rows) red[((2 * wid + hb) * 4 + m) * TN + j * 8 + (lane & 7)] = acc[j][e];
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * TN; e += NW * 64) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 2 * NW; ++w) v += red[w * 4 * TN + e];
+    f(e / TN, e % TN, v);
+  }
+}
+
+// rows of x [rows][K] to LDS, zeros up to a whole pair; pitch: their distance, 64 bytes apart on the banks
+MOE_DEV int few_pitch(int K) { return (K + 2 * BLK - 1) / (2 * BLK) * 512 + 64; }
+MOE_DEV void stage_rows(char *lds, const bf16_t *x, int rows, int K, int threads) {
+  const int pitch = few_pitch(K), per = (pitch - 64) / 16;
+  for (int c = threadIdx.x; c < rows * per; c += threads) {
+    const int m = c / per, k = (c - m * per) * 8;
+    *(u32x4 *)(lds + m * pitch + 2 * k) = k < K ? *(const u32x4 *)(x + (int64_t)m * K + k) : u32x4{};
+  }
+}
+
+template <int TJ, int NW, int GP, bool ZEROS, int D, typename To>
+__global__ __launch_bounds__(NW * 64) void few_kernel(DenseArgs a, int act) {
+  extern __shared__ __align__(16) char lds[];
+  const Weight &p = a.w;
+  const int n0 = blockIdx.x * (8 * TJ), wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pairs = p.K / (2 * BLK), rot = pairs ? (int)(blockIdx.x % (uint32_t)pairs) : 0;
+  const Buffers f = Buffers::of(p, 0);
+  Few<TJ, GP, ZEROS, D> v;
+  v.setup(p, n0, a.M, few_pitch(p.K));
+  auto place = [&](int u) __attribute__((always_inline)) { return u >= pairs ? 0 : u + rot >= pairs ? u + rot - pairs : u + rot; };
+#pragma unroll
+  for (int d = 0; d < D; ++d) v.template load<false>(d, p, f, wid + d * NW < pairs, place(wid + d * NW));
+  stage_rows(lds, a.x, a.M, p.K, NW * 64);
+  __syncthreads();
+  for (int u = wid; u < pairs; u += D * NW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int at = u + d * NW, next = at + D * NW;
+      __builtin_amdgcn_sched_barrier(0);
+      if (at < pairs) v.multiply(d, lds, place(at), 1.f);
+      __builtin_amdgcn_sched_barrier(0);
+      v.template load<false>(d, p, f, next < pairs, place(next));
+    }
+  }
+  if (pairs * 2 * BLK < p.K && wid == pairs % NW) {
+    v.template load<true>(0, p, f, true, pairs);
+    v.multiply(0, lds, pairs, 1.f);
+  }
+  join_few<TJ, NW>((float *)lds, v.acc, a.M, [&](int r, int c, float s) {
+    if (n0 + c < p.N) finish<To>(a, act, r, n0 + c, s);
+  });
+}
+
 struct TokenArgs {
   Weight w;
   const bf16_t *x;
@@ -311,48 +628,73 @@ struct TokenArgs {
   int k, E, tn;
 };
 
-// One workgroup per token and column tile: its waves share the blocks of all k experts, whose routing weights go into
-// the scales; plain stores.
-template <int TJ, int NW, int GP, bool ZEROS, int D, int DX>
-__global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
-  __shared__ __align__(16) float red[NW * 16 * kPitch<TJ>];
-  const int64_t t = blockIdx.x / a.tn;
-  const int n0 = (int)(blockIdx.x - t * a.tn) * (16 * TJ);
-  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Weight &p = a.w;
-  const auto rx = uniform_rsrc(a.x + t * p.K, (uint32_t)p.K * 2);
-  Wave<1, TJ, GP, ZEROS, D, DX> v;
-  v.xo[0] = (lane & 15) == 0 ? 0u : kOobOffset;
-  v.setup(p, n0);
-  float weight[D];
-  const int total = a.k * p.blocks;
-  auto load = [&](int d, int u) __attribute__((always_inline)) {
-    const int slot = u / p.blocks, e = __builtin_amdgcn_readfirstlane(a.ids[t * a.k + slot]);
-    const bool use = e >= 0 && e < a.E;
-    const int64_t at = use ? e : 0;  // (a slot that is left out: sums that count 0)
-    weight[d] = use ? (a.weights ? a.weights[t * a.k + slot] : 1.f) : 0.f;
-    const auto rw = uniform_rsrc(p.codes + at * p.per_codes, use ? (uint32_t)p.per_codes : 0u);
-    const auto rs = uniform_rsrc(p.scales + at * p.per_scales, use ? (uint32_t)(2 * p.per_scales) : 0u);
-    const auto rz = uniform_rsrc(ZEROS ? p.zeros + at * p.per_scales : p.codes, use && ZEROS ? (uint32_t)p.per_scales : 0u);
-    v.load_w(d, p, rw, rs, rz, u - slot * p.blocks);
-  };
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (wid + d * NW < total) load(d, wid + d * NW);
-#pragma unroll
-  for (int d = 0; d < DX; ++d)
-    if (wid + d * NW < total) v.load_x(d, p, rx, (wid + d * NW) % p.blocks);
-  for (int b = wid; b < total; b += D * NW) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int u = b + d * NW;
-      if (u >= total) break;
-      v.multiply(d, d % DX, weight[d]);
-      if (u + D * NW < total) load(d, u + D * NW);
-      if (u + DX * NW < total) v.load_x(d % DX, p, rx, (u + DX * NW) % p.blocks);
+// A walk over the pairs of all of a token's experts, dealt to the waves in turn
+struct Walk {
+  int slot, u;
+  MOE_DEV void go(int step, int pairs, int k) {
+    u += step;
+    while (u >= pairs && slot < k) {
+      u -= pairs;
+      ++slot;
     }
   }
-  join_waves<TJ, NW>(red, v.acc[0], 1, [&](int, int c, float s) {
+};
+
+// One workgroup per token and column tile: its waves share the pairs of all k experts, whose routing weights go into
+// the scales; plain stores.
+template <int TJ, int NW, int GP, bool ZEROS, int D>
+__global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const Weight &p = a.w;
+  const int64_t t = blockIdx.x / a.tn;
+  const int n0 = (int)(blockIdx.x - t * a.tn) * (8 * TJ), wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pairs = p.K / (2 * BLK);
+  Few<TJ, GP, ZEROS, D> v;
+  v.setup(p, n0, 1, few_pitch(p.K));
+  float weight[D];
+  int at[D];  // -1: no expert
+  // whether a slot has an expert
+  auto slot_of = [&](int slot, Buffers &f, float &weight) __attribute__((always_inline)) {
+    const int e = slot < a.k ? __builtin_amdgcn_readfirstlane(a.ids[t * a.k + slot]) : -1;
+    const bool use = e >= 0 && e < a.E;
+    f = Buffers::of(p, use ? e : 0);
+    weight = use ? (a.weights ? a.weights[t * a.k + slot] : 1.f) : 0.f;
+    return use;
+  };
+  Walk walk{0, 0};
+  auto load = [&](int d) __attribute__((always_inline)) {
+    Buffers f;
+    const bool use = slot_of(walk.slot, f, weight[d]);
+    at[d] = use ? walk.u : -1;
+    v.template load<false>(d, p, f, use, use ? walk.u : 0);
+    walk.go(NW, pairs, a.k);
+  };
+  if (pairs) {
+    walk.go(wid, pairs, a.k);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d);
+  }
+  stage_rows(lds, a.x + t * p.K, 1, p.K, NW * 64);
+  __syncthreads();
+  for (int u = wid; u < a.k * pairs; u += D * NW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (at[d] >= 0) v.multiply(d, lds, at[d], weight[d]);
+      __builtin_amdgcn_sched_barrier(0);
+      load(d);
+    }
+  }
+  if (pairs * 2 * BLK < p.K) {
+    for (int slot = wid; slot < a.k; slot += NW) {
+      Buffers f;
+      float w;
+      if (!slot_of(slot, f, w)) continue;
+      v.template load<true>(0, p, f, true, pairs);
+      v.multiply(0, lds, pairs, w);
+    }
+  }
+  join_few<TJ, NW>((float *)lds, v.acc, 1, [&](int, int c, float s) {
     if (n0 + c < p.N) a.y[t * p.N + n0 + c] = s;
   });
 }
@@ -433,6 +775,21 @@ Weight weight_of(const moe_w4_weight &w) {
   return p;
 }
 
+// more LDS than the default allows; the attribute is set once per device
+template <auto KERNEL>
+hipError_t allow_lds(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute((const void *)KERNEL, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return e;
+}
+
 // f(groups per block, zeros?) as constants
 template <class F>
 void by_form(const moe_w4_weight &w, F &&f) {
@@ -445,8 +802,8 @@ void by_form(const moe_w4_weight &w, F &&f) {
   else z(std::integral_constant<int, 1>());
 }
 
-template <int TI, int TJ, int NW, int D, int DX, typename To>
-hipError_t run_dense(const moe_w4_weight &w, DenseArgs a, int act, hipStream_t st) {
+template <int TI, int TJ, int NW, typename To>
+hipError_t run_dense(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
   const int64_t tn = (w.N + 16 * TJ - 1) / (16 * TJ), M = a.M;
   // workgroups of one launch: below 2^31 work-items
   const int64_t most = (((int64_t)1 << 31) / (NW * 64) / tn - 1) * 16 * TI, run = M < most ? M : most;
@@ -458,18 +815,37 @@ hipError_t run_dense(const moe_w4_weight &w, DenseArgs a, int act, hipStream_t s
     if (a.res) b.res = (const To *)a.res + m * w.N;
     const int grid = (int)(tn * ((b.M + 16 * TI - 1) / (16 * TI)));
     by_form(w, [&](auto gp, auto z) {
-      dense_kernel<TI, TJ, NW, decltype(gp)::value, decltype(z)::value, D, DX, To><<<grid, NW * 64, 0, st>>>(b, act);
+      dense_kernel<TI, TJ, NW, decltype(gp)::value, decltype(z)::value, To><<<grid, NW * 64, 0, st>>>(b, act);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
+
+// LDS of few_kernel and token_kernel: the rows, then the sums; 0 where that is over 64 KB
+size_t few_lds(int rows, int64_t K, int NW, int TJ) {
+  const size_t x = (size_t)rows * ((K + 2 * BLK - 1) / (2 * BLK) * 512 + 64), red = (size_t)2 * NW * 4 * 8 * TJ * 4;
+  return x > 65536 ? 0 : x > red ? x : red;
+}
+template <int TJ, int NW, int D, typename To>
+hipError_t run_few(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
+  const int grid = (int)((w.N + 8 * TJ - 1) / (8 * TJ));
+  by_form(w, [&](auto gp, auto z) {
+    few_kernel<TJ, NW, decltype(gp)::value, decltype(z)::value, D, To><<<grid, NW * 64, few_lds(a.M, w.K, NW, TJ), st>>>(a, act);
+  });
+  return hipGetLastError();
+}
 template <typename To>
 hipError_t dense(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
-  if (a.M > 32) return run_dense<4, 2, 8, 2, 1, To>(w, a, act, st);
-  if (a.M > 16) return run_dense<2, 2, 8, 2, 1, To>(w, a, act, st);
-  return run_dense<1, 1, 8, 4, 2, To>(w, a, act, st);
+  if (a.M <= 4 && few_lds(a.M, w.K, 8, 2)) return run_few<2, 8, 2, To>(w, a, act, st);
+  const int64_t tm = (a.M + 31) / 32;
+  if (a.M > 16) {
+    if (tm * ((w.N + 63) / 64) >= 256) return run_dense<2, 4, 8, To>(w, a, act, st);
+    return run_dense<2, 2, 8, To>(w, a, act, st);
+  }
+  if ((w.N + 31) / 32 >= 256) return run_dense<1, 2, 8, To>(w, a, act, st);
+  return run_dense<1, 1, 8, To>(w, a, act, st);
 }
 
 }  // namespace
@@ -509,28 +885,40 @@ hipError_t launch_linear_w4(const void *x, const moe_w4_weight &w, const void *b
 
 hipError_t launch_fused_w4(const void *x, const moe_w4_weight &w, const moe_schedule &s, float *y, hipStream_t st) {
   ExpertArgs a{weight_of(w), (const bf16_t *)x, y, s.counts, s.offsets, s.row_to_token, s.row_weight, (int)s.T, s.layout, s.capacity, 0, 0};
-  const bool few = s.S <= 12 * (int64_t)s.E;
-  a.tn = (a.w.N + 63) / 64;
-  const int run = (1 << 22) / a.tn;  // experts of one launch: at most 2^31 work-items
-  for (; a.e0 < s.E; a.e0 += run) {
-    const int grid = a.tn * (s.E - a.e0 < run ? s.E - a.e0 : run);
-    by_form(w, [&](auto gp, auto z) {
+  // workgroups of one launch: at most 2^31 work-items
+  auto by_experts = [&](int columns, auto &&launch) {
+    a.tn = (a.w.N + columns - 1) / columns;
+    const int run = (1 << 22) / a.tn;
+    for (a.e0 = 0; a.e0 < s.E; a.e0 += run) {
+      by_form(w, [&](auto gp, auto z) { launch(gp, z, a.tn * (s.E - a.e0 < run ? s.E - a.e0 : run)); });
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  };
+  if ((int64_t)s.E * ((a.w.N + 127) / 128) >= STREAM_LEAST)
+    return by_experts(128, [&](auto gp, auto z, int grid) {
       constexpr int GP = decltype(gp)::value;
       constexpr bool Z = decltype(z)::value;
-      if (few) expert_kernel<1, 4, 8, GP, Z, 2, 2><<<grid, 512, 0, st>>>(a);
-      else expert_kernel<2, 4, 8, GP, Z, 2, 1><<<grid, 512, 0, st>>>(a);
+      hipError_t e = allow_lds<stream_kernel<GP, Z>>(2 * Stream<2, GP, Z>::STAGE);
+      if (e == hipSuccess) stream_kernel<GP, Z><<<grid, STREAM_W * 64, 2 * Stream<2, GP, Z>::STAGE, st>>>(a);
     });
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const bool few = s.S <= 12 * (int64_t)s.E;
+  return by_experts(32, [&](auto gp, auto z, int grid) {
+    constexpr int GP = decltype(gp)::value;
+    constexpr bool Z = decltype(z)::value;
+    if (few) expert_kernel<1, 2, 8, GP, Z><<<grid, 512, 0, st>>>(a);
+    else expert_kernel<2, 2, 8, GP, Z><<<grid, 512, 0, st>>>(a);
+  });
 }
 
+int64_t token_w4_width() { return (65536 - 64) / 512 * 2 * BLK; }
 hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t *ids, const float *weights, int64_t T, int k, float *y,
                            hipStream_t st) {
+  constexpr int TJ = 1, NW = 16;
   TokenArgs a{weight_of(w), (const bf16_t *)x, ids, weights, y, k, (int)w.E, 0};
-  a.tn = (a.w.N + 15) / 16;
-  const int64_t run = ((int64_t)1 << 31) / 1024 / a.tn;  // tokens of one launch
+  a.tn = (a.w.N + 8 * TJ - 1) / (8 * TJ);
+  const int64_t run = ((int64_t)1 << 31) / (NW * 64) / a.tn;  // tokens of one launch
   for (int64_t t = 0; t < T; t += run) {
     TokenArgs b = a;
     b.x += t * w.K;
@@ -538,7 +926,9 @@ hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t 
     if (weights) b.weights += t * k;
     b.y += t * w.N;
     const int grid = (int)((T - t < run ? T - t : run) * a.tn);
-    by_form(w, [&](auto gp, auto z) { token_kernel<1, 16, decltype(gp)::value, decltype(z)::value, 4, 2><<<grid, 1024, 0, st>>>(b); });
+    by_form(w, [&](auto gp, auto z) {
+      token_kernel<TJ, NW, decltype(gp)::value, decltype(z)::value, 4><<<grid, NW * 64, few_lds(1, w.K, NW, TJ), st>>>(b);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

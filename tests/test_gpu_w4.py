@@ -132,7 +132,10 @@ def routed(T, k, E, seed, bad=0.1):
     return ids, torch.rand((T, k), generator=gen, device="cuda")
 
 
-EXPERTS = [(1, 1, 4, 17, 128), (1, 8, 64, 64, 520), (7, 3, 5, 33, 264), (60, 2, 9, 100, 136), (128, 4, 8, 48, 640), (300, 2, 3, 20, 72)]
+# (the last three have enough experts and columns for the kernel that does not split the reduction: 16, 17 to 32 and more
+# rows per expert, an odd and an even number of blocks)
+EXPERTS = [(1, 1, 4, 17, 128), (1, 8, 64, 64, 520), (7, 3, 5, 33, 264), (60, 2, 9, 100, 136), (128, 4, 8, 48, 640), (300, 2, 3, 20, 72),
+           (40, 2, 256, 70, 392), (150, 4, 32, 930, 264), (500, 3, 16, 1930, 136)]
 
 
 @pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (32, False), (64, True), (128, False)])
