@@ -116,30 +116,29 @@ MOE_DEV void get8(const uint8_t *p, bool whole, int left, float scale, float (&v
   }
 }
 
-// The largest |a| of a block (32 lanes), as bits: a NaN is above infinity and so reaches the scale.
+// The largest |a| of a block (32 lanes); a NaN among them is the largest.
 MOE_DEV float block_top(const float (&a)[PER]) {
-  uint32_t top = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(a[i]) & 0x7fffffffu);
+  for (int i = 0; i < PER; ++i) top = __builtin_elementwise_maximum(top, fabsf(a[i]));
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-  return __uint_as_float(top);
+  for (int d = 1; d < 32; d <<= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, 64));
+  return top;
 }
 
-// Code of a * inv (|a * inv| <= 448 up to a rounding), rounded up where the remainder and u, in
-// (0, 1), pass one (never 0: the largest value of a block, 448 but for a rounding, keeps its code).  With e the exponent (-6 at least) and k the eighths of 2^e, the code's magnitude is
-// 8 (e + 6) + k for subnormal, normal and carried values alike.  A NaN gives the code of NaN.
-MOE_DEV uint32_t code8(float a, float inv, float u) {
+// Code of a * inv (|a * inv| <= 448 up to a rounding), rounded up where the remainder and u = (h + 1/2) / 2^16 pass one
+// (u is never 0: the largest value of a block, 448 but for a rounding, keeps its code).  With e the exponent (-6 at least)
+// and k the eighths of 2^e, the code's magnitude is 8 (e + 6) + k for subnormal, normal and carried values alike; here 2^16
+// of it at once, the remainder in 16 bits: floor((floor(y + 1/2) + h) / 2^16) is floor((y + 1/2 + h) / 2^16).
+MOE_DEV uint32_t code8(float a, float inv, uint32_t h) {
   const float y = fabsf(a) * inv;
   const uint32_t e = max(__float_as_uint(y) >> 23, 121u);
-  const uint32_t k = (uint32_t)(y * __uint_as_float((257u - e) << 23) + u);
-  uint32_t c = (e - 121u) * 8 + k;
-  c = y != y ? 127u : c < 126u ? c : 126u;
-  return c | (__float_as_uint(a) >> 24 & 0x80u);
+  const uint32_t k = (uint32_t)fmaf(y, __uint_as_float((273u - e) << 23), 0.5f);
+  return min(((e << 19) + k + h >> 16) - 968u, 126u);
 }
 
-// a rounded to codes, and the block's scale
-template <bool HIGH>
+// a rounded to codes, and the block's scale (NaN where a value is not finite, so that all of the block becomes one)
+template <bool SIGNED>
 MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&a)[PER],
                   const uint32_t (&h)[PER]) {
   const float top = block_top(a);
@@ -148,8 +147,9 @@ MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&
   u32x2 c = {0, 0};
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const float u = fmaf((float)(HIGH ? h[i] >> 16 : h[i] & 0xffffu), 0x1p-16f, 0x1p-17f);
-    c[i / 4] |= code8(a[i], inv, u) << (8 * (i & 3));
+    uint32_t k = code8(a[i], inv, SIGNED ? h[i] & 0xffffu : h[i] >> 16);
+    if (SIGNED) k |= __float_as_uint(a[i]) >> 24 & 0x80u;
+    c[i / 4] |= k << (8 * (i & 3));
   }
   if (whole) {
     *(u32x2 *)p = c;
@@ -158,7 +158,14 @@ MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&
     for (int i = 0; i < PER; ++i)
       if (i < left) p[i] = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
   }
-  if ((threadIdx.x & 31) == 0 && left > 0) *scale = none ? 0.f : top / 448.f;
+  if ((threadIdx.x & 31) == 0 && left > 0) *scale = none ? 0.f : top < INFINITY ? top / 448.f : NAN;
+}
+
+// The hardware's root, off by a step at most, with small arguments in its range: the exact one takes three times as many
+// instructions, which 8-bit states would wait for (so does the quotient below)
+MOE_DEV float root_of(float v) {
+  const bool small = v < 0x1p-96f;
+  return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.f);
 }
 
 // elements at .. at + 7 of tensor t (FULL: the whole workgroup's are there, on 16-byte lines)
@@ -189,8 +196,8 @@ MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, 
     const float x = g[i] * s;
     m[i] = fmaf(a.b1, m[i], a.a1 * x);
     v[i] = fmaf(a.b2, v[i], a.a2 * x * x);
-    r[i] = sqrtf(v[i]);
-    w[i] = fmaf(w[i], keep, -(rate * m[i]) / fmaf(r[i], root, a.eps));
+    r[i] = root_of(v[i]);
+    w[i] = fmaf(w[i], keep, -(rate * m[i]) * __builtin_amdgcn_rcpf(fmaf(r[i], root, a.eps)));
   }
   put8((P *)t.p + at, FULL, left, w);
   if (t.master) put8(t.master + at, FULL, left, w);
@@ -207,8 +214,8 @@ MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, 
     uint32_t h[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) h[i] = mix(((uint32_t)at + i) ^ key);
-    put8<false>((uint8_t *)t.m + at, t.ms + at / 256, FULL, left, m, h);
-    put8<true>((uint8_t *)t.v + at, t.vs + at / 256, FULL, left, r, h);
+    put8<true>((uint8_t *)t.m + at, t.ms + at / 256, FULL, left, m, h);
+    put8<false>((uint8_t *)t.v + at, t.vs + at / 256, FULL, left, r, h);
   }
 }
 

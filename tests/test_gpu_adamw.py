@@ -2,9 +2,9 @@
 
 Tolerances count roundings of half a step (2^-24 in fp32, 2^-8 in bf16).  m: the two coefficients, the
 scaled gradient, its product and the sum, at most 5 of |b1 m| + |a1 g|; v: 7 of v; the parameter: 3 of itself
-(the decay and the sum) and of the step 3 (rate), 1 (product), 5 (m), 4.5 (root of v), 2.5 (root of the
-correction), 3 (eps, sum, quotient), below 20 of the step taken with |b1 m| + |a1 g|.  8-bit states add
-one rounding of their values (two of v): counted as 24.
+(the decay and the sum) and of the step 3 (rate), 1 (product), 5 (m), 5.5 (v, and 2 for a root off by a whole step),
+2.5 (root of the correction), 2 (eps, sum), 3 (a reciprocal off by a whole step, the product): 22 of the step taken with
+|b1 m| + |a1 g|.  8-bit states add one rounding of their values (two of v): 24.
 """
 import numpy as np
 import pytest
