@@ -581,8 +581,9 @@ int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *exper
  *   Element alignment, any sizes (bf16 runs fastest with K a multiple of 8 and
  *   16-byte aligned x and W); M may be 0; M <= 2^24, K and V <= 2^22.
  *   workspace: moe_linear_ce_fwd_workspace_bytes(...) bytes, 256-byte aligned:
- *   at most two numbers per row and 128 columns of the vocabulary, or a piece of
- *   256 MB (or 1024 columns) of logits where the tiles cannot join them.
+ *   two numbers per row and tile (128 or 256 columns; 32 or 64 for fp32 and rows off
+ *   16-byte lines); for at most 16 rows and for products of few tiles, whose reduction
+ *   is split, a piece's logits, at most 256 MB or 1024 columns of them.
  * Sums are fp32 per row and run of columns, joined in a fixed order (reproducible).
  * A logit of +inf or NaN makes its row's loss NaN.
  */

@@ -746,6 +746,7 @@ class W4Weight:
 
 
 def _w4_shapes(lead, N, K, group):
+    """Shapes of a weight's codes and of its scales."""
     return (*lead, N, -(-K // 128) * 64), (*lead, -(-K // group), -(-N // 16) * 16)
 
 
@@ -755,16 +756,18 @@ def _w4_struct(w: W4Weight, index: int, experts: bool):
     if w.group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {w.group}")
     rank = 3 if experts else 2
-    _need(w.codes, "codes", torch.uint8, rank, index)
-    _need(w.scales, "scales", torch.bfloat16, rank, index)
-    codes, scales = _w4_shapes(w.codes.shape[:-2], w.N, w.K, w.group)
-    if tuple(w.codes.shape) != codes or tuple(w.scales.shape) != scales:
-        raise ValueError(f"codes must be {codes} and scales {scales}, got {tuple(w.codes.shape)} and {tuple(w.scales.shape)}")
-    if w.zeros is not None:
-        _need(w.zeros, "zeros", torch.uint8, rank, index)
-        if tuple(w.zeros.shape) != scales:
-            raise ValueError(f"zeros must be {scales}, got {tuple(w.zeros.shape)}")
-    return _lib.MoeW4Weight(_ptr(w.codes), _ptr(w.scales), _ptr(w.zeros), w.N, w.K, w.E or 1, w.group)
+    c, s, z = w.codes, w.scales, w.zeros
+    _need(c, "codes", torch.uint8, rank, index)
+    _need(s, "scales", torch.bfloat16, rank, index)
+    codes, scales = _w4_shapes(c.shape[:-2], w.N, w.K, w.group)
+    if c.shape != codes or s.shape != scales:
+        raise ValueError(f"codes must be {codes} and scales {scales}, got {tuple(c.shape)} and {tuple(s.shape)}")
+    if z is not None:
+        _need(z, "zeros", torch.uint8, rank, index)
+        if z.shape != scales:
+            raise ValueError(f"zeros must be {scales}, got {tuple(z.shape)}")
+        z = z.data_ptr()
+    return _lib.MoeW4Weight(c.data_ptr(), s.data_ptr(), z, w.N, w.K, codes[0] if experts else 1, w.group)
 
 
 def moe_w4_quantize(W: torch.Tensor, *, group: int = 128, symmetric: bool = False, stream=None) -> W4Weight:
@@ -964,20 +967,25 @@ def moe_linear_ce_bwd(d_loss: torch.Tensor, x: torch.Tensor, W: torch.Tensor, ta
 
 def _tensors(ts, name: str, count: int, dtypes, sizes, index: int) -> list:
     """Addresses of a list of dense device tensors of these dtypes (all alike) and element counts."""
-    ts = list(ts)
     if len(ts) != count:
         raise ValueError(f"{name} must have {count} tensors, got {len(ts)}")
-    for i, (t, n) in enumerate(zip(ts, sizes)):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
-            _require(t, f"{name}[{i}]")
-            raise TypeError(f"{name}[{i}] must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    dt = getattr(ts[0], "dtype", None)
+    if dt not in dtypes:
+        _require(ts[0], f"{name}[0]")
+        raise TypeError(f"{name}[0] must be {' or '.join(map(str, dtypes))}, got {dt}")
+    at = []
+    for t, n in zip(ts, sizes):  # (a step's host time is these checks)
+        if getattr(t, "dtype", None) is dt and t.get_device() == index and t.numel() == n and t.is_contiguous():
+            at.append(t.data_ptr())
+            continue
+        i = len(at)
+        _require(t, f"{name}[{i}]")
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be all of one dtype, {dt}, got {t.dtype}")
         if t.numel() != n:
             raise ValueError(f"{name}[{i}] must have {n} elements, got {t.numel()}")
-        if t.get_device() != index:
-            raise ValueError(f"{name}[{i}] must be on cuda:{index}, got {t.device}")
-    if len({t.dtype for t in ts}) > 1:
-        raise TypeError(f"{name} must be all of one dtype")
-    return [t.data_ptr() for t in ts]
+        raise ValueError(f"{name}[{i}] must be on cuda:{index}, got {t.device}")
+    return at
 
 
 def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -1006,9 +1014,8 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9
     p = _tensors(params, "params", count, real, sizes, index)
     if len(set(p)) != count and len({a for a, n in zip(p, sizes) if n}) != sum(n > 0 for n in sizes):
         raise ValueError("params must not hold a tensor twice")
-    grads = list(grads)
+    grads, exp_avgs, exp_avg_sqs = list(grads), list(exp_avgs), list(exp_avg_sqs)
     g = _tensors(grads, "grads", count, real, sizes, index)
-    exp_avgs = list(exp_avgs)
     eight = bool(exp_avgs) and isinstance(exp_avgs[0], torch.Tensor) and exp_avgs[0].dtype == torch.float8_e4m3fn
     kind = (torch.float8_e4m3fn,) if eight else (torch.float32,)
     m = _tensors(exp_avgs, "exp_avgs", count, kind, sizes, index)
@@ -1019,14 +1026,14 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9
         if m_scales is None or v_scales is None:
             raise ValueError("states in 8 bits need m_scales and v_scales")
         blocks = [-(-n // 256) for n in sizes]
-        ms = _tensors(m_scales, "m_scales", count, (torch.float32,), blocks, index)
-        vs = _tensors(v_scales, "v_scales", count, (torch.float32,), blocks, index)
+        ms = _tensors(list(m_scales), "m_scales", count, (torch.float32,), blocks, index)
+        vs = _tensors(list(v_scales), "v_scales", count, (torch.float32,), blocks, index)
     elif m_scales is not None or v_scales is not None:
         raise ValueError("m_scales and v_scales go with states in 8 bits")
     if masters is not None:
         if params[0].dtype != torch.bfloat16:
             raise TypeError("masters go with bfloat16 params")
-        w = _tensors(masters, "masters", count, (torch.float32,), sizes, index)
+        w = _tensors(list(masters), "masters", count, (torch.float32,), sizes, index)
     numbers = range(count) if numbers is None else list(numbers)
     if len(numbers) != count:
         raise ValueError(f"numbers must have {count} entries")

@@ -7,8 +7,8 @@
 // the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
 // logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
 // fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it.
-// What cannot take those tiles (fp32, rows off 16-byte lines, few rows, short vocabularies whose reduction is
-// better split) writes a piece's logits in fp32 to the workspace and reads them back.
+// fp32 and rows off 16-byte lines do the same in the staged tiles.  Few rows, and products so small that their reduction
+// is better split, write a piece's logits in fp32 to the workspace and read them back.
 #include "cross_entropy.hpp"
 
 namespace moe {
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void stats_kernel(const float *__restrict__ l,
   }
 }
 
-// dl of a piece, zeros behind it up to its row length; fp32 takes the exact exponential (the hardware's is off by some 2^-21 at |l - lse| = 10)
+// dl of a piece, zeros behind it up to its row length
 template <typename T>
 __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, CeArgs a, T *__restrict__ dl, int64_t M,
                                                  int n, int chunks) {
@@ -75,37 +75,32 @@ __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, Ce
     for (int i = 0; i < CHUNK / 256; ++i) {
       const int col = c * CHUNK + i * 256 + threadIdx.x;
       if (col >= hi) break;
-      float d = 0.f;
-      if constexpr (sizeof(T) == 2) {
-        d = ce_dl(r, l[m * n + col], a.col0 + col);
-      } else if (r.target >= 0) {
-        d = r.scale * expf(l[m * n + col] - r.lse);
-        if (a.col0 + col == r.target) d -= r.g;
-      }
-      st(dl + m * a.ld + col, d);
+      st(dl + m * a.ld + col, ce_dl<T>(r, l[m * n + col], a.col0 + col));
     }
   }
 }
 
 // ---- rows -------------------------------------------------------------------------
-// loss and lse from a row's parts.  LANES = 64: a wave per row, 4 rows per workgroup; 4: a workgroup takes
-// 64 rows, whose parts lie side by side, 4 threads each (from M = 2048 on: lines are then read whole).
+// loss and lse from a row's parts.  LANES = 64: a wave per row, 4 rows per workgroup; 16: a workgroup takes 16 rows, whose
+// parts lie side by side (a line), 16 threads each, from M = 256 on.  8192 rows of 256 parts: 31 us with 4 threads a row.
 template <int LANES>
 __global__ __launch_bounds__(256) void join_kernel(CeArgs a, int64_t M, int parts, float z, float *loss, float *lse) {
-  __shared__ float2 red[4][64];
-  const int lane = LANES == 64 ? threadIdx.x & 63 : threadIdx.x >> 6;
-  const int64_t m = LANES == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  __shared__ float2 red[16][16];
+  const int lane = LANES == 64 ? threadIdx.x & 63 : threadIdx.x >> 4, row = threadIdx.x & 15;
+  const int64_t m = LANES == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x * 16 + row;
   float2 r{-INFINITY, 0.f};
-  if (m < M)
+  if (m < M) {
+#pragma unroll 4
     for (int p = lane; p < parts; p += LANES) r = ce_join(r, a.part[(int64_t)p * M + m]);
+  }
   if constexpr (LANES == 64) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) r = ce_join(r, float2{__shfl_xor(r.x, d, 64), __shfl_xor(r.y, d, 64)});
   } else {
-    red[lane][threadIdx.x & 63] = r;
+    red[lane][row] = r;
     __syncthreads();
-    r = ce_join(ce_join(red[0][threadIdx.x & 63], red[1][threadIdx.x & 63]),
-                ce_join(red[2][threadIdx.x & 63], red[3][threadIdx.x & 63]));
+#pragma unroll
+    for (int i = 1; i < 16; ++i) r = ce_join(r, red[i][row]);  // (thread 0 of a row: its own first)
   }
   if (lane || m >= M) return;
   const float v = r.x + logf(r.y);
@@ -178,44 +173,47 @@ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 int64_t greatest(int64_t a, int64_t b) { return a > b ? a : b; }
 int64_t weight_piece(int64_t K) { return greatest(256, least(((int64_t)1 << 30) / K - 1, 1 << 20) / 256 * 256); }
 
+// How a piece's logits are taken: by the tiles that end in the epilogues above, of which `tiles` need rows on 16-byte
+// lines; else through memory.
+enum Way { TILES, STAGED, MEMORY };
+
 struct Fwd {
-  bool tiles;
   int64_t piece;
-  int parts;
+  int columns, parts;               // of a part; parts of a row
   size_t part, logits, gemm, total;  // offsets of the parts (after the targets' logits), ...
 };
-Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, bool tiles, bool spare) {
+int64_t fwd_piece(int64_t M, int64_t K, int64_t V, Way way) {
+  if (way == TILES) return even_piece(V, weight_piece(K));
+  if (way == STAGED) return even_piece(V, ((int64_t)1 << 29) / M * 64 / 256 * 256);  // of one launch
+  return even_piece(V, greatest(1024, ((int64_t)1 << 26) / M / 256 * 256));          // 256 MB of logits
+}
+Way fwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
+  if (on_lines && dtype == MOE_BF16 && ce_tiles(M, K, fwd_piece(M, K, V, TILES))) return TILES;
+  return ce_staged(M, K, fwd_piece(M, K, V, STAGED), dtype) ? STAGED : MEMORY;
+}
+Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   Fwd f;
-  f.tiles = tiles;
   f.part = up256((size_t)M * 4);
-  if (tiles) {
-    f.piece = even_piece(V, weight_piece(K));
-    f.parts = 0;
-    const int bn = ce_tile_columns(M, K, f.piece);
-    for (int64_t v = 0; v < V; v += f.piece) f.parts += (int)((least(f.piece, V - v) + bn - 1) / bn);
-    f.logits = f.gemm = f.total = f.part + up256((size_t)f.parts * M * 8);
-    return f;
-  }
-  // 256 MB of logits; 1024 columns where only operands off their lines come here
-  f.piece = even_piece(V, spare ? 1024 : greatest(1024, ((int64_t)1 << 26) / M / 256 * 256));
-  f.parts = (int)((f.piece + CHUNK - 1) / CHUNK);
+  f.piece = fwd_piece(M, K, V, way);
+  f.columns = way == TILES ? ce_tile_columns(M, K, f.piece) : way == STAGED ? ce_staged_columns(M, K, f.piece, dtype) : CHUNK;
+  // (a staged tile has two waves' columns, used or not; parts in memory are shared by the pieces)
+  auto of = [&](int64_t n) { return way == STAGED ? (n + 2 * f.columns - 1) / (2 * f.columns) * 2 : (n + f.columns - 1) / f.columns; };
+  f.parts = (int)of(f.piece);
+  if (way != MEMORY)
+    for (int64_t v = f.piece; v < V; v += f.piece) f.parts += (int)of(least(f.piece, V - v));
   f.logits = f.part + up256((size_t)f.parts * M * 8);
-  f.gemm = f.logits + up256((size_t)M * f.piece * 4);
+  f.gemm = f.logits + (way == MEMORY ? up256((size_t)M * f.piece * 4) : 0);
   size_t g = 0;
   for (int64_t n : {f.piece, V % f.piece}) {
-    if (!n) continue;
-    const size_t b = ce_part_bytes(M, n, K, dtype);
+    if (!n || way != MEMORY) continue;
+    const size_t b = ce_logits_part_bytes(M, n, K, dtype);
     g = b > g ? b : g;
   }
   f.total = f.gemm + up256(g);
   return f;
 }
-bool fwd_tiles(int64_t M, int64_t K, int64_t V, int dtype) {
-  return dtype == MOE_BF16 && ce_tiles(M, K, even_piece(V, weight_piece(K)));
-}
 
 struct Bwd {
-  bool tiles;
   int64_t piece;
   size_t dl, sum, logits, gemm, total;  // offsets after the rows
 };
@@ -231,22 +229,23 @@ bool bwd_lines(int64_t M, int64_t K, int64_t V, int dtype) {
   const int64_t p = bwd_ld(bwd_piece(M, K, V)), most = (int64_t)1 << 30;
   return dtype == MOE_BF16 && K % 8 == 0 && K <= (1 << 20) && p <= (1 << 20) && M * p < most && M * K < most && p * K < most;
 }
-bool bwd_tiles(int64_t M, int64_t K, int64_t V, int dtype) {
-  return bwd_lines(M, K, V, dtype) && ce_tiles(M, K, bwd_piece(M, K, V));
+Way bwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
+  const int64_t p = bwd_piece(M, K, V);
+  if (on_lines && bwd_lines(M, K, V, dtype) && ce_tiles(M, K, p)) return TILES;
+  return ce_staged(M, K, p, dtype) ? STAGED : MEMORY;
 }
-Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, bool tiles, bool spare) {
+Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   const size_t es = dtype == MOE_F32 ? 4 : 2;
   Bwd w;
-  w.tiles = tiles;
-  w.piece = spare ? even_piece(V, 1024) : bwd_piece(M, K, V);
+  w.piece = bwd_piece(M, K, V);
   w.dl = up256((size_t)M * sizeof(CeRow));
   w.sum = w.dl + up256((size_t)M * bwd_ld(w.piece) * es);
   w.logits = w.sum + (w.piece < V && dtype == MOE_BF16 ? up256((size_t)M * K * 4) : 0);
-  w.gemm = w.logits + (tiles ? 0 : up256((size_t)M * w.piece * 4));
+  w.gemm = w.logits + (way == MEMORY ? up256((size_t)M * w.piece * 4) : 0);
   size_t g = 0;
   for (int64_t n : {w.piece, V % w.piece}) {
     if (!n) continue;
-    for (size_t b : {tiles ? 0 : ce_part_bytes(M, n, K, dtype), ce_part_bytes(M, K, n, dtype), ce_part_bytes(n, K, M, dtype)})
+    for (size_t b : {way == MEMORY ? ce_logits_part_bytes(M, n, K, dtype) : 0, ce_part_bytes(M, K, n, dtype), ce_part_bytes(n, K, M, dtype)})
       g = b > g ? b : g;
   }
   w.total = w.gemm + up256(g);
@@ -257,14 +256,15 @@ int chunk_grid(int64_t M, int chunks) { return (int)least(M * chunks, kGrid); }
 
 }  // namespace
 
+// (x and W may lie off 16-byte lines: the larger of both ways)
 size_t linear_ce_fwd_workspace(int64_t M, int64_t K, int64_t V, int dtype) {
-  const bool t = fwd_tiles(M, K, V, dtype);
-  const size_t a = fwd_space(M, K, V, dtype, false, t).total, b = t ? fwd_space(M, K, V, dtype, true, false).total : 0;
+  const size_t a = fwd_space(M, K, V, dtype, fwd_way(M, K, V, dtype, true)).total;
+  const size_t b = fwd_space(M, K, V, dtype, fwd_way(M, K, V, dtype, false)).total;
   return a > b ? a : b;
 }
 size_t linear_ce_bwd_workspace(int64_t M, int64_t K, int64_t V, int dtype) {
-  const bool t = bwd_tiles(M, K, V, dtype);
-  const size_t a = bwd_space(M, K, V, dtype, false, t).total, b = t ? bwd_space(M, K, V, dtype, true, false).total : 0;
+  const size_t a = bwd_space(M, K, V, dtype, bwd_way(M, K, V, dtype, true)).total;
+  const size_t b = bwd_space(M, K, V, dtype, bwd_way(M, K, V, dtype, false)).total;
   return a > b ? a : b;
 }
 
@@ -276,20 +276,24 @@ hipError_t launch_linear_ce_fwd(const void *x, const void *W, const void *target
   a.V = V;
   hipError_t e = hipSuccess;
   if (M > 0) {
-    const bool sized = fwd_tiles(M, K, V, dtype), tiles = sized && on_line(x) && on_line(W);
-    const Fwd f = fwd_space(M, K, V, dtype, tiles, sized && !tiles);
+    const Way way = fwd_way(M, K, V, dtype, on_line(x) && on_line(W));
+    const Fwd f = fwd_space(M, K, V, dtype, way);
     const size_t es = dtype == MOE_F32 ? 4 : 2;
     a.target_logit = (float *)ws;
     a.part = (float2 *)((char *)ws + f.part);
     float *logits = (float *)((char *)ws + f.logits);
-    const int bn = tiles ? ce_tile_columns(M, K, f.piece) : 1;
     for (int64_t v = 0; v < V && e == hipSuccess; v += f.piece) {
       const int n = (int)least(f.piece, V - v);
       const char *w = (const char *)W + (size_t)v * K * es;
       a.col0 = v;
-      if (tiles) {
+      if (way == TILES) {
         e = launch_ce_tiles(x, w, nullptr, a, (int)M, (int)K, n, (int)f.piece, st);
-        a.part0 += (n + bn - 1) / bn;
+        a.part0 += (n + f.columns - 1) / f.columns;
+        continue;
+      }
+      if (way == STAGED) {
+        e = launch_ce_staged(x, w, nullptr, a, (int)M, (int)K, n, (int)f.piece, dtype, st);
+        a.part0 += (n + 2 * f.columns - 1) / (2 * f.columns) * 2;
         continue;
       }
       e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32,
@@ -301,8 +305,8 @@ hipError_t launch_linear_ce_fwd(const void *x, const void *W, const void *target
     }
     if (e != hipSuccess) return e;
     a.col0 = 0;
-    if (M < 2048) join_kernel<64><<<(int)((M + 3) / 4), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
-    else join_kernel<4><<<(int)((M + 63) / 64), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
+    if (M < 256) join_kernel<64><<<(int)((M + 3) / 4), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
+    else join_kernel<16><<<(int)((M + 15) / 16), 256, 0, st>>>(a, M, f.parts, z, loss, lse);
     e = hipGetLastError();
   }
   if (e == hipSuccess && total) {
@@ -317,9 +321,9 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
                                 void *dX, void *dW, int dtype, void *ws, hipStream_t st) {
   const size_t es = dtype == MOE_F32 ? 4 : 2;
   if (M == 0) return dW ? launch_fill_zero(dW, (size_t)V * K * es, nullptr, 0, st) : hipSuccess;
-  const bool on = on_line(x) && on_line(W), sized = bwd_tiles(M, K, V, dtype), tiles = sized && on;
-  const bool lines = on && bwd_lines(M, K, V, dtype);
-  const Bwd b = bwd_space(M, K, V, dtype, tiles, sized && !tiles);
+  const bool on = on_line(x) && on_line(W), lines = on && bwd_lines(M, K, V, dtype);
+  const Way way = bwd_way(M, K, V, dtype, on);
+  const Bwd b = bwd_space(M, K, V, dtype, way);
   CeArgs a{};
   a.targets = targets;
   a.wide = wide;
@@ -337,8 +341,10 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
     const char *w = (const char *)W + (size_t)v * K * es;
     a.col0 = v;
     a.ld = lines ? bwd_ld(n) : n;
-    if (tiles) {
+    if (way == TILES) {
       e = launch_ce_tiles(x, w, dl, a, (int)M, (int)K, n, (int)b.piece, st);
+    } else if (way == STAGED) {
+      e = launch_ce_staged(x, w, dl, a, (int)M, (int)K, n, (int)b.piece, dtype, st);
     } else {
       e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32, part, st);
       if (e != hipSuccess) break;

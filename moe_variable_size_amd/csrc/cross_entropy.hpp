@@ -40,9 +40,15 @@ MOE_DEV float2 ce_join(float2 a, float2 b) {
   const float top = fmaxf(a.x, b.x), base = ce_base(top);
   return float2{top, a.y * __expf(a.x - base) + b.y * __expf(b.x - base)};
 }
+// fp32 operands take the exact exponential (the hardware's is off by some 2^-21 at |l - lse| = 10)
+template <typename T>
+MOE_DEV float ce_exp(float d) {
+  return sizeof(T) == 4 ? expf(d) : __expf(d);
+}
+template <typename T>
 MOE_DEV float ce_dl(const CeRow &r, float l, int64_t col) {
   if (r.target < 0) return 0.f;
-  const float d = r.scale * __expf(l - r.lse);
+  const float d = r.scale * ce_exp<T>(l - r.lse);
   return col == r.target ? d - r.g : d;
 }
 
@@ -54,7 +60,14 @@ int ce_tile_columns(int64_t M, int64_t K, int64_t V);
 // dl NULL: the forward's statistics; shape_v: the size that the tile's shape goes by
 hipError_t launch_ce_tiles(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v,
                            hipStream_t st);
+// The same in staged tiles, for any alignment: whether their reduction is whole, the columns of a wave
+bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype);
+int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype);
+hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
+                            hipStream_t st);
+// workspaces of dX and dW, and of logits that launch_linear_fwd leaves in memory
 size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+size_t ce_logits_part_bytes(int64_t M, int64_t V, int64_t K, int dtype);
 // out = dl W + sum (sum NULL: 0; fp32, may be out)
 hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
                         int V, int dtype, void *part, hipStream_t st);

@@ -30,6 +30,7 @@ struct GemmArgs {
   int M, N, K;
   int64_t lda, ldb;  // K-major: elements between rows; MN-major: between reduction rows
   bool vec;          // N a multiple of 8; out, z, residual and bias on 16-byte lines
+  Plan plan;         // of the staged tiles; shape 0: staged_plan's
 };
 
 // buffer resource from wave-uniform values, in scalar registers
@@ -109,6 +110,11 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
     }
   }
 }
+
+// The cross entropy's epilogues (cross_entropy.hip), in the place of an activation: logits l = x W^T stay in the
+// accumulators.  The forward leaves the largest value and the sum of exponentials of a row's columns in a tile (or a wave
+// of it), and the target's logit; the backward leaves dl.
+constexpr int kCeStats = 16, kCeGrad = 17;
 
 // ---- staged tiles: any alignment and size ------------------------------------
 // 64 S x 64 S outputs per 4 waves (2 x 2, S x S blocks of 32 x 32 each), 32 reduction elements per
@@ -204,7 +210,7 @@ MOE_DEV int acc_row(int i, int lane) { return ((i >> 2) << 3) + ((lane >> 5) << 
 
 // splits > 1: range blockIdx / tiles of the reduction, fp32 products to part [splits][M][N]
 template <typename T, typename To, int S, int E, bool AK, bool BKM, int ACT>
-__global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part) {
+__global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part, CeArgs ce) {
   using LA = Tile<T, S, AK>;
   using LB = Tile<T, S, BKM>;
   constexpr int TS = 64 * S, EA = sizeof(T) == 4 || AK ? E : 1, EB = sizeof(T) == 4 || BKM ? E : 1;
@@ -268,6 +274,48 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
               acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
       }
     }
+  }
+  if constexpr (ACT == kCeStats) {
+    const int n = n0 + wn + (lane & 31);
+    float2 *out = ce.part + (int64_t)(ce.part0 + (n0 + wn) / (32 * S)) * p.M;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = m0 + wm + i * 32 + acc_row(e, lane), t = m < p.M ? ce_target(ce, m) : -1;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          if (t >= 0 && t == n + j * 32 && t < p.N) ce.target_logit[m] = acc[i][j][e];
+          if (n + j * 32 >= p.N) acc[i][j][e] = -INFINITY;
+          top = fmaxf(top, acc[i][j][e]);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        const float base = ce_base(top);
+#pragma unroll
+        for (int j = 0; j < S; ++j) sum += ce_exp<T>(acc[i][j][e] - base);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        if ((lane & 31) == 0 && m < p.M) out[m] = float2{top, sum};
+      }
+    return;
+  }
+  if constexpr (ACT == kCeGrad) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = m0 + wm + i * 32 + acc_row(e, lane);
+        if (m >= p.M) continue;
+        const CeRow row = ce.rows[m];
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const int n = n0 + wn + j * 32 + (lane & 31);
+          if (n < ce.ld) stf((To *)p.out + (int64_t)m * ce.ld + n, n < p.N ? ce_dl<T>(row, acc[i][j][e], ce.col0 + n) : 0.f);
+        }
+      }
+    return;
   }
   if (splits > 1) part += (int64_t)split * p.M * p.N;
 #pragma unroll
@@ -478,11 +526,7 @@ MOE_DEV void tile_epilogue(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2
   }
 }
 
-// ---- the cross entropy's epilogues (cross_entropy.hip) ----------------------------
-// Logits l = x W^T stay in the accumulators.  The forward leaves the largest value and the sum of
-// exponentials of a tile's columns for each row, and the target's logit; the backward leaves dl.
-constexpr int kCeStats = 16, kCeGrad = 17;  // in the place of an activation
-
+// ---- the cross entropy's epilogues of these tiles ----------------------------------
 // A lane holds 4 HN columns per half of 2 HM rows: its own maximum and sum first, then the 4 lanes of a row,
 // then the WGN waves through LDS.
 template <int HM, int HN, int WGM, int WGN>
@@ -577,7 +621,7 @@ MOE_DEV void ce_grad(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2][HM][
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = n + 4 * h + e;
-          v[h][e] = col < p.N ? ce_dl(row, v[h][e], q.ce.col0 + col) : 0.f;
+          v[h][e] = col < p.N ? ce_dl<bf16_t>(row, v[h][e], q.ce.col0 + col) : 0.f;
         }
       put8((bf16_t *)p.out + (int64_t)m * q.ce.ld + n, v);
     }
@@ -1124,6 +1168,36 @@ hipError_t run_stream(const GemmArgs &a, int act, hipStream_t st) {
 }
 
 template <bool AK, bool BKM, typename T, typename To>
+hipError_t run_staged(const GemmArgs &a, const Plan &pl, int act, void *part, const CeArgs &ce, hipStream_t st) {
+  const int ts = 64 * pl.shape;
+  // memory rows (of lda, ldb elements, their whole length) on lines of four elements
+  const bool fours = a.lda % 4 == 0 && a.ldb % 4 == 0 && on_line(a.A, 4 * sizeof(T)) && on_line(a.B, 4 * sizeof(T));
+  const int grid = ((a.N + ts - 1) / ts) * ((a.M + ts - 1) / ts) * pl.splits;
+  auto run = [&](auto A) {
+    constexpr int ACT = decltype(A)::value;
+    float *const out = (float *)part;
+    if constexpr (sizeof(T) == 2) {
+      if (pl.shape == 2) {
+        if (fours) staged_gemm<T, To, 2, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
+        else staged_gemm<T, To, 2, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
+        return;
+      }
+    }
+    if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
+    else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
+  };
+  if constexpr (AK && BKM && sizeof(T) == sizeof(To)) {
+    if (act >= kCeStats) {
+      if (act == kCeStats) run(std::integral_constant<int, kCeStats>());
+      else run(std::integral_constant<int, kCeGrad>());
+      return hipGetLastError();
+    }
+  }
+  by_act_of<AK && BKM>(act, run);
+  return hipGetLastError();
+}
+
+template <bool AK, bool BKM, typename T, typename To>
 hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
   if constexpr (AK) {
     // in runs of rows where one launch could not hold them (no sizes in memory make dW's do)
@@ -1175,25 +1249,8 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
       return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
     }
   }
-  const Plan pl = staged_plan(a.M, a.N, a.K, sizeof(T) == 2);
-  const int ts = 64 * pl.shape;
-  // memory rows (of lda, ldb elements, their whole length) on lines of four elements
-  const bool fours = a.lda % 4 == 0 && a.ldb % 4 == 0 && on_line(a.A, 4 * sizeof(T)) && on_line(a.B, 4 * sizeof(T));
-  const int grid = ((a.N + ts - 1) / ts) * ((a.M + ts - 1) / ts) * pl.splits;
-  by_act_of<AK && BKM>(act, [&](auto A) {
-    constexpr int ACT = decltype(A)::value;
-    float *const out = (float *)part;
-    if constexpr (sizeof(T) == 2) {
-      if (pl.shape == 2) {
-        if (fours) staged_gemm<T, To, 2, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-        else staged_gemm<T, To, 2, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-        return;
-      }
-    }
-    if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-    else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out);
-  });
-  const hipError_t e = hipGetLastError();
+  const Plan pl = a.plan.shape ? a.plan : staged_plan(a.M, a.N, a.K, sizeof(T) == 2);
+  const hipError_t e = run_staged<AK, BKM, T, To>(a, pl, act, part, CeArgs{}, st);
   if (e != hipSuccess || pl.splits == 1) return e;
   return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
 }
@@ -1273,17 +1330,38 @@ hipError_t launch_ce_tiles(const void *x, const void *W, void *dl, const CeArgs 
   const int shape = unsplit_shape(M, shape_v, K);
   return dl ? run_piped<true, true, bf16_t>(q, shape, kCeGrad, st) : run_piped<true, true, float>(q, shape, kCeStats, st);
 }
-size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype) { return part_bytes(M, N, K, dtype == MOE_BF16); }
+bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype) {
+  return M > 16 && V > 16 && launch_rows(M, V) >= M && staged_plan(M, V, K, dtype == MOE_BF16).splits == 1;
+}
+int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype) { return 32 * staged_plan(M, V, K, dtype == MOE_BF16).shape; }
+hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
+                            hipStream_t st) {
+  GemmArgs a{x, W, nullptr, nullptr, dl, nullptr, M, V, K, K, K, false};
+  const Plan pl{staged_plan(M, shape_v, K, dtype == MOE_BF16).shape, 1};
+  const int act = dl ? kCeGrad : kCeStats;
+  if (dtype == MOE_F32) return run_staged<true, true, float, float>(a, pl, act, nullptr, ce, st);
+  return run_staged<true, true, bf16_t, bf16_t>(a, pl, act, nullptr, ce, st);
+}
+// The plan of dX and dW: staged fp32 tiles by rounds over the chip
+static Plan ce_plan(int64_t M, int64_t N, int64_t K, int dtype) {
+  return dtype == MOE_F32 ? Plan{1, rounds_splits(M, N, K)} : Plan{0, 1};
+}
+size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (dtype == MOE_BF16) return part_bytes(M, N, K, true);
+  const int k = rounds_splits(M, N, K);
+  return k > 1 ? (size_t)k * M * N * 4 : 0;
+}
+size_t ce_logits_part_bytes(int64_t M, int64_t V, int64_t K, int dtype) { return part_bytes(M, V, K, dtype == MOE_BF16); }
 hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
                         int V, int dtype, void *part, hipStream_t st) {
-  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false};
+  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false, ce_plan(M, K, V, dtype)};
   if (dtype == MOE_F32) return gemm<true, false, float, float>(a, MOE_ACT_NONE, part, st);
   if (out_f32) return gemm<true, false, bf16_t, float>(a, MOE_ACT_NONE, part, st);
   return gemm<true, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
 }
 hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, void *dW, int M, int K, int V, int dtype, void *part,
                         hipStream_t st) {
-  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false};
+  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false, ce_plan(V, K, M, dtype)};
   if (dtype == MOE_F32) return gemm<false, false, float, float>(a, MOE_ACT_NONE, part, st);
   return gemm<false, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
 }
