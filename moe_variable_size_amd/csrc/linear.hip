@@ -208,6 +208,20 @@ MOE_DEV f32x4 stage_four(const float *lds, int r, int k) {
 // row of register i of a 32 x 32 accumulator
 MOE_DEV int acc_row(int i, int lane) { return ((i >> 2) << 3) + ((lane >> 5) << 2) + (i & 3); }
 
+// f over the 32 lanes of a half wave: within 16 by lane permutations of the operand (neighbours, pairs, then halves and
+// rows mirrored, once their members are alike), the last step through LDS's crossbar.
+template <class F>
+MOE_DEV float over_half(float v, F &&f) {
+  auto other = [&](auto ctrl) __attribute__((always_inline)) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  v = f(v, other(std::integral_constant<int, 0xB1>()));   // quad_perm 1 0 3 2
+  v = f(v, other(std::integral_constant<int, 0x4E>()));   // quad_perm 2 3 0 1
+  v = f(v, other(std::integral_constant<int, 0x141>()));  // row_half_mirror
+  v = f(v, other(std::integral_constant<int, 0x140>()));  // row_mirror
+  return f(v, __shfl_xor(v, 16, 64));
+}
+
 // splits > 1: range blockIdx / tiles of the reduction, fp32 products to part [splits][M][N]
 template <typename T, typename To, int S, int E, bool AK, bool BKM, int ACT>
 __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part, CeArgs ce) {
@@ -290,13 +304,11 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
           if (n + j * 32 >= p.N) acc[i][j][e] = -INFINITY;
           top = fmaxf(top, acc[i][j][e]);
         }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        top = over_half(top, [](float a, float b) __attribute__((always_inline)) { return fmaxf(a, b); });
         const float base = ce_base(top);
 #pragma unroll
         for (int j = 0; j < S; ++j) sum += ce_exp<T>(acc[i][j][e] - base);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        sum = over_half(sum, [](float a, float b) __attribute__((always_inline)) { return a + b; });
         if ((lane & 31) == 0 && m < p.M) out[m] = float2{top, sum};
       }
     return;

@@ -80,14 +80,15 @@ inline Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   return Plan{1, (int)(k < 1 ? 1 : k)};
 }
 // Reduction ranges of a product in fp32 staged tiles of a cross entropy's gradient: the same limits, chosen by rounds of
-// workgroups over the 256 CUs (0.45 us per step of each that shares a CU) and what the join costs, as plan_of.  dX of 777 x
-// 5003 x 1001 (208 tiles) in 4 ranges, as above, 107 us, in 6 92.
+// workgroups over the 256 CUs (0.63 us per step of each that shares a CU, 0.85 alone) and what the join costs, as plan_of.
+// dX of 777 x 5003 x 1001 (208 tiles) in 1 range 133 us, in 4, as above, 102, in 6 90 (and 6 for the join).
 inline int rounds_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t t1 = ((M + 63) / 64) * ((N + 63) / 64), steps = (K + SBK - 1) / SBK;
   int best = 1;
   double least = 0;
   for (int k = 1; k <= 16 && (k == 1 || (steps >= 4 * k && t1 * k <= 2560)); ++k) {
-    double t = __builtin_ceil(t1 * k / 256.0) * __builtin_ceil((double)steps / k) * 0.45;
+    const double each = __builtin_ceil(t1 * k / 256.0) * 0.63;
+    double t = (each > 0.85 ? each : 0.85) * __builtin_ceil((double)steps / k);
     if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
     if (k == 1 || t < least) {
       least = t;
