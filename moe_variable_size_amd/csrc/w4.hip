@@ -24,8 +24,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int STREAM_LEAST = 256;
-constexpr int BLK = 128;  // reduction elements of a block, 64 bytes of codes
+constexpr int BLK = 128;   // reduction elements of a block, 64 bytes of codes
+constexpr int WAVES = 8;   // of a workgroup, but for single tokens' experts
+constexpr int TOKEN_W = 16;
 
 MOE_DEV __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)p;
@@ -176,7 +177,6 @@ struct Wave {
   }
   // all of the wave's blocks; they begin at another place in each workgroup, since rows are often a power of two apart and
   // all workgroups on the same block would meet on few channels
-  template <int NW>
   MOE_DEV void run(const Weight &p, const Buffers &f, const void *x, uint32_t xn, int n0, uint32_t place) {
     setup(p, n0);
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), whole = p.K / BLK;
@@ -188,28 +188,28 @@ struct Wave {
       load<false>(d, p, f, x, xn, u < whole, u >= whole ? 0 : b >= whole ? b - whole : b);
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d, wid + d * NW);
-    for (int u = wid; u < whole; u += D * NW) {
+    for (int d = 0; d < D; ++d) fetch(d, wid + d * WAVES);
+    for (int u = wid; u < whole; u += D * WAVES) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         __builtin_amdgcn_sched_barrier(0);
         multiply(d);
         __builtin_amdgcn_sched_barrier(0);
-        fetch(d, u + (D + d) * NW);
+        fetch(d, u + (D + d) * WAVES);
       }
     }
-    if (whole < p.blocks && wid == whole % NW) {
+    if (whole < p.blocks && wid == whole % WAVES) {
       load<true>(0, p, f, x, xn, true, whole);
       multiply(0);
     }
   }
 };
 
-// The waves' sums of 16 rows (`rows` of them in use), added in wave order through red [NW][16][16 TJ + 4]; f(row, column,
+// The waves' sums of 16 rows (`rows` of them in use), added in wave order through red [WAVES][16][16 TJ + 4]; f(row, column,
 // sum) for each
 template <int TJ>
 constexpr int kPitch = 16 * TJ + 4;
-template <int TJ, int NW, class F>
+template <int TJ, class F>
 MOE_DEV void join_waves(float *red, const f32x4 (&acc)[TJ], int rows, F &&f) {
   constexpr int TN = 16 * TJ;
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
@@ -222,10 +222,10 @@ MOE_DEV void join_waves(float *red, const f32x4 (&acc)[TJ], int rows, F &&f) {
       if (r < rows) red[(wid * 16 + r) * kPitch<TJ> + j * 16 + (lane & 15)] = acc[j][e];
     }
   __syncthreads();
-  for (int e = threadIdx.x; e < min(rows, 16) * TN; e += NW * 64) {
+  for (int e = threadIdx.x; e < min(rows, 16) * TN; e += WAVES * 64) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[(w * 16 + e / TN) * kPitch<TJ> + e % TN];
+    for (int w = 0; w < WAVES; ++w) v += red[(w * 16 + e / TN) * kPitch<TJ> + e % TN];
     f(e / TN, e % TN, v);
   }
 }
@@ -250,9 +250,9 @@ MOE_DEV void finish(const DenseArgs &a, int act, int m, int n, float s) {
   stf((To *)a.out + at, s);
 }
 
-template <int TI, int TJ, int NW, int GP, bool ZEROS, typename To>
-__global__ __launch_bounds__(NW * 64) void dense_kernel(DenseArgs a, int act) {
-  __shared__ __align__(16) float red[NW * 16 * kPitch<TJ>];
+template <int TI, int TJ, int GP, bool ZEROS, typename To>
+__global__ __launch_bounds__(WAVES * 64) void dense_kernel(DenseArgs a, int act) {
+  __shared__ __align__(16) float red[WAVES * 16 * kPitch<TJ>];
   const int tm = (a.M + 16 * TI - 1) / (16 * TI);
   // the row tiles of one column tile are neighbours: its codes come from L2 from the second on
   const int m0 = blockIdx.x % tm * (16 * TI), n0 = blockIdx.x / tm * (16 * TJ);
@@ -264,12 +264,12 @@ __global__ __launch_bounds__(NW * 64) void dense_kernel(DenseArgs a, int act) {
     const int r = i * 16 + (lane & 15);
     v.xo[i] = m0 + r < a.M ? (uint32_t)r * (uint32_t)p.K * 2 : kOobOffset;
   }
-  v.template run<NW>(p, Buffers::of(p, 0), a.x + (int64_t)m0 * p.K, (uint32_t)min(16 * TI, a.M - m0) * (uint32_t)p.K * 2, n0, blockIdx.x);
+  v.run(p, Buffers::of(p, 0), a.x + (int64_t)m0 * p.K, (uint32_t)min(16 * TI, a.M - m0) * (uint32_t)p.K * 2, n0, blockIdx.x);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int rows = a.M - m0 - i * 16;
     if (rows <= 0) break;
-    join_waves<TJ, NW>(red, v.acc[i], rows, [&](int r, int c, float s) {
+    join_waves<TJ>(red, v.acc[i], rows, [&](int r, int c, float s) {
       if (n0 + c < p.N) finish<To>(a, act, m0 + i * 16 + r, n0 + c, s);
     });
   }
@@ -285,7 +285,7 @@ struct ExpertArgs {
   int T, layout, capacity, tn, e0;  // e0: first expert of the launch
 };
 
-template <int TI, int TJ, int NW, int GP, bool ZEROS>
+template <int TI, int TJ, int GP, bool ZEROS>
 MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row0, int rows) {
   const int lane = threadIdx.x & 63;
   const Weight &p = a.w;
@@ -295,11 +295,11 @@ MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row
     const int r = i * 16 + (lane & 15), t = r < rows ? a.row_to_token[row0 + r] : -1;
     v.xo[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.K * 2 : kOobOffset;
   }
-  v.template run<NW>(p, Buffers::of(p, e), a.x, (uint32_t)a.T * (uint32_t)p.K * 2, n0, blockIdx.x);
+  v.run(p, Buffers::of(p, e), a.x, (uint32_t)a.T * (uint32_t)p.K * 2, n0, blockIdx.x);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     if (i * 16 >= rows) break;
-    join_waves<TJ, NW>(red, v.acc[i], rows - i * 16, [&](int r, int c, float s) {
+    join_waves<TJ>(red, v.acc[i], rows - i * 16, [&](int r, int c, float s) {
       r += i * 16;
       if (n0 + c >= p.N) return;
       const int t = a.row_to_token[row0 + r];
@@ -310,15 +310,15 @@ MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row
 
 // One workgroup per expert and column tile; an expert's rows 16 TI at a time (the last ones 16 if that will do), its
 // codes then coming out of the caches.
-template <int TI, int TJ, int NW, int GP, bool ZEROS>
-__global__ __launch_bounds__(NW * 64) void expert_kernel(ExpertArgs a) {
-  __shared__ __align__(16) float red[NW * 16 * kPitch<TJ>];
+template <int TI, int TJ, int GP, bool ZEROS>
+__global__ __launch_bounds__(WAVES * 64) void expert_kernel(ExpertArgs a) {
+  __shared__ __align__(16) float red[WAVES * 16 * kPitch<TJ>];
   const int e = a.e0 + blockIdx.x / a.tn, n0 = blockIdx.x % a.tn * (16 * TJ);
   const int count = __builtin_amdgcn_readfirstlane(a.counts[e]);
   const int first = a.layout == MOE_LAYOUT_MASKED ? e * a.capacity : __builtin_amdgcn_readfirstlane(a.offsets[e]) - count;
   for (int r = 0; r < count; r += 16 * TI) {
-    if (TI > 1 && count - r <= 16) expert_rows<1, TJ, NW, GP, ZEROS>(a, red, e, n0, first + r, count - r);
-    else expert_rows<TI, TJ, NW, GP, ZEROS>(a, red, e, n0, first + r, min(count - r, 16 * TI));
+    if (TI > 1 && count - r <= 16) expert_rows<1, TJ, GP, ZEROS>(a, red, e, n0, first + r, count - r);
+    else expert_rows<TI, TJ, GP, ZEROS>(a, red, e, n0, first + r, min(count - r, 16 * TI));
   }
 }
 
@@ -359,14 +359,13 @@ MOE_DEV void dma4(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, uin
                : "memory", "m0");
 }
 
-constexpr int STREAM_W = 8;  // waves
 template <int TI, int GP, bool ZEROS>
 struct Stream {
   static constexpr int G2 = 2 * GP;                               // groups of a stage
   static constexpr int XB = TI * 8192;                            // x: [16 TI][512 bytes]
   static constexpr int WB = 2048 + 256 + (ZEROS ? 256 : 0);       // a wave's codes, scales [G2][16], zeros [G2][16]
-  static constexpr int STAGE = XB + STREAM_W * WB;
-  static constexpr int XL = TI * 8 / STREAM_W;                    // a wave's loads of x
+  static constexpr int STAGE = XB + WAVES * WB;
+  static constexpr int XL = TI * 8 / WAVES;                    // a wave's loads of x
 };
 
 template <int TI, int GP, bool ZEROS>
@@ -476,9 +475,9 @@ MOE_DEV void stream_rows(const ExpertArgs &a, char *lds, int e, int n0, int row0
 }
 
 template <int GP, bool ZEROS>
-__global__ __launch_bounds__(STREAM_W * 64, 4) void stream_kernel(ExpertArgs a) {
+__global__ __launch_bounds__(WAVES * 64, 4) void stream_kernel(ExpertArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const int e = a.e0 + blockIdx.x / a.tn, n0 = blockIdx.x % a.tn * (16 * STREAM_W);
+  const int e = a.e0 + blockIdx.x / a.tn, n0 = blockIdx.x % a.tn * (16 * WAVES);
   const int count = __builtin_amdgcn_readfirstlane(a.counts[e]);
   const int first = a.layout == MOE_LAYOUT_MASKED ? e * a.capacity : __builtin_amdgcn_readfirstlane(a.offsets[e]) - count;
   for (int r = 0; r < count; r += 32) {
@@ -492,8 +491,9 @@ __global__ __launch_bounds__(STREAM_W * 64, 4) void stream_kernel(ExpertArgs a) 
 // first and the 8 of the second block of a pair; x's 16 rows are those of both blocks in turn (row r: r >> 1, block r &
 // 1; rows that are not there repeat the first), and of the products' 16 x 16 sums those of one block with itself count.
 // Since the other operand is in LDS, codes can be loaded D pairs ahead.
-template <int TJ, int GP, bool ZEROS, int D>
+template <int TJ, int GP, bool ZEROS>
 struct Few {
+  static constexpr int D = 2;
   u32x4 w[D][TJ];
   uint32_t s[D][TJ], z[D][TJ];  // lane quarter q: of group q (q % 2, 0) of the lane's block
   f32x4 acc[TJ];
@@ -586,35 +586,37 @@ MOE_DEV void stage_rows(char *lds, const bf16_t *x, int rows, int K, int threads
   }
 }
 
-template <int TJ, int NW, int GP, bool ZEROS, int D, typename To>
-__global__ __launch_bounds__(NW * 64) void few_kernel(DenseArgs a, int act) {
+template <int TJ, int GP, bool ZEROS, typename To>
+__global__ __launch_bounds__(WAVES * 64) void few_kernel(DenseArgs a, int act) {
   extern __shared__ __align__(16) char lds[];
   const Weight &p = a.w;
   const int n0 = blockIdx.x * (8 * TJ), wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = p.K / (2 * BLK), rot = pairs ? (int)(blockIdx.x % (uint32_t)pairs) : 0;
   const Buffers f = Buffers::of(p, 0);
-  Few<TJ, GP, ZEROS, D> v;
+  using F = Few<TJ, GP, ZEROS>;
+  constexpr int D = F::D;
+  F v;
   v.setup(p, n0, a.M, few_pitch(p.K));
   auto place = [&](int u) __attribute__((always_inline)) { return u >= pairs ? 0 : u + rot >= pairs ? u + rot - pairs : u + rot; };
 #pragma unroll
-  for (int d = 0; d < D; ++d) v.template load<false>(d, p, f, wid + d * NW < pairs, place(wid + d * NW));
-  stage_rows(lds, a.x, a.M, p.K, NW * 64);
+  for (int d = 0; d < D; ++d) v.template load<false>(d, p, f, wid + d * WAVES < pairs, place(wid + d * WAVES));
+  stage_rows(lds, a.x, a.M, p.K, WAVES * 64);
   __syncthreads();
-  for (int u = wid; u < pairs; u += D * NW) {
+  for (int u = wid; u < pairs; u += D * WAVES) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int at = u + d * NW, next = at + D * NW;
+      const int at = u + d * WAVES, next = at + D * WAVES;
       __builtin_amdgcn_sched_barrier(0);
       if (at < pairs) v.multiply(d, lds, place(at), 1.f);
       __builtin_amdgcn_sched_barrier(0);
       v.template load<false>(d, p, f, next < pairs, place(next));
     }
   }
-  if (pairs * 2 * BLK < p.K && wid == pairs % NW) {
+  if (pairs * 2 * BLK < p.K && wid == pairs % WAVES) {
     v.template load<true>(0, p, f, true, pairs);
     v.multiply(0, lds, pairs, 1.f);
   }
-  join_few<TJ, NW>((float *)lds, v.acc, a.M, [&](int r, int c, float s) {
+  join_few<TJ, WAVES>((float *)lds, v.acc, a.M, [&](int r, int c, float s) {
     if (n0 + c < p.N) finish<To>(a, act, r, n0 + c, s);
   });
 }
@@ -641,15 +643,18 @@ struct Walk {
 };
 
 // One workgroup per token and column tile: its waves share the pairs of all k experts, whose routing weights go into
-// the scales; plain stores.
-template <int TJ, int NW, int GP, bool ZEROS, int D>
-__global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
+// the scales; plain stores.  8 of 64 experts of 7168 x 2048, us: 18.1 with 16 waves and tiles of 8 columns, 20.8 with 8
+// waves, 22.5 with tiles of 16 columns, 36 with x from memory.
+template <int GP, bool ZEROS>
+__global__ __launch_bounds__(TOKEN_W * 64) void token_kernel(TokenArgs a) {
   extern __shared__ __align__(16) char lds[];
   const Weight &p = a.w;
   const int64_t t = blockIdx.x / a.tn;
-  const int n0 = (int)(blockIdx.x - t * a.tn) * (8 * TJ), wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (int)(blockIdx.x - t * a.tn) * 8, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = p.K / (2 * BLK);
-  Few<TJ, GP, ZEROS, D> v;
+  using F = Few<1, GP, ZEROS>;
+  constexpr int D = F::D;
+  F v;
   v.setup(p, n0, 1, few_pitch(p.K));
   float weight[D];
   int at[D];  // -1: no expert
@@ -667,16 +672,16 @@ __global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
     const bool use = slot_of(walk.slot, f, weight[d]);
     at[d] = use ? walk.u : -1;
     v.template load<false>(d, p, f, use, use ? walk.u : 0);
-    walk.go(NW, pairs, a.k);
+    walk.go(TOKEN_W, pairs, a.k);
   };
   if (pairs) {
     walk.go(wid, pairs, a.k);
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d);
   }
-  stage_rows(lds, a.x + t * p.K, 1, p.K, NW * 64);
+  stage_rows(lds, a.x + t * p.K, 1, p.K, TOKEN_W * 64);
   __syncthreads();
-  for (int u = wid; u < a.k * pairs; u += D * NW) {
+  for (int u = wid; u < a.k * pairs; u += D * TOKEN_W) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       __builtin_amdgcn_sched_barrier(0);
@@ -686,7 +691,7 @@ __global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
     }
   }
   if (pairs * 2 * BLK < p.K) {
-    for (int slot = wid; slot < a.k; slot += NW) {
+    for (int slot = wid; slot < a.k; slot += TOKEN_W) {
       Buffers f;
       float w;
       if (!slot_of(slot, f, w)) continue;
@@ -694,7 +699,7 @@ __global__ __launch_bounds__(NW * 64) void token_kernel(TokenArgs a) {
       v.multiply(0, lds, pairs, w);
     }
   }
-  join_few<TJ, NW>((float *)lds, v.acc, 1, [&](int, int c, float s) {
+  join_few<1, TOKEN_W>((float *)lds, v.acc, 1, [&](int, int c, float s) {
     if (n0 + c < p.N) a.y[t * p.N + n0 + c] = s;
   });
 }
@@ -802,11 +807,11 @@ void by_form(const moe_w4_weight &w, F &&f) {
   else z(std::integral_constant<int, 1>());
 }
 
-template <int TI, int TJ, int NW, typename To>
+template <int TI, int TJ, typename To>
 hipError_t run_dense(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
   const int64_t tn = (w.N + 16 * TJ - 1) / (16 * TJ), M = a.M;
   // workgroups of one launch: below 2^31 work-items
-  const int64_t most = (((int64_t)1 << 31) / (NW * 64) / tn - 1) * 16 * TI, run = M < most ? M : most;
+  const int64_t most = (((int64_t)1 << 31) / (WAVES * 64) / tn - 1) * 16 * TI, run = M < most ? M : most;
   for (int64_t m = 0; m < M; m += run) {
     DenseArgs b = a;
     b.M = (int)(M - m < run ? M - m : run);
@@ -815,7 +820,7 @@ hipError_t run_dense(const moe_w4_weight &w, const DenseArgs &a, int act, hipStr
     if (a.res) b.res = (const To *)a.res + m * w.N;
     const int grid = (int)(tn * ((b.M + 16 * TI - 1) / (16 * TI)));
     by_form(w, [&](auto gp, auto z) {
-      dense_kernel<TI, TJ, NW, decltype(gp)::value, decltype(z)::value, To><<<grid, NW * 64, 0, st>>>(b, act);
+      dense_kernel<TI, TJ, decltype(gp)::value, decltype(z)::value, To><<<grid, WAVES * 64, 0, st>>>(b, act);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -828,24 +833,41 @@ size_t few_lds(int rows, int64_t K, int NW, int TJ) {
   const size_t x = (size_t)rows * ((K + 2 * BLK - 1) / (2 * BLK) * 512 + 64), red = (size_t)2 * NW * 4 * 8 * TJ * 4;
   return x > 65536 ? 0 : x > red ? x : red;
 }
-template <int TJ, int NW, int D, typename To>
+template <int TJ, typename To>
 hipError_t run_few(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
   const int grid = (int)((w.N + 8 * TJ - 1) / (8 * TJ));
   by_form(w, [&](auto gp, auto z) {
-    few_kernel<TJ, NW, decltype(gp)::value, decltype(z)::value, D, To><<<grid, NW * 64, few_lds(a.M, w.K, NW, TJ), st>>>(a, act);
+    few_kernel<TJ, decltype(gp)::value, decltype(z)::value, To><<<grid, WAVES * 64, few_lds(a.M, w.K, WAVES, TJ), st>>>(a, act);
   });
   return hipGetLastError();
 }
+
+// Which kernel and tile: narrow columns while they leave CUs without a workgroup, wide ones (fewer rows of x to
+// fetch for the codes) from then on.  us, groups of 128:
+// At most 2 rows, 4 below 4096 columns, with x in LDS; M x K x N, tiles of 8, 16, 32 columns | dense of 16, 32:
+//     1 x 8192 x 2048     5.0   5.9   8.3 |  6.5   8.4        4 x 8192 x 2048    7.0   8.1       |  7.9
+//     1 x 4096 x 4096     5.4   5.2   6.6 |  4.8   5.9        3 x 4096 x 4096    5.8   5.6   7.1 |  5.2   6.2
+//     1 x 8192 x 8192    11.3  10.1  10.6 | 13.4  10.1        3 x 8192 x 8192   15.6  11.6  12.0 | 14.0  10.6
+//     1 x 8192 x 12288   15.2  13.2  14.5 | 18.4  17.8        3 x 8192 x 12288  19.5  14.9  16.2 | 19.8  18.4
+//     1 x 8192 x 16384   20.1  17.4  15.9 | 23.2  18.5        3 x 8192 x 16384  24.8  19.6  17.5 | 24.9  19.2
+// up to 16 rows, tiles of 16, 32 columns: 16 x 4096 x 4096 7.4 and 8.7, 16 x 8192 x 8192 21.7 and 14.5
+// more, tiles of 32 rows and 32, 64 columns: 64 x 8192 x 4096 23.0 and 27.9, 64 x 8192 x 8192 44.1 and 29.1.
+// (From some 256 rows on, 107 us for 256 x 8192 x 8192, weights are better dequantised for a matrix product.)
 template <typename To>
 hipError_t dense(const moe_w4_weight &w, const DenseArgs &a, int act, hipStream_t st) {
-  if (a.M <= 4 && few_lds(a.M, w.K, 8, 2)) return run_few<2, 8, 2, To>(w, a, act, st);
+  const bool narrow = (w.N + 15) / 16 < 256;
+  if (a.M <= (narrow ? 4 : 2) && few_lds(a.M, w.K, WAVES, 4)) {
+    if (narrow) return run_few<1, To>(w, a, act, st);
+    if ((w.N + 31) / 32 >= 512) return run_few<4, To>(w, a, act, st);
+    return run_few<2, To>(w, a, act, st);
+  }
   const int64_t tm = (a.M + 31) / 32;
   if (a.M > 16) {
-    if (tm * ((w.N + 63) / 64) >= 256) return run_dense<2, 4, 8, To>(w, a, act, st);
-    return run_dense<2, 2, 8, To>(w, a, act, st);
+    if (tm * ((w.N + 63) / 64) >= 256) return run_dense<2, 4, To>(w, a, act, st);
+    return run_dense<2, 2, To>(w, a, act, st);
   }
-  if ((w.N + 31) / 32 >= 256) return run_dense<1, 2, 8, To>(w, a, act, st);
-  return run_dense<1, 1, 8, To>(w, a, act, st);
+  if ((w.N + 31) / 32 >= 256) return run_dense<1, 2, To>(w, a, act, st);
+  return run_dense<1, 1, To>(w, a, act, st);
 }
 
 }  // namespace
@@ -896,29 +918,33 @@ hipError_t launch_fused_w4(const void *x, const moe_w4_weight &w, const moe_sche
     }
     return hipSuccess;
   };
-  if ((int64_t)s.E * ((a.w.N + 127) / 128) >= STREAM_LEAST)
+  // 128 columns per workgroup where that leaves few CUs without one: 8 experts of 4096 x 2048 (128 workgroups) with 12 rows
+  // each take 15.4 us by tiles of 32 columns and 19.2 so, 4 of 4096 x 7168 (224) 28.7 and 20.3, 16 of 4096 x 2048 (256)
+  // 29.4 and 20.7, 64 105.9 and 59.8
+  if ((int64_t)s.E * ((a.w.N + 127) / 128) >= 192)
     return by_experts(128, [&](auto gp, auto z, int grid) {
       constexpr int GP = decltype(gp)::value;
       constexpr bool Z = decltype(z)::value;
       hipError_t e = allow_lds<stream_kernel<GP, Z>>(2 * Stream<2, GP, Z>::STAGE);
-      if (e == hipSuccess) stream_kernel<GP, Z><<<grid, STREAM_W * 64, 2 * Stream<2, GP, Z>::STAGE, st>>>(a);
+      if (e == hipSuccess) stream_kernel<GP, Z><<<grid, WAVES * 64, 2 * Stream<2, GP, Z>::STAGE, st>>>(a);
     });
-  const bool few = s.S <= 12 * (int64_t)s.E;
+  // 16 rows at a time, or 32 where most experts have more than 16: 8 experts of 4096 x 2048 take 12.5 and 14.3 us with 4
+  // rows each, 16.5 and 18.9 with 16, 30.2 and 27.8 with 32
+  const bool few = s.S <= 16 * (int64_t)s.E;
   return by_experts(32, [&](auto gp, auto z, int grid) {
     constexpr int GP = decltype(gp)::value;
     constexpr bool Z = decltype(z)::value;
-    if (few) expert_kernel<1, 2, 8, GP, Z><<<grid, 512, 0, st>>>(a);
-    else expert_kernel<2, 2, 8, GP, Z><<<grid, 512, 0, st>>>(a);
+    if (few) expert_kernel<1, 2, GP, Z><<<grid, WAVES * 64, 0, st>>>(a);
+    else expert_kernel<2, 2, GP, Z><<<grid, WAVES * 64, 0, st>>>(a);
   });
 }
 
 int64_t token_w4_width() { return (65536 - 64) / 512 * 2 * BLK; }
 hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t *ids, const float *weights, int64_t T, int k, float *y,
                            hipStream_t st) {
-  constexpr int TJ = 1, NW = 16;
   TokenArgs a{weight_of(w), (const bf16_t *)x, ids, weights, y, k, (int)w.E, 0};
-  a.tn = (a.w.N + 8 * TJ - 1) / (8 * TJ);
-  const int64_t run = ((int64_t)1 << 31) / (NW * 64) / a.tn;  // tokens of one launch
+  a.tn = (a.w.N + 7) / 8;
+  const int64_t run = ((int64_t)1 << 31) / (TOKEN_W * 64) / a.tn;  // tokens of one launch
   for (int64_t t = 0; t < T; t += run) {
     TokenArgs b = a;
     b.x += t * w.K;
@@ -927,7 +953,7 @@ hipError_t launch_token_w4(const void *x, const moe_w4_weight &w, const int32_t 
     b.y += t * w.N;
     const int grid = (int)((T - t < run ? T - t : run) * a.tn);
     by_form(w, [&](auto gp, auto z) {
-      token_kernel<TJ, NW, decltype(gp)::value, decltype(z)::value, 4><<<grid, NW * 64, few_lds(1, w.K, NW, TJ), st>>>(b);
+      token_kernel<decltype(gp)::value, decltype(z)::value><<<grid, TOKEN_W * 64, few_lds(1, w.K, TOKEN_W, 1), st>>>(b);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
