@@ -585,7 +585,7 @@ int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *exper
  *   16-byte lines); for at most 16 rows and for products of few tiles, whose reduction
  *   is split, a piece's logits, at most 256 MB or 1024 columns of them.
  * Sums are fp32 per row and run of columns, joined in a fixed order (reproducible).
- * A logit of +inf or NaN makes its row's loss NaN.
+ * A logit of +inf or NaN makes its row's loss NaN (0 in a row that does not count).
  */
 #define MOE_REDUCE_NONE 0
 #define MOE_REDUCE_SUM 1
@@ -602,7 +602,8 @@ int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t
  *   dl = g_m ((1 + 2 z_weight lse_m) exp(l - lse_m) - [v = t]), 0 in rows that do
  *   not count, rounded to `dtype` for the two products;
  *   dX = dl W [M, K],  dW = dl^T x [V, K], in `dtype`: each OVERWRITTEN, or NULL to
- *   skip.
+ *   skip.  (0 times what is not finite is NaN: rows of x that do not count have to be
+ *   finite for dW, too.)
  *   x, W, targets, z_weight as in the forward, lse [M] and total [3] from it (total
  *   for _MEAN alone).  M may be 0 (dW is then zeros).
  *   workspace: moe_linear_ce_bwd_workspace_bytes(...) bytes, 256-byte aligned: dl
@@ -655,7 +656,7 @@ typedef struct moe_adamw_tensor {
  *   ([1] each, NULL: the numbers) that are read when the launch runs, for graphs
  *   that are replayed; step is then not looked at.
  *   grad_scale [1] (device, NULL for 1): s; where it is not finite, nothing is
- *   changed.
+ *   changed (t is the caller's: whether such a step counts).
  *   0 <= beta < 1, 0 <= eps, lr and weight_decay finite (MOE_ERR_OPTION).
  *   param_dtype and grad_dtype MOE_F32 or MOE_BF16 each; a master copy needs
  *   MOE_BF16 parameters (MOE_ERR_DTYPE).
@@ -731,7 +732,9 @@ int moe_set_combine(int32_t mode);
  * stream and keeps them per kernel family.  Families: "build_schedule",
  * "fill_zero", "grouped_gemm", "fused_fwd", "bwd_dx", "bwd_dw", "tile_map",
  * "gated_up", "gated_down", "fused_fwd_fp8", "gated_bwd_dw_down",
- * "gated_bwd_dh", "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx".
+ * "gated_bwd_dh", "gated_bwd_dx", "gated_bwd_dw_gu", "fused_fwd_mx",
+ * "linear_ce_fwd", "linear_ce_bwd", "adamw", "w4_quantize", "w4_dequantize",
+ * "linear_w4", "fused_fwd_w4", "token_fwd_w4", among others.
  *   moe_timing_enable(1) clears earlier records and starts recording;
  *   moe_timing_enable(0) stops recording (records are kept).
  *   moe_timing_read waits for the recorded events of `family` and returns the

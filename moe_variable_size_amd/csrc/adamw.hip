@@ -8,6 +8,12 @@
 // a fraction 1 - b of itself per step, mostly less than half the distance of two codes (1/16 to 1/8): rounded to
 // nearest it would stand still.  So codes are rounded up with the probability of the remainder, by a
 // hash of (seed, t, tensor, element): right on average, and the same in every run.
+//
+// Memory bound: 22 bytes per element for bf16 parameters and gradients with fp32 states, 10 and 16 / 256 with 8-bit
+// ones.  8 elements per thread make every access 16 or 32 bytes wide, and 32 lanes a block of 256, whose largest value needs no
+// LDS.  Tensors go by in one launch, their descriptors in its arguments (48 of them: 6.8 us for 12 small ones;
+// a table in memory would have to be copied there first).  277M elements, bf16: 1099 us with fp32 states (5.5 TB/s; a
+// large copy reaches 4.8), 560 with 8-bit ones (5.0).  Non-temporal loads and stores of the states: 1157 and 553.
 #include <math.h>
 
 #include "common.hpp"

@@ -113,7 +113,9 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 
 // The cross entropy's epilogues (cross_entropy.hip), in the place of an activation: logits l = x W^T stay in the
 // accumulators.  The forward leaves the largest value and the sum of exponentials of a row's columns in a tile (or a wave
-// of it), and the target's logit; the backward leaves dl.
+// of it), and the target's logit; the backward leaves dl.  The products bound both: 8192 x 4096 x 65536 in bf16 takes 3.08
+// ms with the statistics (1.43 PFLOP/s) and 3.32 with the gradient (1.32), its bf16 stores among them; 777 x 1001 x 5003 in
+// fp32 111 and 106 us in the staged tiles, 109 for the plain product with its stores.
 constexpr int kCeStats = 16, kCeGrad = 17;
 
 // ---- staged tiles: any alignment and size ------------------------------------

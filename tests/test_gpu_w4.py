@@ -58,7 +58,9 @@ ACTS = {"none": lambda z: z, "relu": lambda z: np.maximum(z, 0), "silu": lambda 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zeros", [True, False])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 8), (1, 16, 128), (1, 4099, 264), (2, 37, 4096), (15, 64, 1032), (16, 129, 2048), (17, 33, 384),
-                                   (32, 200, 136), (33, 65, 640), (64, 130, 1024), (65, 47, 72), (200, 31, 1320), (3, 50, 14336)])
+                                   (32, 200, 136), (33, 65, 640), (64, 130, 1024), (65, 47, 72), (200, 31, 1320), (3, 50, 14336),
+                                   # more columns: a few rows' tiles of 8 (above), 16 and 32, 16 and 32 dense columns, 32 rows x 64
+                                   (2, 4100, 264), (1, 16390, 72), (3, 4100, 264), (4, 8200, 136), (40, 8200, 136)])
 def test_linear(M, N, K, group, zeros):
     w, x = weight(N, K, group, zeros, seed=M + N), rows(M, K, seed=K)
     W, xx = values(w), f64(x)
