@@ -581,11 +581,14 @@ int moe_token_fwd_w4(const void *x, const moe_w4_weight *w, const int32_t *exper
  *   Element alignment, any sizes (bf16 runs fastest with K a multiple of 8 and
  *   16-byte aligned x and W); M may be 0; M <= 2^24, K and V <= 2^22.
  *   workspace: moe_linear_ce_fwd_workspace_bytes(...) bytes, 256-byte aligned:
- *   two numbers per row and tile (128 or 256 columns; 32 or 64 for fp32 and rows off
- *   16-byte lines); for at most 16 rows and for products of few tiles, whose reduction
- *   is split, a piece's logits, at most 256 MB or 1024 columns of them.
+ *   two numbers per row and run of 32 to 256 columns; for at most 16 rows and for
+ *   products of few tiles, whose reduction is split, a piece's logits, at most 256 MB
+ *   or 1024 columns of them.
  * Sums are fp32 per row and run of columns, joined in a fixed order (reproducible).
  * A logit of +inf or NaN makes its row's loss NaN (0 in a row that does not count).
+ * fp32 products (the logits' for more than 16 rows) are six products of bf16 parts,
+ * off by at most 2^-23 of their size; there a value of x (W) that is not finite, or
+ * above 3.39e38, makes its row's (every row's) logits NaN.
  */
 #define MOE_REDUCE_NONE 0
 #define MOE_REDUCE_SUM 1

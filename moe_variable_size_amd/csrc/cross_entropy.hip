@@ -7,11 +7,12 @@
 // the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
 // logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
 // fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it.
-// fp32 and rows off 16-byte lines do the same in the staged tiles.  Few rows, and products so small that their reduction
+// bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
 // bf16, 8192 x 4096 x 65536: 12.7 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.39 PFLOP/s and 43 us
-// besides; the loss of 2048 x 4096 x 50257 646 us.  One row x 4096 x 32000: 51 us, 38 of them the streamed product (7.0 TB/s),
+// besides; the loss of 2048 x 4096 x 50257 646 us.  fp32, 1074 x 600 x
+// 47121, loss and gradients: 1.60 ms (2.36 by fp32 instructions; 1.99 for logits kept and three such products).  One row x 4096 x 32000: 51 us, 38 of them the streamed product (7.0 TB/s),
 // the others two launches.
 #include "cross_entropy.hpp"
 
@@ -191,9 +192,13 @@ int64_t fwd_piece(int64_t M, int64_t K, int64_t V, Way way) {
   if (way == STAGED) return even_piece(V, ((int64_t)1 << 29) / M * 64 / 256 * 256);  // of one launch
   return even_piece(V, greatest(1024, ((int64_t)1 << 26) / M / 256 * 256));          // 256 MB of logits
 }
+// (fp32 tiles take no fewer than four columns, the last piece's among them)
+bool staged(int64_t M, int64_t K, int64_t V, int64_t piece, int dtype) {
+  return ce_staged(M, K, piece, dtype) && (dtype == MOE_BF16 || V % piece == 0 || V % piece >= 4);
+}
 Way fwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
   if (on_lines && dtype == MOE_BF16 && ce_tiles(M, K, fwd_piece(M, K, V, TILES))) return TILES;
-  return ce_staged(M, K, fwd_piece(M, K, V, STAGED), dtype) ? STAGED : MEMORY;
+  return staged(M, K, V, fwd_piece(M, K, V, STAGED), dtype) ? STAGED : MEMORY;
 }
 Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   Fwd f;
@@ -210,7 +215,7 @@ Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   size_t g = 0;
   for (int64_t n : {f.piece, V % f.piece}) {
     if (!n || way != MEMORY) continue;
-    const size_t b = ce_logits_part_bytes(M, n, K, dtype);
+    const size_t b = ce_logits_part_bytes(M, K, n, dtype);
     g = b > g ? b : g;
   }
   f.total = f.gemm + up256(g);
@@ -236,7 +241,7 @@ bool bwd_lines(int64_t M, int64_t K, int64_t V, int dtype) {
 Way bwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
   const int64_t p = bwd_piece(M, K, V);
   if (on_lines && bwd_lines(M, K, V, dtype) && ce_tiles(M, K, p)) return TILES;
-  return ce_staged(M, K, p, dtype) ? STAGED : MEMORY;
+  return staged(M, K, V, p, dtype) ? STAGED : MEMORY;
 }
 Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   const size_t es = dtype == MOE_F32 ? 4 : 2;
@@ -249,7 +254,7 @@ Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   size_t g = 0;
   for (int64_t n : {w.piece, V % w.piece}) {
     if (!n) continue;
-    for (size_t b : {way == MEMORY ? ce_logits_part_bytes(M, n, K, dtype) : 0, ce_part_bytes(M, K, n, dtype), ce_part_bytes(n, K, M, dtype)})
+    for (size_t b : {way == MEMORY ? ce_logits_part_bytes(M, K, n, dtype) : 0, ce_part_bytes(M, K, n, dtype)})
       g = b > g ? b : g;
   }
   w.total = w.gemm + up256(g);
@@ -300,8 +305,7 @@ hipError_t launch_linear_ce_fwd(const void *x, const void *W, const void *target
         a.part0 += (n + 2 * f.columns - 1) / (2 * f.columns) * 2;
         continue;
       }
-      e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32,
-                            (char *)ws + f.gemm, st);
+      e = launch_ce_logits(x, w, logits, (int)M, (int)K, n, dtype, (char *)ws + f.gemm, st);
       if (e != hipSuccess) break;
       const int chunks = (n + CHUNK - 1) / CHUNK;
       stats_kernel<<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, M, n, chunks);
@@ -350,7 +354,7 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
     } else if (way == STAGED) {
       e = launch_ce_staged(x, w, dl, a, (int)M, (int)K, n, (int)b.piece, dtype, st);
     } else {
-      e = launch_linear_fwd(x, w, nullptr, nullptr, logits, nullptr, (int)M, (int)K, n, MOE_ACT_NONE, dtype, MOE_F32, part, st);
+      e = launch_ce_logits(x, w, logits, (int)M, (int)K, n, dtype, part, st);
       if (e != hipSuccess) break;
       const int chunks = (n + CHUNK - 1) / CHUNK;
       if (dtype == MOE_F32) dl_kernel<float><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);

@@ -65,9 +65,10 @@ bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype);
 int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype);
 hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
                             hipStream_t st);
-// workspaces of dX and dW, and of logits that launch_linear_fwd leaves in memory
-size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype);
-size_t ce_logits_part_bytes(int64_t M, int64_t V, int64_t K, int dtype);
+// workspaces of dX and dW, and of logits that are left in memory; these
+size_t ce_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
+size_t ce_logits_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
+hipError_t launch_ce_logits(const void *x, const void *W, float *logits, int M, int K, int V, int dtype, void *part, hipStream_t st);
 // out = dl W + sum (sum NULL: 0; fp32, may be out)
 hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
                         int V, int dtype, void *part, hipStream_t st);

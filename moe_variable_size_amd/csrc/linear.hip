@@ -30,7 +30,6 @@ struct GemmArgs {
   int M, N, K;
   int64_t lda, ldb;  // K-major: elements between rows; MN-major: between reduction rows
   bool vec;          // N a multiple of 8; out, z, residual and bias on 16-byte lines
-  Plan plan;         // of the staged tiles; shape 0: staged_plan's
 };
 
 // buffer resource from wave-uniform values, in scalar registers
@@ -114,8 +113,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
 // The cross entropy's epilogues (cross_entropy.hip), in the place of an activation: logits l = x W^T stay in the
 // accumulators.  The forward leaves the largest value and the sum of exponentials of a row's columns in a tile (or a wave
 // of it), and the target's logit; the backward leaves dl.  The products bound both: 8192 x 4096 x 65536 in bf16 takes 3.08
-// ms with the statistics (1.43 PFLOP/s) and 3.32 with the gradient (1.32), its bf16 stores among them; 777 x 1001 x 5003 in
-// fp32 111 and 106 us in the staged tiles, 109 for the plain product with its stores.
+// ms with the statistics (1.43 PFLOP/s) and 3.32 with the gradient (1.32), its bf16 stores among them.
 constexpr int kCeStats = 16, kCeGrad = 17;
 
 // ---- staged tiles: any alignment and size ------------------------------------
@@ -224,6 +222,72 @@ MOE_DEV float over_half(float v, F &&f) {
   return f(v, __shfl_xor(v, 16, 64));
 }
 
+// What becomes of a tile's sums: a wave's S x S blocks at row m0 + wm, column n0 + wn
+template <typename T, typename To, int S, int ACT>
+MOE_DEV void staged_out(const GemmArgs &p, int splits, int split, float *part, const CeArgs &ce, f32x16 (&acc)[S][S], int m0, int n0,
+                        int wm, int wn) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (ACT == kCeStats) {
+    const int n = n0 + wn + (lane & 31);
+    float2 *out = ce.part + (int64_t)(ce.part0 + (n0 + wn) / (32 * S)) * p.M;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = m0 + wm + i * 32 + acc_row(e, lane), t = m < p.M ? ce_target(ce, m) : -1;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          if (t >= 0 && t == n + j * 32 && t < p.N) ce.target_logit[m] = acc[i][j][e];
+          if (n + j * 32 >= p.N) acc[i][j][e] = -INFINITY;
+          top = fmaxf(top, acc[i][j][e]);
+        }
+        top = over_half(top, [](float a, float b) __attribute__((always_inline)) { return fmaxf(a, b); });
+        const float base = ce_base(top);
+#pragma unroll
+        for (int j = 0; j < S; ++j) sum += ce_exp<T>(acc[i][j][e] - base);
+        sum = over_half(sum, [](float a, float b) __attribute__((always_inline)) { return a + b; });
+        if ((lane & 31) == 0 && m < p.M) out[m] = float2{top, sum};
+      }
+    return;
+  }
+  if constexpr (ACT == kCeGrad) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = m0 + wm + i * 32 + acc_row(e, lane);
+        if (m >= p.M) continue;
+        const CeRow row = ce.rows[m];
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const int n = n0 + wn + j * 32 + (lane & 31);
+          if (n < ce.ld) stf((To *)p.out + (int64_t)m * ce.ld + n, n < p.N ? ce_dl<T>(row, acc[i][j][e], ce.col0 + n) : 0.f);
+        }
+      }
+    return;
+  }
+  if (splits > 1) part += (int64_t)split * p.M * p.N;
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const int n = n0 + wn + j * 32 + (lane & 31);
+    if (n >= p.N) continue;
+    const float b = p.bias ? ldf((const T *)p.bias + n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = m0 + wm + i * 32 + acc_row(e, lane);
+        if (m >= p.M) continue;
+        const int64_t at = (int64_t)m * p.N + n;
+        if (splits > 1)
+          part[at] = acc[i][j][e];
+        else
+          finish1<T, To, ACT>(p, acc[i][j][e] + b, at);
+      }
+  }
+}
+
 // splits > 1: range blockIdx / tiles of the reduction, fp32 products to part [splits][M][N]
 template <typename T, typename To, int S, int E, bool AK, bool BKM, int ACT>
 __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float *part, CeArgs ce) {
@@ -291,65 +355,7 @@ __global__ __launch_bounds__(SNT) void staged_gemm(GemmArgs p, int splits, float
       }
     }
   }
-  if constexpr (ACT == kCeStats) {
-    const int n = n0 + wn + (lane & 31);
-    float2 *out = ce.part + (int64_t)(ce.part0 + (n0 + wn) / (32 * S)) * p.M;
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int m = m0 + wm + i * 32 + acc_row(e, lane), t = m < p.M ? ce_target(ce, m) : -1;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          if (t >= 0 && t == n + j * 32 && t < p.N) ce.target_logit[m] = acc[i][j][e];
-          if (n + j * 32 >= p.N) acc[i][j][e] = -INFINITY;
-          top = fmaxf(top, acc[i][j][e]);
-        }
-        top = over_half(top, [](float a, float b) __attribute__((always_inline)) { return fmaxf(a, b); });
-        const float base = ce_base(top);
-#pragma unroll
-        for (int j = 0; j < S; ++j) sum += ce_exp<T>(acc[i][j][e] - base);
-        sum = over_half(sum, [](float a, float b) __attribute__((always_inline)) { return a + b; });
-        if ((lane & 31) == 0 && m < p.M) out[m] = float2{top, sum};
-      }
-    return;
-  }
-  if constexpr (ACT == kCeGrad) {
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int m = m0 + wm + i * 32 + acc_row(e, lane);
-        if (m >= p.M) continue;
-        const CeRow row = ce.rows[m];
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          const int n = n0 + wn + j * 32 + (lane & 31);
-          if (n < ce.ld) stf((To *)p.out + (int64_t)m * ce.ld + n, n < p.N ? ce_dl<T>(row, acc[i][j][e], ce.col0 + n) : 0.f);
-        }
-      }
-    return;
-  }
-  if (splits > 1) part += (int64_t)split * p.M * p.N;
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    const int n = n0 + wn + j * 32 + (lane & 31);
-    if (n >= p.N) continue;
-    const float b = p.bias ? ldf((const T *)p.bias + n) : 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int m = m0 + wm + i * 32 + acc_row(e, lane);
-        if (m >= p.M) continue;
-        const int64_t at = (int64_t)m * p.N + n;
-        if (splits > 1)
-          part[at] = acc[i][j][e];
-        else
-          finish1<T, To, ACT>(p, acc[i][j][e] + b, at);
-      }
-  }
+  staged_out<T, To, S, ACT>(p, splits, split, part, ce, acc, m0, n0, wm, wn);
 }
 
 // ---- pipelined tiles: bf16 rows on 16-byte lines -------------------------------
@@ -461,6 +467,184 @@ MOE_DEV void tile_of(int b, int total, int tm, int tn, int &mb, int &nb) {
   const int u = t - g * band;
   mb = 8 * g + u % rows;
   nb = u / rows;
+}
+
+// ---- fp32 in three parts of bf16 -----------------------------------------------------
+// The cross entropy's fp32 products.  With a1 = bf16(a), a2 = bf16(a - a1) and a3 = a - a1 - a2, all exact (3 x 8 bits),
+//     a b = a1 b1 + (a1 b2 + a2 b1) + (a1 b3 + a2 b2 + a3 b1) + what is left out,
+// a2 b3 + a3 b2 + a3 b3, at most 2^-23 |a b| (|a2| <= 2^-8 |a|, |a3| <= 2^-16 |a|): two half steps of fp32.  Six products of
+// bf16 take 3 / 8 of the matrix cores' time for one of fp32, and add up in fp32 in K / 16 steps each instead of K / 2.
+// (What is not finite, or above 3.39e38, makes its row's or column's sums NaN.)  4096^3: 680 us (1.21 PFLOP/s of bf16, the
+// clock at 1.9 GHz for the power it takes); by fp32 instructions 1000, at 90 % of what they can do.
+//
+//
+// Tiles of 64 S x 64 S per 4 waves, steps of 16 reduction elements.  The parts are made once per element, on the way from
+// registers to LDS, which holds them in three planes [row][reduction], or [reduction][row] where memory has it so, for
+// transposing reads.  While a step is multiplied, the next one is split into the other half of LDS and the one after is
+// loaded, so there is one barrier per step and a load has a whole step's time.
+//
+// Loads are runs of four at any alignment, none behind a branch.  A run that would end past its row is taken as the row's
+// last four elements instead and moved into place before the step that splits it.  (Rows have at least four.)
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+MOE_DEV uint32_t pack2(float a, float b) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b}); }
+
+constexpr int BK = 16;
+template <int S, bool KMAJ>
+struct Fine {
+  static constexpr int RUNS = S;  // of a thread
+  static constexpr int PER = (KMAJ ? BK : 64 * S) / 4;
+  static constexpr int PITCH = KMAJ ? BK + 8 : 64 * S + 32;
+  static constexpr int PLANE = PITCH * (KMAJ ? 64 * S : BK);
+  MOE_DEV static int at(int r, int k) { return KMAJ ? r * PITCH + k : k * PITCH + r; }
+
+  const float *p;   // the operand; K-major: from the tile's first row on
+  int64_t ld;
+  int rows, ke;     // K-major: rows from there; MN-major: all of them
+  uint32_t off[RUNS];
+  int first, shift;  // first row (reduction element) of the lane's runs; how far those past the end are moved
+  bool over;
+
+  MOE_DEV void setup(const void *op, int64_t l, int r0, int total, int end) {
+    ld = l;
+    ke = end;
+    first = threadIdx.x % PER * 4;
+    const int o = threadIdx.x / PER;
+    if constexpr (KMAJ) {
+      p = (const float *)op + r0 * l;
+      rows = min(total - r0, 64 * S);
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) {
+        const int r = o + i * (SNT / PER);
+        off[i] = r < rows ? ((uint32_t)r * (uint32_t)ld + first) * 4 : kOobOffset;
+      }
+      shift = 0;
+    } else {
+      p = (const float *)op;
+      rows = total;
+      const int left = total - r0;
+      shift = left < 64 * S ? -left & 3 : 0;
+      over = first < left && first + 4 > left;
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) {
+        const int k = o + i * (SNT / PER);
+        off[i] = first < left ? ((uint32_t)k * (uint32_t)ld + r0 + first - (over ? shift : 0)) * 4 : kOobOffset;
+      }
+    }
+  }
+  // elements k0 .. k0 + BK - 1 (zeros from ke on)
+  MOE_DEV void load(int k0, float (&v)[4 * RUNS]) {
+    const int left = ke - k0;
+    if constexpr (KMAJ) {
+      const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(p, ((uint32_t)(rows - 1) * (uint32_t)ld + ke) * 4);
+      const uint32_t at = (uint32_t)(first + 4 > left ? k0 - (-left & 3) : k0) * 4;
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) buf_load<float, 4>(rs, first < left ? off[i] + at : kOobOffset, v + 4 * i);
+    } else {
+      const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(p + k0 * ld, left > 0 ? ((uint32_t)(min(left, BK) - 1) * (uint32_t)ld + rows) * 4 : 0u);
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) buf_load<float, 4>(rs, off[i], v + 4 * i);
+    }
+  }
+  // runs that were taken from before their place (as loaded for k0)
+  MOE_DEV void settle(int k0, float (&v)[4 * RUNS]) {
+    const int left = ke - k0, n = KMAJ ? (left < BK ? -left & 3 : 0) : shift;
+    const bool mine = KMAJ ? first < left && first + 4 > left : over;
+    for (int t = 0; t < n; ++t)
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * i + j] = !mine ? v[4 * i + j] : j < 3 ? v[4 * i + j + 1] : 0.f;
+  }
+  MOE_DEV void store(bf16_t *lds, const float (&v)[4 * RUNS]) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+      const int o = threadIdx.x / PER + i * (SNT / PER);
+      float a[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        const u32x2 w = {pack2(a[0], a[1]), pack2(a[2], a[3])};
+        *(u32x2 *)&lds[t * PLANE + (KMAJ ? at(o, first) : at(first, o))] = w;
+        if (t == 2) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] -= __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      }
+    }
+  }
+  // 32 rows at r0 of the step: lane l holds row l & 31, elements 8 (l >> 5) .. +7
+  MOE_DEV static bf16x8_t frag(const bf16_t *plane, int r0) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KMAJ) {
+      return *(const bf16x8_t *)&plane[at(r0 + (lane & 31), 8 * (lane >> 5))];
+    } else {  // (as frag of the pipelined tiles, 16 columns per 16 lanes)
+      const int j = lane & 15, k = 8 * (lane >> 5) + (j >> 2), col = r0 + (lane & 16) + 4 * (j & 3);
+      LDS_AS i16x4 *p0 = (LDS_AS i16x4 *)(LDS_AS char *)(char *)&plane[at(col, k)];
+      LDS_AS i16x4 *p1 = (LDS_AS i16x4 *)((LDS_AS char *)p0 + 8 * PITCH);
+      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p0);
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p1);
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+template <int S, bool AK, bool BKM, int ACT>
+__global__ __launch_bounds__(SNT, 2) void fine_gemm(GemmArgs p, int splits, float *part, CeArgs ce) {
+  using FA = Fine<S, AK>;
+  using FB = Fine<S, BKM>;
+  __shared__ __align__(16) bf16_t As[2][3 * FA::PLANE], Bs[2][3 * FB::PLANE];
+  const int wid = threadIdx.x >> 6, wm = (wid >> 1) * 32 * S, wn = (wid & 1) * 32 * S;
+  const int tm = (p.M + 64 * S - 1) / (64 * S), tn = (p.N + 64 * S - 1) / (64 * S), split = blockIdx.x / (tm * tn);
+  int mb, nb;
+  tile_of(blockIdx.x - split * (tm * tn), tm * tn, tm, tn, mb, nb);
+  const int m0 = mb * 64 * S, n0 = nb * 64 * S;
+  const int steps = (p.K + BK - 1) / BK;
+  const int ub = (int)((int64_t)steps * split / splits), ue = (int)((int64_t)steps * (split + 1) / splits);
+  FA fa;
+  FB fb;
+  fa.setup(p.A, p.lda, m0, p.M, min(p.K, ue * BK));
+  fb.setup(p.B, p.ldb, n0, p.N, min(p.K, ue * BK));
+  f32x16 acc[S][S] = {};
+  float va[2][4 * FA::RUNS], vb[2][4 * FB::RUNS];
+  // step u out of half H, the next one into the other
+  auto step = [&](int u, auto half) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value;
+    fa.load((u + 2) * BK, va[H]);
+    fb.load((u + 2) * BK, vb[H]);
+    fa.settle((u + 1) * BK, va[1 - H]);
+    fb.settle((u + 1) * BK, vb[1 - H]);
+    bf16x8_t a[S][3], b[S][3];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        a[i][t] = FA::frag(As[H] + t * FA::PLANE, wm + i * 32);
+        b[i][t] = FB::frag(Bs[H] + t * FB::PLANE, wn + i * 32);
+      }
+#pragma unroll
+    for (int sum = 2; sum >= 0; --sum)  // (small ones first)
+#pragma unroll
+      for (int t = 0; t <= sum; ++t)
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i][t], b[j][sum - t], acc[i][j], 0, 0, 0);
+    fa.store(As[1 - H], va[1 - H]);
+    fb.store(Bs[1 - H], vb[1 - H]);
+    __syncthreads();
+  };
+  fa.load(ub * BK, va[0]);
+  fb.load(ub * BK, vb[0]);
+  fa.load((ub + 1) * BK, va[1]);
+  fb.load((ub + 1) * BK, vb[1]);
+  fa.settle(ub * BK, va[0]);
+  fb.settle(ub * BK, vb[0]);
+  fa.store(As[0], va[0]);
+  fb.store(Bs[0], vb[0]);
+  __syncthreads();
+  for (int u = ub; u < ue; u += 2) {
+    step(u, std::integral_constant<int, 0>());
+    if (u + 1 < ue) step(u + 1, std::integral_constant<int, 1>());
+  }
+  staged_out<float, float, S, ACT>(p, splits, split, part, ce, acc, m0, n0, wm, wn);
 }
 
 struct PipeArgs {
@@ -1200,7 +1384,7 @@ hipError_t run_staged(const GemmArgs &a, const Plan &pl, int act, void *part, co
     if (fours) staged_gemm<T, To, 1, 4, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
     else staged_gemm<T, To, 1, 1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, out, ce);
   };
-  if constexpr (AK && BKM && sizeof(T) == sizeof(To)) {
+  if constexpr (AK && BKM && sizeof(T) == 2 && sizeof(To) == 2) {
     if (act >= kCeStats) {
       if (act == kCeStats) run(std::integral_constant<int, kCeStats>());
       else run(std::integral_constant<int, kCeGrad>());
@@ -1263,7 +1447,7 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
       return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
     }
   }
-  const Plan pl = a.plan.shape ? a.plan : staged_plan(a.M, a.N, a.K, sizeof(T) == 2);
+  const Plan pl = staged_plan(a.M, a.N, a.K, sizeof(T) == 2);
   const hipError_t e = run_staged<AK, BKM, T, To>(a, pl, act, part, CeArgs{}, st);
   if (e != hipSuccess || pl.splits == 1) return e;
   return join<AK && BKM, T, To>(a, act, part, pl.splits, st);
@@ -1344,38 +1528,73 @@ hipError_t launch_ce_tiles(const void *x, const void *W, void *dl, const CeArgs 
   const int shape = unsplit_shape(M, shape_v, K);
   return dl ? run_piped<true, true, bf16_t>(q, shape, kCeGrad, st) : run_piped<true, true, float>(q, shape, kCeStats, st);
 }
-bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype) {
-  return M > 16 && V > 16 && launch_rows(M, V) >= M && staged_plan(M, V, K, dtype == MOE_BF16).splits == 1;
+// fp32 (reduction and rows of at least four): what a product's epilogue or its ranges' sums take
+template <bool AK, bool BKM, int ACT>
+static void launch_fine(const GemmArgs &a, const Plan &pl, void *part, const CeArgs &ce, hipStream_t st) {
+  const int ts = 64 * pl.shape, grid = ((a.M + ts - 1) / ts) * ((a.N + ts - 1) / ts) * pl.splits;
+  if (pl.shape == 2) fine_gemm<2, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part, ce);
+  else fine_gemm<1, AK, BKM, ACT><<<grid, SNT, 0, st>>>(a, pl.splits, (float *)part, ce);
 }
-int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype) { return 32 * staged_plan(M, V, K, dtype == MOE_BF16).shape; }
-hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
-                            hipStream_t st) {
-  GemmArgs a{x, W, nullptr, nullptr, dl, nullptr, M, V, K, K, K, false};
-  const Plan pl{staged_plan(M, shape_v, K, dtype == MOE_BF16).shape, 1};
-  const int act = dl ? kCeGrad : kCeStats;
-  if (dtype == MOE_F32) return run_staged<true, true, float, float>(a, pl, act, nullptr, ce, st);
-  return run_staged<true, true, bf16_t, bf16_t>(a, pl, act, nullptr, ce, st);
+template <bool AK, bool BKM>
+static hipError_t fine(const GemmArgs &a, void *part, hipStream_t st) {
+  const Plan pl = fine_plan(a.M, a.N, a.K, true);
+  launch_fine<AK, BKM, MOE_ACT_NONE>(a, pl, part, CeArgs{}, st);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || pl.splits == 1 ? e : join<AK && BKM, float, float>(a, MOE_ACT_NONE, part, pl.splits, st);
 }
-// The plan of dX and dW: staged fp32 tiles by rounds over the chip
-static Plan ce_plan(int64_t M, int64_t N, int64_t K, int dtype) {
-  return dtype == MOE_F32 ? Plan{1, rounds_splits(M, N, K)} : Plan{0, 1};
-}
-size_t ce_part_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
-  if (dtype == MOE_BF16) return part_bytes(M, N, K, true);
-  const int k = rounds_splits(M, N, K);
+static size_t fine_bytes(int64_t M, int64_t N, int64_t K) {
+  const int k = fine_plan(M, N, K, true).splits;
   return k > 1 ? (size_t)k * M * N * 4 : 0;
 }
-size_t ce_logits_part_bytes(int64_t M, int64_t V, int64_t K, int dtype) { return part_bytes(M, V, K, dtype == MOE_BF16); }
+bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype) {
+  if (M <= 16 || V <= 16 || launch_rows(M, V) < M) return false;
+  return dtype == MOE_F32 ? K >= 4 && fine_whole(M, V, K) : staged_plan(M, V, K, true).splits == 1;
+}
+int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype) {
+  return 32 * (dtype == MOE_F32 ? fine_plan(M, V, K, false) : staged_plan(M, V, K, true)).shape;
+}
+hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
+                            hipStream_t st) {
+  const GemmArgs a{x, W, nullptr, nullptr, dl, nullptr, M, V, K, K, K, false};
+  if (dtype == MOE_F32) {
+    const Plan pl = fine_plan(M, shape_v, K, false);
+    if (dl) launch_fine<true, true, kCeGrad>(a, pl, nullptr, ce, st);
+    else launch_fine<true, true, kCeStats>(a, pl, nullptr, ce, st);
+    return hipGetLastError();
+  }
+  const Plan pl{staged_plan(M, shape_v, K, true).shape, 1};
+  return run_staged<true, true, bf16_t, bf16_t>(a, pl, dl ? kCeGrad : kCeStats, nullptr, ce, st);
+}
+// Whether an fp32 product of these sizes takes the parts (few rows of x: streamed instead)
+static bool takes_parts(int64_t M, int64_t K, int64_t V, int dtype) { return dtype == MOE_F32 && K >= 4 && V >= 4 && M > 0; }
+size_t ce_part_bytes(int64_t M, int64_t K, int64_t V, int dtype) {
+  size_t most = 0;
+  for (size_t b : {part_bytes(M, K, V, dtype == MOE_BF16), part_bytes(V, K, M, dtype == MOE_BF16),
+                   takes_parts(M, K, V, dtype) ? fine_bytes(M, K, V) : 0, takes_parts(M, K, V, dtype) ? fine_bytes(V, K, M) : 0})
+    most = b > most ? b : most;
+  return most;
+}
+size_t ce_logits_part_bytes(int64_t M, int64_t K, int64_t V, int dtype) {
+  const size_t a = part_bytes(M, V, K, dtype == MOE_BF16), b = M > 16 && takes_parts(M, K, V, dtype) ? fine_bytes(M, V, K) : 0;
+  return a > b ? a : b;
+}
+hipError_t launch_ce_logits(const void *x, const void *W, float *logits, int M, int K, int V, int dtype, void *part, hipStream_t st) {
+  if (M > 16 && takes_parts(M, K, V, dtype))
+    return fine<true, true>(GemmArgs{x, W, nullptr, nullptr, logits, nullptr, M, V, K, K, K, false}, part, st);
+  return launch_linear_fwd(x, W, nullptr, nullptr, logits, nullptr, M, K, V, MOE_ACT_NONE, dtype, MOE_F32, part, st);
+}
 hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
                         int V, int dtype, void *part, hipStream_t st) {
-  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false, ce_plan(M, K, V, dtype)};
+  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false};
+  if (takes_parts(M, K, V, dtype)) return fine<true, false>(a, part, st);
   if (dtype == MOE_F32) return gemm<true, false, float, float>(a, MOE_ACT_NONE, part, st);
   if (out_f32) return gemm<true, false, bf16_t, float>(a, MOE_ACT_NONE, part, st);
   return gemm<true, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
 }
 hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, void *dW, int M, int K, int V, int dtype, void *part,
                         hipStream_t st) {
-  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false, ce_plan(V, K, M, dtype)};
+  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false};
+  if (takes_parts(M, K, V, dtype)) return fine<false, false>(a, part, st);
   if (dtype == MOE_F32) return gemm<false, false, float, float>(a, MOE_ACT_NONE, part, st);
   return gemm<false, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
 }

@@ -79,23 +79,40 @@ inline Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   if (k > 16) k = 16;
   return Plan{1, (int)(k < 1 ? 1 : k)};
 }
-// Reduction ranges of a product in fp32 staged tiles of a cross entropy's gradient: the same limits, chosen by rounds of
-// workgroups over the 256 CUs (0.63 us per step of each that shares a CU, 0.85 alone) and what the join costs, as plan_of.
-// dX of 777 x 5003 x 1001 (208 tiles) in 1 range 133 us, in 4, as above, 102, in 6 90 (and 6 for the join).
-inline int rounds_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t t1 = ((M + 63) / 64) * ((N + 63) / 64), steps = (K + SBK - 1) / SBK;
-  int best = 1;
+// The cross entropy's fp32 products in three parts of bf16 (shape: S, tiles of 64 S x 64 S; a range's reduction in steps of
+// 16), by the same kind of estimate: a step of a CU's c workgroups takes 0.28 c us for S = 1 (0.47 at least) and 0.67 c for S = 2 (0.79),
+// and a tile's ends as much as 3 and 9 steps.  Measured, us, without the join (the rule's in brackets): 1074 x 47121 x 600
+// S = 1 494, [2 413]; 777 x 5003 x 1001 1 100, [2 91]; 132 x 37693 x 6408 [1 707], 2 730; 64 x 32000 x 4096 [1 168], 2 220;
+// reductions in ranges, 777 x 1001 x 5003 1 in 4 79, 2 in 4 [71], 2 in 8 60; 1074 x 600 x 47121 1 in 6 503, 2 in 4 516, 2 in 8 [432].
+inline Plan fine_plan(int64_t M, int64_t N, int64_t K, bool split, double *us = nullptr) {
+  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int64_t steps = (K + 15) / 16;
+  Plan best{1, 1};
   double least = 0;
-  for (int k = 1; k <= 16 && (k == 1 || (steps >= 4 * k && t1 * k <= 2560)); ++k) {
-    const double each = __builtin_ceil(t1 * k / 256.0) * 0.63;
-    double t = (each > 0.85 ? each : 0.85) * __builtin_ceil((double)steps / k);
-    if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
-    if (k == 1 || t < least) {
-      least = t;
-      best = k;
+  for (int S = 1; S <= 2; ++S) {
+    const double tiles = (double)((M + 64 * S - 1) / (64 * S)) * ((N + 64 * S - 1) / (64 * S));
+    for (int k : kSplits) {
+      if (k > 1 && (!split || steps < 4 * k || tiles * k > 1280 / S)) break;
+      const double c = __builtin_ceil(tiles * k / 256), alone = S == 1 ? 0.47 : 0.79, each = S == 1 ? 0.28 : 0.67;
+      double t = 6 + ((steps + k - 1) / k + (S == 1 ? 3 : 9)) * (each * c > alone ? each * c : alone);
+      if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = Plan{S, k};
+      }
     }
   }
+  if (us) *us = least;
   return best;
+}
+// Whether the logits' product is better not split, so that it ends in the statistics or the gradient: a split one writes
+// logits that have to be read again.  344 x 2838 x 2632: 100 us whole, in ranges 43 and 14 for the join and the logits; 777 x
+// 5003 x 1001: 91 whole, 74 and 35.
+inline bool fine_whole(int64_t M, int64_t V, int64_t K) {
+  double whole, split;
+  fine_plan(M, V, K, false, &whole);
+  fine_plan(M, V, K, true, &split);
+  return whole <= split + 5 + 8.0 * M * V / 4e6;
 }
 // Rows of one launch, at most M of them.  A dispatch holds fewer than 2^32 work-items: the streamed
 // products take 64 per row of x (at most 16 columns), the smallest tiles 256 per 64 x 64 outputs.  Both are

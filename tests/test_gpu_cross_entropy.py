@@ -359,3 +359,61 @@ def test_refusals_on_device_tensors():
             bad()
     with pytest.raises(_lib.MoeError):
         fwd(x, W, t, z_weight=float("nan"))
+
+
+@pytest.mark.parametrize("M,K,V", [
+    (17, 4, 33), (70, 5, 300), (65, 67, 130), (100, 130, 515), (40, 600, 333),  # small tiles; odd ends in every direction
+    (777, 101, 5003), (300, 258, 3070), (1027, 35, 8191),                      # 128 x 128 too
+    (33, 4100, 700), (200, 2633, 900),                                         # reductions in ranges, the logits' among them
+    (3, 100, 301), (5, 1030, 77), (19, 3, 50), (50, 2, 7), (40, 64, 3), (30, 9, 2),  # few rows; fewer than four of something
+])
+def test_fp32_of_any_value(M, K, V):
+    """Numbers of all 24 bits, rows of very different size.  Each product is off by two half steps at most, its sums by one
+    per addition (8 at the joins); what follows as above."""
+    gen = torch.Generator(device="cuda").manual_seed(M + V)
+    x = torch.randn((M, K), generator=gen, device="cuda") * 10 ** torch.linspace(-3, 0.5, M, device="cuda")[:, None]
+    W = torch.randn((V, K), generator=gen, device="cuda") * 10 ** torch.linspace(-3, 0, V, device="cuda")[:, None] / K ** 0.5
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    t[M // 2] = -1
+    g = torch.randn(M, generator=gen, device="cuda")
+    xd, Wd, z = x.double(), W.double(), 1e-3
+    l, size = xd @ Wd.t(), xd.abs() @ Wd.abs().t()
+    off = (K + 10) * H32 * size
+    lse = torch.logsumexp(l, 1)
+    p = torch.exp(l - lse[:, None])
+    # of an exponential: its argument's and its own; of the sum: its terms', one per addition
+    exps = (2 * (l - lse[:, None]).abs() + 4) * H32
+    lse_off = (p * (off + exps)).sum(1) + (90 + V / 32 + 3 * lse.abs()) * H32
+    got, got_lse = api.moe_linear_ce_fwd(x, W, t, z_weight=z)
+    assert ((got_lse.double() - lse).abs() <= lse_off).all()
+    ok = t >= 0
+    at = t.clamp(min=0)[:, None]
+    want = torch.where(ok, lse - l.gather(1, at)[:, 0] + z * lse ** 2, 0.0)
+    lim = lse_off * (1 + 2 * z * lse.abs()) + off.gather(1, at)[:, 0] + 4 * H32 * (lse.abs() + l.gather(1, at)[:, 0].abs() + z * lse ** 2)
+    assert ((got.double() - want).abs() <= lim).all() and float(got[M // 2]) == 0
+    gg = torch.where(ok, g.double(), 0.0)
+    f = gg * (1 + 2 * z * lse)
+    d = p * f[:, None]
+    d_off = d.abs() * (off + exps + lse_off[:, None]) + (p * gg[:, None]).abs() * (2 * z * lse_off)[:, None] + 6 * H32 * d.abs()
+    d.scatter_add_(1, at, -gg[:, None])
+    d_off += 2 * H32 * d.abs()
+    dX, dW = api.moe_linear_ce_bwd(g, x, W, t, got_lse, z_weight=z)
+    for a, b, e, s in ((dX, d @ Wd, d_off @ Wd.abs(), (V + 20) * (d.abs() @ Wd.abs())),
+                       (dW, d.t() @ xd, d_off.t() @ xd.abs(), (M + 20) * (d.abs().t() @ xd.abs()))):
+        assert ((a.double() - b).abs() <= 1.01 * e + H32 * s).all()
+
+
+def test_fp32_that_is_not_finite():
+    """An infinite or NaN value of x stays in its row, one of W in every row that is not left out."""
+    M, K, V = 70, 33, 300
+    x, W, t, g = make(M, K, V, F32, seed=31, ignore=0)
+    want, lse = api.moe_linear_ce_fwd(x, W, t)
+    x[7, 3], x[50, 32] = float("inf"), float("nan")
+    got, lse2 = api.moe_linear_ce_fwd(x, W, t)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[7] = bad[50] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+    dX, _ = api.moe_linear_ce_bwd(g, x, W, t, lse2)
+    assert torch.isnan(dX[bad]).all() and torch.isfinite(dX[~bad]).all()
+    W[299, 0] = -float("inf")
+    assert torch.isnan(api.moe_linear_ce_fwd(x, W, t)[0]).all()
