@@ -13,7 +13,7 @@
 // ones.  8 elements per thread make every access 16 or 32 bytes wide, and 32 lanes a block of 256, whose largest value needs no
 // LDS.  Tensors go by in one launch, their descriptors in its arguments (48 of them: 6.8 us for 12 small ones;
 // a table in memory would have to be copied there first).  277M elements, bf16: 1099 us with fp32 states (5.5 TB/s; a
-// large copy reaches 4.8), 560 with 8-bit ones (5.0).  Non-temporal loads and stores of the states: 1157 and 553.
+// large copy reaches 4.8), 602 with 8-bit ones (4.6).  Non-temporal loads and stores of the states: 1157 with fp32 ones.
 #include <math.h>
 
 #include "common.hpp"
@@ -149,7 +149,7 @@ MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&
                   const uint32_t (&h)[PER]) {
   const float top = block_top(a);
   const bool none = top < kLeast;
-  const float inv = none ? 0.f : 448.f / top;
+  const float inv = none ? 0.f : 1.f / top * 448.f;
   u32x2 c = {0, 0};
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -164,14 +164,33 @@ MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&
     for (int i = 0; i < PER; ++i)
       if (i < left) p[i] = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
   }
-  if ((threadIdx.x & 31) == 0 && left > 0) *scale = none ? 0.f : top < INFINITY ? top / 448.f : NAN;
+  if ((threadIdx.x & 31) == 0 && left > 0) *scale = none ? 0.f : top < INFINITY ? top * (1.f / 448.f) : NAN;
 }
 
-// The hardware's root, off by a step at most, with small arguments in its range: the exact one takes three times as many
-// instructions, which 8-bit states would wait for (so does the quotient below)
+// The hardware's root, off by a step at most, with small arguments in its range (the exact one takes three times as many
+// instructions)
 MOE_DEV float root_of(float v) {
   const bool small = v < 0x1p-96f;
   return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.f);
+}
+
+// States in 8 bits: every operation rounded once, in the formulas' order, none fused, and the root to nearest (the hardware's
+// reciprocal root and one correction by the remainder).  A sum or a root that is a step off turns a rounding of codes the other
+// way now and then, and in later steps, through a block's largest value, the scale of all of it; like this the states do
+// not depend on how the arithmetic is carried out.  (277M elements: 560 us fused and with the root above.)
+MOE_DEV float exact_root(float v) {
+  const bool small = v < 0x1p-96f;
+  const float x = small ? v * 0x1p64f : v, y = __builtin_amdgcn_rsqf(x), s = x * y, e = fmaf(-s, s, x);
+  const float root = fmaf(e, 0.5f * y, s) * (small ? 0x1p-32f : 1.f);
+  return e == e ? root : v;  // (of 0, infinity and NaN: they themselves)
+}
+MOE_DEV float mean_of(float b, float old, float a, float x) {
+#pragma clang fp contract(off)
+  return b * old + a * x;
+}
+MOE_DEV float square_of(float b, float old, float a, float x) {
+#pragma clang fp contract(off)
+  return b * old + a * x * x;
 }
 
 // elements at .. at + 7 of tensor t (FULL: the whole workgroup's are there, on 16-byte lines)
@@ -200,9 +219,15 @@ MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const float x = g[i] * s;
-    m[i] = fmaf(a.b1, m[i], a.a1 * x);
-    v[i] = fmaf(a.b2, v[i], a.a2 * x * x);
-    r[i] = root_of(v[i]);
+    if constexpr (BITS == 8) {
+      m[i] = mean_of(a.b1, m[i], a.a1, x);
+      v[i] = square_of(a.b2, v[i], a.a2, x);
+      r[i] = exact_root(v[i]);
+    } else {
+      m[i] = fmaf(a.b1, m[i], a.a1 * x);
+      v[i] = fmaf(a.b2, v[i], a.a2 * x * x);
+      r[i] = root_of(v[i]);
+    }
     w[i] = fmaf(w[i], keep, -(rate * m[i]) * __builtin_amdgcn_rcpf(fmaf(r[i], root, a.eps)));
   }
   put8((P *)t.p + at, FULL, left, w);

@@ -6,7 +6,10 @@
 // exp(l - largest) of their columns (linear.hip, ce_stats); the parts of a row are joined here.  Backward:
 // the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
 // logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
-// fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it.
+// fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it; of many rows the
+// roundings average out, but of few a row's largest entry, its target's, would move all of the row's dX and dW by up to 2^-8
+// of them, where their own rounding is 2^-8 / sqrt 3 in norm.  There (bf16, up to 128 rows) dl is two rows, its rounding and
+// the rest's, which these products, bound by the weights, take for little (1 x 256 x 505: 50 us for 46).
 // bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
@@ -66,8 +69,8 @@ __global__ __launch_bounds__(256) void stats_kernel(const float *__restrict__ l,
   }
 }
 
-// dl of a piece, zeros behind it up to its row length
-template <typename T>
+// dl of a piece, zeros behind it up to its row length; PARTS = 2: what its rounding leaves to rows M .. 2 M - 1
+template <typename T, int PARTS>
 __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, CeArgs a, T *__restrict__ dl, int64_t M,
                                                  int n, int chunks) {
   const int64_t total = M * chunks;
@@ -75,12 +78,15 @@ __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, Ce
     const int64_t m = b / chunks;
     const int c = (int)(b - m * chunks), hi = min(n, (c + 1) * CHUNK);
     const CeRow r = a.rows[m];
-    if (hi == n && threadIdx.x < a.ld - n) st(dl + m * a.ld + n + threadIdx.x, 0.f);
+    if (hi == n && threadIdx.x < a.ld - n)
+      for (int p = 0; p < PARTS; ++p) st(dl + (p * M + m) * a.ld + n + threadIdx.x, 0.f);
 #pragma unroll
     for (int i = 0; i < CHUNK / 256; ++i) {
       const int col = c * CHUNK + i * 256 + threadIdx.x;
       if (col >= hi) break;
-      st(dl + m * a.ld + col, ce_dl<T>(r, l[m * n + col], a.col0 + col));
+      const float d = ce_dl<T>(r, l[m * n + col], a.col0 + col);
+      st(dl + m * a.ld + col, d);
+      if constexpr (PARTS == 2) st(dl + (M + m) * a.ld + col, d - (float)(__bf16)d);
     }
   }
 }
@@ -155,6 +161,13 @@ __global__ __launch_bounds__(256) void rows_kernel(CeArgs a, int64_t M, const fl
   rows[m] = CeRow{v, g * (1.f + 2.f * z * v), g, (int)t};
 }
 
+// x twice, for the two parts of dl
+__global__ __launch_bounds__(256) void twice_kernel(const bf16_t *__restrict__ x, bf16_t *__restrict__ y, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) y[i] = y[n + i] = x[i];
+}
+__global__ __launch_bounds__(256) void add_kernel(const float *__restrict__ x, bf16_t *__restrict__ y, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) st(y + i, x[i] + x[n + i]);
+}
 __global__ __launch_bounds__(256) void round_kernel(const float *__restrict__ x, bf16_t *__restrict__ y, int64_t n, bool wide) {
   const int64_t step = (int64_t)gridDim.x * 1024;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += step) {
@@ -224,8 +237,10 @@ Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
 
 struct Bwd {
   int64_t piece;
-  size_t dl, sum, logits, gemm, total;  // offsets after the rows
+  size_t dl, x2, sum, logits, gemm, total;  // offsets after the rows
 };
+// Parts of dl
+int dl_parts(int64_t M, int dtype) { return dtype == MOE_BF16 && M <= 128 ? 2 : 1; }
 // 256 MB of dl in bf16
 int64_t bwd_piece(int64_t M, int64_t K, int64_t V) {
   const int64_t most = greatest(256, ((int64_t)1 << 27) / M / 256 * 256);
@@ -240,21 +255,24 @@ bool bwd_lines(int64_t M, int64_t K, int64_t V, int dtype) {
 }
 Way bwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
   const int64_t p = bwd_piece(M, K, V);
+  if (dl_parts(M, dtype) == 2) return MEMORY;
   if (on_lines && bwd_lines(M, K, V, dtype) && ce_tiles(M, K, p)) return TILES;
   return staged(M, K, V, p, dtype) ? STAGED : MEMORY;
 }
 Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   const size_t es = dtype == MOE_F32 ? 4 : 2;
+  const int parts = dl_parts(M, dtype);
   Bwd w;
   w.piece = bwd_piece(M, K, V);
   w.dl = up256((size_t)M * sizeof(CeRow));
-  w.sum = w.dl + up256((size_t)M * bwd_ld(w.piece) * es);
-  w.logits = w.sum + (w.piece < V && dtype == MOE_BF16 ? up256((size_t)M * K * 4) : 0);
+  w.x2 = w.dl + up256((size_t)parts * M * bwd_ld(w.piece) * es);
+  w.sum = w.x2 + (parts == 2 ? up256((size_t)2 * M * K * es) : 0);
+  w.logits = w.sum + (parts == 2 || (w.piece < V && dtype == MOE_BF16) ? up256((size_t)parts * M * K * 4) : 0);
   w.gemm = w.logits + (way == MEMORY ? up256((size_t)M * w.piece * 4) : 0);
   size_t g = 0;
   for (int64_t n : {w.piece, V % w.piece}) {
     if (!n) continue;
-    for (size_t b : {way == MEMORY ? ce_logits_part_bytes(M, K, n, dtype) : 0, ce_part_bytes(M, K, n, dtype)})
+    for (size_t b : {way == MEMORY ? ce_logits_part_bytes(M, K, n, dtype) : 0, ce_part_bytes(parts * M, K, n, dtype)})
       g = b > g ? b : g;
   }
   w.total = w.gemm + up256(g);
@@ -343,7 +361,14 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
   void *part = (char *)ws + b.gemm;
   rows_kernel<<<(int)((M + 255) / 256), 256, 0, st>>>(a, M, d_loss, lse, total, reduction, z, (CeRow *)ws);
   hipError_t e = hipGetLastError();
-  const bool once = b.piece >= V;
+  const int parts = dl_parts(M, dtype), rows = (int)M * parts;
+  const bool once = b.piece >= V && parts == 1;
+  const void *xs = x;
+  if (e == hipSuccess && dW && parts == 2) {
+    xs = (char *)ws + b.x2;
+    twice_kernel<<<(int)least((M * K + 255) / 256, 2048), 256, 0, st>>>((const bf16_t *)x, (bf16_t *)((char *)ws + b.x2), M * K);
+    e = hipGetLastError();
+  }
   for (int64_t v = 0; v < V && e == hipSuccess; v += b.piece) {
     const int n = (int)least(b.piece, V - v);
     const char *w = (const char *)W + (size_t)v * K * es;
@@ -357,18 +382,20 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
       e = launch_ce_logits(x, w, logits, (int)M, (int)K, n, dtype, part, st);
       if (e != hipSuccess) break;
       const int chunks = (n + CHUNK - 1) / CHUNK;
-      if (dtype == MOE_F32) dl_kernel<float><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);
-      else dl_kernel<bf16_t><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
+      if (dtype == MOE_F32) dl_kernel<float, 1><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);
+      else if (parts == 2) dl_kernel<bf16_t, 2><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
+      else dl_kernel<bf16_t, 1><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
       e = hipGetLastError();
     }
     if (e == hipSuccess && dW)
-      e = launch_ce_dw(dl, a.ld, x, (char *)dW + (size_t)v * K * es, (int)M, (int)K, n, dtype, part, st);
+      e = launch_ce_dw(dl, a.ld, xs, (char *)dW + (size_t)v * K * es, rows, (int)K, n, dtype, part, st);
     if (e == hipSuccess && dX)
-      e = launch_ce_dx(dl, a.ld, w, v ? sum : nullptr, once ? dX : sum, !once, (int)M, (int)K, n, dtype, part, st);
+      e = launch_ce_dx(dl, a.ld, w, v ? sum : nullptr, once ? dX : sum, !once, rows, (int)K, n, dtype, part, st);
   }
   if (e == hipSuccess && dX && !once && dtype == MOE_BF16) {
     const int64_t n = M * K;
-    round_kernel<<<(int)least((n + 1023) / 1024, 8192), 256, 0, st>>>(sum, (bf16_t *)dX, n, (uintptr_t)dX % 8 == 0);
+    if (parts == 2) add_kernel<<<(int)least((n + 255) / 256, 2048), 256, 0, st>>>(sum, (bf16_t *)dX, n);
+    else round_kernel<<<(int)least((n + 1023) / 1024, 8192), 256, 0, st>>>(sum, (bf16_t *)dX, n, (uintptr_t)dX % 8 == 0);
     e = hipGetLastError();
   }
   return e;

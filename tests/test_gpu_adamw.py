@@ -351,3 +351,35 @@ def test_refusals_on_device_tensors():
     with pytest.raises(_lib.MoeError):
         call(p, [t(8), t(5)], [t(8), t(5)], [t(8), t(5)], step=1, lr=float("nan"))
     call([], [], [], [], **ok)
+
+
+def test_states_in_8_bits_are_those_of_single_roundings():
+    """Codes and scales are, bit for bit, what fp32 operations give one by one, over steps that build on each other."""
+    f = np.float32
+    s = Set([70001, 256, 3], bits=8, seed=77)
+    b1, b2, one = f(0.9), f(0.99), f(1.0)
+    a1, a2 = f(1.0 - 0.9), f(1.0 - 0.99)
+    for t in range(1, 5):
+        want = []
+        for i, n in enumerate(s.sizes):
+            g = s.g[i].cpu().numpy().astype(f)
+            rep = lambda a: np.repeat(a.cpu().numpy(), 256)[:n]  # noqa: E731
+            m = O.e4m3(s.m[i].view(torch.uint8).cpu().numpy()).astype(f) * rep(s.ms[i])
+            r = O.e4m3(s.v[i].view(torch.uint8).cpu().numpy()).astype(f) * rep(s.vs[i])
+            m = b1 * m + a1 * g
+            r = np.sqrt(b2 * (r * r) + a2 * g * g)
+            u = O.dither(np.arange(n), i, 5, t)
+            for a, uu in ((m, u[0]), (r, u[1])):
+                b = np.zeros(-(-n // 256) * 256, f)
+                b[:n] = a
+                top = np.abs(b.reshape(-1, 256)).max(1)
+                inv = np.repeat(one / top * f(448.0), 256)[:n]
+                y = np.abs(a) * inv
+                assert y.dtype == f
+                d = 2.0 ** (np.maximum(np.frexp(y.astype(np.float64))[1] - 1, -6) - 3)
+                want.append((np.sign(a) * np.minimum(np.floor(y / d + uu) * d, 448.0), top * (one / f(448.0))))
+        api.moe_adamw_step(s.p, s.g, s.m, s.v, step=t, lr=1e-3, betas=(0.9, 0.99), m_scales=s.ms, v_scales=s.vs, seed=5)
+        for i in range(len(s.sizes)):
+            for (q, scale), (codes, scales) in zip(want[2 * i:2 * i + 2], ((s.m[i], s.ms[i]), (s.v[i], s.vs[i]))):
+                assert np.array_equal(scales.cpu().numpy(), scale)
+                assert np.array_equal(O.e4m3(codes.view(torch.uint8).cpu().numpy()), q)

@@ -417,3 +417,27 @@ def test_fp32_that_is_not_finite():
     assert torch.isnan(dX[bad]).all() and torch.isfinite(dX[~bad]).all()
     W[299, 0] = -float("inf")
     assert torch.isnan(api.moe_linear_ce_fwd(x, W, t)[0]).all()
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 1880, 708), (1, 64, 300), (2, 997, 1698), (5, 33, 4097), (16, 2072, 2183), (60, 136, 5000), (128, 256, 3001)])
+def test_few_rows_lose_nothing_in_dl(M, K, V):
+    """Gradients of few rows are off by their own rounding alone: half a step of each element, beside what lse, the exponentials
+    and the sums leave (dl's second part ends at 2^-16 of it, 2^8 half steps of fp32)."""
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+    x = torch.randn((M, K), generator=gen, device="cuda").to(BF)
+    W = (torch.randn((V, K), generator=gen, device="cuda") / K ** 0.5).to(BF)
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    g = torch.randn(M, generator=gen, device="cuda")
+    _, lse = api.moe_linear_ce_fwd(x, W, t)
+    got = api.moe_linear_ce_bwd(g, x, W, t, lse)
+    xd, Wd = x.double(), W.double()
+    d = torch.softmax(xd @ Wd.t(), 1) * g.double()[:, None]
+    # the logits' sums and lse (as off as they) in p, 4 half steps per unit of exponent
+    far = float((xd.abs() @ Wd.abs().t()).max())
+    spread = d.abs() * (2 * K * far + 200) * H32
+    d.scatter_add_(1, t[:, None], -g.double()[:, None])
+    for a, want, room, n in ((got[0], d @ Wd, (spread + 2 ** 8 * H32 * d.abs()) @ Wd.abs() + V * H32 * (d.abs() @ Wd.abs()), V),
+                             (got[1], d.t() @ xd, (spread + 2 ** 8 * H32 * d.abs()).t() @ xd.abs() + 2 * M * H32 * (d.abs().t() @ xd.abs()), M)):
+        assert ((a.double() - want).abs() <= H16 * want.abs() * 1.01 + 1.01 * room + 1e-37).all()
+        # a rounding is 2^-8 sqrt(1 / 3) in norm at most, of many evenly spread ones
+        assert float((a.double() - want).norm()) <= H16 * (1 / 3) ** 0.5 * float(want.norm()) + float(room.norm())
