@@ -604,7 +604,7 @@ int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t
  * for every row (_SUM) or d_loss[0] / total[1] (_MEAN):
  *   dl = g_m ((1 + 2 z_weight lse_m) exp(l - lse_m) - [v = t]), 0 in rows that do
  *   not count, rounded to `dtype` for the two products (twice, with what the
- *   rounding leaves, for at most 128 rows of bf16);
+ *   rounding leaves, for at most 512 rows of bf16);
  *   dX = dl W [M, K],  dW = dl^T x [V, K], in `dtype`: each OVERWRITTEN, or NULL to
  *   skip.  (0 times what is not finite is NaN: rows of x that do not count have to be
  *   finite for dW, too.)
@@ -612,7 +612,8 @@ int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t
  *   for _MEAN alone).  M may be 0 (dW is then zeros).
  *   workspace: moe_linear_ce_bwd_workspace_bytes(...) bytes, 256-byte aligned: dl
  *   of a piece of the vocabulary (256 MB, or 256 columns; twice that for at most
- *   128 rows of bf16, and logits in fp32), dX's sum in fp32, and the products'.
+ *   512 rows of bf16), for few rows its logits in fp32, dX's sum in fp32, and the
+ *   products'.
  */
 size_t moe_linear_ce_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype);
 int moe_linear_ce_bwd(const float *d_loss, int32_t reduction, const float *total, const void *x,

@@ -7,9 +7,9 @@
 // the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
 // logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
 // fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it; of many rows the
-// roundings average out, but of few a row's largest entry, its target's, would move all of the row's dX and dW by up to 2^-8
-// of them, where their own rounding is 2^-8 / sqrt 3 in norm.  There (bf16, up to 128 rows) dl is two rows, its rounding and
-// the rest's, which these products, bound by the weights, take for little (1 x 256 x 505: 50 us for 46).
+// roundings average out to one more like dX's and dW's own, but of few a row's largest entry, its target's, would move all of
+// the row's gradients by up to 2^-8 of them, where their own rounding is 2^-8 / sqrt 3 in norm at most.  There (bf16, up
+// to 512 rows: 3 deviations of their mean within a quarter of it) dl is two rows, its rounding and what that leaves.
 // bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
@@ -69,8 +69,8 @@ __global__ __launch_bounds__(256) void stats_kernel(const float *__restrict__ l,
   }
 }
 
-// dl of a piece, zeros behind it up to its row length; PARTS = 2: what its rounding leaves to rows M .. 2 M - 1
-template <typename T, int PARTS>
+// dl of a piece, zeros behind it up to its row length
+template <typename T>
 __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, CeArgs a, T *__restrict__ dl, int64_t M,
                                                  int n, int chunks) {
   const int64_t total = M * chunks;
@@ -78,15 +78,17 @@ __global__ __launch_bounds__(256) void dl_kernel(const float *__restrict__ l, Ce
     const int64_t m = b / chunks;
     const int c = (int)(b - m * chunks), hi = min(n, (c + 1) * CHUNK);
     const CeRow r = a.rows[m];
-    if (hi == n && threadIdx.x < a.ld - n)
-      for (int p = 0; p < PARTS; ++p) st(dl + (p * M + m) * a.ld + n + threadIdx.x, 0.f);
+    if (hi == n && threadIdx.x < a.ld - n) {
+      st(dl + m * a.ld + n + threadIdx.x, 0.f);
+      if (a.rest) st(a.rest + m * a.ld + n + threadIdx.x, 0.f);
+    }
 #pragma unroll
     for (int i = 0; i < CHUNK / 256; ++i) {
       const int col = c * CHUNK + i * 256 + threadIdx.x;
       if (col >= hi) break;
       const float d = ce_dl<T>(r, l[m * n + col], a.col0 + col);
       st(dl + m * a.ld + col, d);
-      if constexpr (PARTS == 2) st(dl + (M + m) * a.ld + col, d - (float)(__bf16)d);
+      if (a.rest) st(a.rest + m * a.ld + col, d - (float)(__bf16)d);
     }
   }
 }
@@ -240,7 +242,7 @@ struct Bwd {
   size_t dl, x2, sum, logits, gemm, total;  // offsets after the rows
 };
 // Parts of dl
-int dl_parts(int64_t M, int dtype) { return dtype == MOE_BF16 && M <= 128 ? 2 : 1; }
+int dl_parts(int64_t M, int dtype) { return dtype == MOE_BF16 && M <= 512 ? 2 : 1; }
 // 256 MB of dl in bf16
 int64_t bwd_piece(int64_t M, int64_t K, int64_t V) {
   const int64_t most = greatest(256, ((int64_t)1 << 27) / M / 256 * 256);
@@ -251,11 +253,11 @@ int64_t bwd_ld(int64_t piece) { return (piece + 7) / 8 * 8; }
 // look at no column past the end but those zeros (the loads of four elements of other tiles would pass the buffer's)
 bool bwd_lines(int64_t M, int64_t K, int64_t V, int dtype) {
   const int64_t p = bwd_ld(bwd_piece(M, K, V)), most = (int64_t)1 << 30;
+  M *= dl_parts(M, dtype);
   return dtype == MOE_BF16 && K % 8 == 0 && K <= (1 << 20) && p <= (1 << 20) && M * p < most && M * K < most && p * K < most;
 }
 Way bwd_way(int64_t M, int64_t K, int64_t V, int dtype, bool on_lines) {
   const int64_t p = bwd_piece(M, K, V);
-  if (dl_parts(M, dtype) == 2) return MEMORY;
   if (on_lines && bwd_lines(M, K, V, dtype) && ce_tiles(M, K, p)) return TILES;
   return staged(M, K, V, p, dtype) ? STAGED : MEMORY;
 }
@@ -374,6 +376,7 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
     const char *w = (const char *)W + (size_t)v * K * es;
     a.col0 = v;
     a.ld = lines ? bwd_ld(n) : n;
+    a.rest = parts == 2 ? (bf16_t *)dl + M * a.ld : nullptr;
     if (way == TILES) {
       e = launch_ce_tiles(x, w, dl, a, (int)M, (int)K, n, (int)b.piece, st);
     } else if (way == STAGED) {
@@ -382,9 +385,8 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
       e = launch_ce_logits(x, w, logits, (int)M, (int)K, n, dtype, part, st);
       if (e != hipSuccess) break;
       const int chunks = (n + CHUNK - 1) / CHUNK;
-      if (dtype == MOE_F32) dl_kernel<float, 1><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);
-      else if (parts == 2) dl_kernel<bf16_t, 2><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
-      else dl_kernel<bf16_t, 1><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
+      if (dtype == MOE_F32) dl_kernel<float><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (float *)dl, M, n, chunks);
+      else dl_kernel<bf16_t><<<chunk_grid(M, chunks), 256, 0, st>>>(logits, a, (bf16_t *)dl, M, n, chunks);
       e = hipGetLastError();
     }
     if (e == hipSuccess && dW)

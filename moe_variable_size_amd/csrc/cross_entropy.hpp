@@ -20,6 +20,7 @@ struct CeArgs {
   // backward
   const CeRow *rows;    // [M]
   int64_t ld;           // dl's row length
+  bf16_t *rest;         // what dl's rounding leaves (bf16; NULL: not kept)
   // both
   int64_t col0, V;      // first column of this piece of the vocabulary; the whole vocabulary
 };

@@ -262,7 +262,10 @@ MOE_DEV void staged_out(const GemmArgs &p, int splits, int split, float *part, c
 #pragma unroll
         for (int j = 0; j < S; ++j) {
           const int n = n0 + wn + j * 32 + (lane & 31);
-          if (n < ce.ld) stf((To *)p.out + (int64_t)m * ce.ld + n, n < p.N ? ce_dl<T>(row, acc[i][j][e], ce.col0 + n) : 0.f);
+          if (n >= ce.ld) continue;
+          const float d = n < p.N ? ce_dl<T>(row, acc[i][j][e], ce.col0 + n) : 0.f;
+          stf((To *)p.out + (int64_t)m * ce.ld + n, d);
+          if (sizeof(T) == 2 && ce.rest) stf(ce.rest + (int64_t)m * ce.ld + n, d - (float)(__bf16)d);
         }
       }
     return;
@@ -822,6 +825,12 @@ MOE_DEV void ce_grad(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2][HM][
           v[h][e] = col < p.N ? ce_dl<bf16_t>(row, v[h][e], q.ce.col0 + col) : 0.f;
         }
       put8((bf16_t *)p.out + (int64_t)m * q.ce.ld + n, v);
+      if (!q.ce.rest) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h][e] -= (float)(__bf16)v[h][e];
+      put8(q.ce.rest + (int64_t)m * q.ce.ld + n, v);
     }
   }
 }

@@ -419,7 +419,8 @@ def test_fp32_that_is_not_finite():
     assert torch.isnan(api.moe_linear_ce_fwd(x, W, t)[0]).all()
 
 
-@pytest.mark.parametrize("M,K,V", [(1, 1880, 708), (1, 64, 300), (2, 997, 1698), (5, 33, 4097), (16, 2072, 2183), (60, 136, 5000), (128, 256, 3001)])
+@pytest.mark.parametrize("M,K,V", [(1, 1880, 708), (1, 64, 300), (2, 997, 1698), (5, 33, 4097), (16, 2072, 2183), (60, 136, 5000), (128, 256, 3001),
+                                   (300, 264, 20011), (512, 64, 1000), (400, 65, 3001)])
 def test_few_rows_lose_nothing_in_dl(M, K, V):
     """Gradients of few rows are off by their own rounding alone: half a step of each element, beside what lse, the exponentials
     and the sums leave (dl's second part ends at 2^-16 of it, 2^8 half steps of fp32)."""
