@@ -80,10 +80,11 @@ inline Plan staged_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   return Plan{1, (int)(k < 1 ? 1 : k)};
 }
 // The cross entropy's fp32 products in three parts of bf16 (shape: S, tiles of 64 S x 64 S; a range's reduction in steps of
-// 16), by the same kind of estimate: a step of a CU's c workgroups takes 0.28 c us for S = 1 (0.47 at least) and 0.67 c for S = 2 (0.79),
-// and a tile's ends as much as 3 and 9 steps.  Measured, us, without the join (the rule's in brackets): 1074 x 47121 x 600
-// S = 1 494, [2 413]; 777 x 5003 x 1001 1 100, [2 91]; 132 x 37693 x 6408 [1 707], 2 730; 64 x 32000 x 4096 [1 168], 2 220;
-// reductions in ranges, 777 x 1001 x 5003 1 in 4 79, 2 in 4 [71], 2 in 8 60; 1074 x 600 x 47121 1 in 6 503, 2 in 4 516, 2 in 8 [432].
+// 16), by the same kind of estimate: a step of a CU's c workgroups takes 0.28 c us for S = 1 (0.47 at least), for S = 2, of
+// which a CU holds two, 0.79, 1.2 and then 0.67 c, and a tile's ends as much as 3 and 9 steps.  Measured, us, without the join
+// (the rule's in brackets): 1074 x 47121 x 600 S = 1 494, [2 413]; 777 x 5003 x 1001 1 100, [2 91]; 132 x 37693 x 6408 [1 707], 2
+// 730; 64 x 32000 x 4096 [1 168], 2 220; reductions in ranges, 777 x 1001 x 5003 1 in 4 79, 2 in 4 71, [2 in 8 60]; 1074 x 600 x
+// 47121 1 in 6 503, 2 in 4 516, [2 in 8 432].
 inline Plan fine_plan(int64_t M, int64_t N, int64_t K, bool split, double *us = nullptr) {
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t steps = (K + 15) / 16;
@@ -93,7 +94,7 @@ inline Plan fine_plan(int64_t M, int64_t N, int64_t K, bool split, double *us = 
     const double tiles = (double)((M + 64 * S - 1) / (64 * S)) * ((N + 64 * S - 1) / (64 * S));
     for (int k : kSplits) {
       if (k > 1 && (!split || steps < 4 * k || tiles * k > 1280 / S)) break;
-      const double c = __builtin_ceil(tiles * k / 256), alone = S == 1 ? 0.47 : 0.79, each = S == 1 ? 0.28 : 0.67;
+      const double c = __builtin_ceil(tiles * k / 256), alone = S == 1 ? 0.47 : 0.79, each = S == 1 ? 0.28 : c <= 2 ? 0.6 : 0.67;
       double t = 6 + ((steps + k - 1) / k + (S == 1 ? 3 : 9)) * (each * c > alone ? each * c : alone);
       if (k > 1) t += 4 + (2.0 * k + 1) * M * N * 4 / 4e6;
       if (least == 0 || t < least) {
