@@ -811,7 +811,7 @@ def moe_linear_w4_fwd(x: torch.Tensor, w: W4Weight, *, bias: Optional[torch.Tens
     """act(x W^T + bias) + residual for few rows of x [M, K] bfloat16 (K a multiple
     of 8) with 4-bit weights; bias [N] bfloat16, residual [M, N] in ``out_dtype``
     (bfloat16, the default, or float32), which may be ``out`` itself.  From some
-    hundred rows on ``moe_w4_dequantize`` and ``moe_linear_fwd`` are faster."""
+    256 rows on ``moe_w4_dequantize`` and ``moe_linear_fwd`` are faster."""
     lib = _lib.load()
     _need(x, "x", torch.bfloat16, 2, -1)
     c = _w4_struct(w, x.get_device(), False)
@@ -1364,6 +1364,8 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 def linear_cross_entropy(x, W, targets, *, z_weight=0.0, reduction="mean"):
     """Differentiable cross entropy of the logits x W^T (``moe_linear_ce_fwd``),
     which are not kept: float32 losses [M] ("none"), their sum or their mean over
-    the rows whose target is in [0, V).  Gradients reach x and W."""
+    the rows whose target is in [0, V).  Gradients reach x and W.  (Captured in a
+    graph, forward and backward go in together, with no eager result of the same
+    leaves still alive.)"""
     _option(MOE_REDUCTIONS, reduction, "reduction")
     return LinearCrossEntropyFunction.apply(x, W, targets, z_weight, reduction)
