@@ -16,6 +16,8 @@
 // large copy reaches 4.8), 602 with 8-bit ones (4.6).  Non-temporal loads and stores of the states: 1157 with fp32 ones.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -127,9 +129,16 @@ MOE_DEV float block_top(const float (&a)[PER]) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = __builtin_elementwise_maximum(top, fabsf(a[i]));
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, 64));
-  return top;
+  // neighbours, pairs, then halves and rows of 16 mirrored (once their members are alike); the last step through LDS's crossbar
+  auto join = [&](auto ctrl) __attribute__((always_inline)) {
+    const int other = __builtin_amdgcn_update_dpp(0, __float_as_int(top), decltype(ctrl)::value, 0xF, 0xF, false);
+    top = __builtin_elementwise_maximum(top, __int_as_float(other));
+  };
+  join(std::integral_constant<int, 0xB1>());   // quad_perm 1 0 3 2
+  join(std::integral_constant<int, 0x4E>());   // quad_perm 2 3 0 1
+  join(std::integral_constant<int, 0x141>());  // row_half_mirror
+  join(std::integral_constant<int, 0x140>());  // row_mirror
+  return __builtin_elementwise_maximum(top, __shfl_xor(top, 16, 64));
 }
 
 // Code of a * inv (|a * inv| <= 448 up to a rounding), rounded up where the remainder and u = (h + 1/2) / 2^16 pass one
