@@ -13,7 +13,7 @@
 // ones.  8 elements per thread make every access 16 or 32 bytes wide, and 32 lanes a block of 256, whose largest value needs no
 // LDS.  Tensors go by in one launch, their descriptors in its arguments (48 of them: 6.8 us for 12 small ones;
 // a table in memory would have to be copied there first).  277M elements, bf16: 1099 us with fp32 states (5.5 TB/s; a
-// large copy reaches 4.8), 602 with 8-bit ones (4.6).  Non-temporal loads and stores of the states: 1157 with fp32 ones.
+// large copy reaches 4.8), 501 with 8-bit ones (5.6).  Non-temporal loads and stores of the states: 1157 with fp32 ones.
 #include <math.h>
 
 #include <type_traits>
@@ -141,30 +141,37 @@ MOE_DEV float block_top(const float (&a)[PER]) {
   return __builtin_elementwise_maximum(top, __shfl_xor(top, 16, 64));
 }
 
-// Code of a * inv (|a * inv| <= 448 up to a rounding), rounded up where the remainder and u = (h + 1/2) / 2^16 pass one
-// (u is never 0: the largest value of a block, 448 but for a rounding, keeps its code).  With e the exponent (-6 at least)
-// and k the eighths of 2^e, the code's magnitude is 8 (e + 6) + k for subnormal, normal and carried values alike; here 2^16
-// of it at once, the remainder in 16 bits: floor((floor(y + 1/2) + h) / 2^16) is floor((y + 1/2 + h) / 2^16).
-MOE_DEV uint32_t code8(float a, float inv, uint32_t h) {
-  const float y = fabsf(a) * inv;
-  const uint32_t e = max(__float_as_uint(y) >> 23, 121u);
-  const uint32_t k = (uint32_t)fmaf(y, __uint_as_float((273u - e) << 23), 0.5f);
-  return min(((e << 19) + k + h >> 16) - 968u, 126u);
+// Codes of four values (at most 448 but for a rounding) into a word.  The instruction adds the random number's upper 20
+// bits to the 20 bits that a code drops (shifted alike where it is subnormal), and cuts off: with 16 bits h and a half behind
+// them that is floor(y / d + u), u = (h + 1/2) / 2^16.  (u is never 0: the largest value of a block, 448 but for a rounding,
+// keeps its code.)  With ten instructions less per code, and the roots' range looked at once per wave, 277M elements take 501 us
+// for 611.
+MOE_DEV uint32_t codes4(const float *y, const uint32_t (&u)[4]) {
+  int c = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (int)u[0], 0, 0);
+  c = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (int)u[1], c, 1);
+  c = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (int)u[2], c, 2);
+  return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y[3], (int)u[3], c, 3);
 }
 
-// a rounded to codes, and the block's scale (NaN where a value is not finite, so that all of the block becomes one)
-template <bool SIGNED>
+// a rounded to codes, and the block's scale (NaN where a value is not finite, so that all of the block becomes one),
+// with the low or the high halves of h
+template <bool LOW>
 MOE_DEV void put8(uint8_t *p, float *scale, bool whole, int left, const float (&a)[PER],
                   const uint32_t (&h)[PER]) {
   const float top = block_top(a);
   const bool none = top < kLeast;
   const float inv = none ? 0.f : 1.f / top * 448.f;
-  u32x2 c = {0, 0};
+  u32x2 c;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    uint32_t k = code8(a[i], inv, SIGNED ? h[i] & 0xffffu : h[i] >> 16);
-    if (SIGNED) k |= __float_as_uint(a[i]) >> 24 & 0x80u;
-    c[i / 4] |= k << (8 * (i & 3));
+  for (int w = 0; w < 2; ++w) {
+    float y[4];
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = a[4 * w + i] * inv;
+      u[i] = (LOW ? h[4 * w + i] << 16 : h[4 * w + i] & 0xffff0000u) | 0x8000u;
+    }
+    c[w] = codes4(y, u);
   }
   if (whole) {
     *(u32x2 *)p = c;
@@ -186,12 +193,17 @@ MOE_DEV float root_of(float v) {
 // States in 8 bits: every operation rounded once, in the formulas' order, none fused, and the root to nearest (the hardware's
 // reciprocal root and one correction by the remainder).  A sum or a root that is a step off turns a rounding of codes the other
 // way now and then, and in later steps, through a block's largest value, the scale of all of it; like this the states do
-// not depend on how the arithmetic is carried out.  (277M elements: 560 us fused and with the root above.)
+// not depend on how the arithmetic is carried out.
 MOE_DEV float exact_root(float v) {
   const bool small = v < 0x1p-96f;
   const float x = small ? v * 0x1p64f : v, y = __builtin_amdgcn_rsqf(x), s = x * y, e = fmaf(-s, s, x);
   const float root = fmaf(e, 0.5f * y, s) * (small ? 0x1p-32f : 1.f);
   return e == e ? root : v;  // (of 0, infinity and NaN: they themselves)
+}
+// the same where no argument of the wave is small or not finite
+MOE_DEV float exact_root_in_range(float v) {
+  const float y = __builtin_amdgcn_rsqf(v), s = v * y;
+  return fmaf(fmaf(-s, s, v), 0.5f * y, s);
 }
 MOE_DEV float mean_of(float b, float old, float a, float x) {
 #pragma clang fp contract(off)
@@ -231,14 +243,32 @@ MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, 
     if constexpr (BITS == 8) {
       m[i] = mean_of(a.b1, m[i], a.a1, x);
       v[i] = square_of(a.b2, v[i], a.a2, x);
-      r[i] = exact_root(v[i]);
     } else {
       m[i] = fmaf(a.b1, m[i], a.a1 * x);
       v[i] = fmaf(a.b2, v[i], a.a2 * x * x);
-      r[i] = root_of(v[i]);
     }
-    w[i] = fmaf(w[i], keep, -(rate * m[i]) * __builtin_amdgcn_rcpf(fmaf(r[i], root, a.eps)));
   }
+  if constexpr (BITS == 8) {
+    float lo = v[0], hi = v[0];  // (NaN if one is)
+#pragma unroll
+    for (int i = 1; i < PER; ++i) {
+      lo = __builtin_elementwise_minimum(lo, v[i]);
+      hi = __builtin_elementwise_maximum(hi, v[i]);
+    }
+    if (__all(lo >= 0x1p-96f && hi < INFINITY)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) r[i] = exact_root_in_range(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) r[i] = exact_root(v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) r[i] = root_of(v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    w[i] = fmaf(w[i], keep, -(rate * m[i]) * __builtin_amdgcn_rcpf(fmaf(r[i], root, a.eps)));
   put8((P *)t.p + at, FULL, left, w);
   if (t.master) put8(t.master + at, FULL, left, w);
   if constexpr (BITS == 32) {
