@@ -61,12 +61,13 @@ int ce_tile_columns(int64_t M, int64_t K, int64_t V);
 // dl NULL: the forward's statistics; shape_v: the size that the tile's shape goes by
 hipError_t launch_ce_tiles(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v,
                            hipStream_t st);
-// The same in staged tiles, for any alignment: whether their reduction is whole, the columns of a wave
+// The same in tiles for any alignment, staged ones for bf16 and those of bf16 parts for fp32: whether their reduction is
+// whole, the columns of a wave
 bool ce_staged(int64_t M, int64_t K, int64_t V, int dtype);
 int ce_staged_columns(int64_t M, int64_t K, int64_t V, int dtype);
 hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs &ce, int M, int K, int V, int shape_v, int dtype,
                             hipStream_t st);
-// workspaces of dX and dW, and of logits that are left in memory; these
+// Workspaces of dX and dW, and of logits that are left in memory; these logits
 size_t ce_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
 size_t ce_logits_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
 hipError_t launch_ce_logits(const void *x, const void *W, float *logits, int M, int K, int V, int dtype, void *part, hipStream_t st);

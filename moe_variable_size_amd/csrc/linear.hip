@@ -1574,7 +1574,8 @@ hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs
   const Plan pl{staged_plan(M, shape_v, K, true).shape, 1};
   return run_staged<true, true, bf16_t, bf16_t>(a, pl, dl ? kCeGrad : kCeStats, nullptr, ce, st);
 }
-// Whether an fp32 product of these sizes takes the parts (few rows of x: streamed instead)
+// Whether products of these sizes take the parts (runs of four have to fit into every row; the logits of few rows of x
+// are streamed instead)
 static bool takes_parts(int64_t M, int64_t K, int64_t V, int dtype) { return dtype == MOE_F32 && K >= 4 && V >= 4 && M > 0; }
 size_t ce_part_bytes(int64_t M, int64_t K, int64_t V, int dtype) {
   size_t most = 0;
