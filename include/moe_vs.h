@@ -603,8 +603,11 @@ int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t
  * Gradient of sum_m g_m loss_m, with g = d_loss [M] (MOE_REDUCE_NONE), d_loss[0]
  * for every row (_SUM) or d_loss[0] / total[1] (_MEAN):
  *   dl = g_m ((1 + 2 z_weight lse_m) exp(l - lse_m) - [v = t]), 0 in rows that do
- *   not count, rounded to `dtype` for the two products (twice, with what the
- *   rounding leaves, for at most 512 rows of bf16);
+ *   not count, rounded to `dtype` for the two products: for at most 512 rows of
+ *   bf16 twice, with what the rounding leaves; for more of them dl / g_m, so that
+ *   no rounding is common to rows that share g, which comes into dX in fp32 and
+ *   into dW, for _NONE, by way of bf16(g_m / G x) and G = max |g| in fp32 (exact
+ *   where the counting rows' g are alike);
  *   dX = dl W [M, K],  dW = dl^T x [V, K], in `dtype`: each OVERWRITTEN, or NULL to
  *   skip.  (0 times what is not finite is NaN: rows of x that do not count have to be
  *   finite for dW, too.)
@@ -612,8 +615,8 @@ int moe_linear_ce_fwd(const void *x, const void *W, const void *targets, int32_t
  *   for _MEAN alone).  M may be 0 (dW is then zeros).
  *   workspace: moe_linear_ce_bwd_workspace_bytes(...) bytes, 256-byte aligned: dl
  *   of a piece of the vocabulary (256 MB, or 256 columns; twice that for at most
- *   512 rows of bf16), for few rows its logits in fp32, dX's sum in fp32, and the
- *   products'.
+ *   512 rows of bf16), for few rows its logits in fp32, in bf16 x once more (twice
+ *   for at most 512 rows), dX's sum in fp32, and the products'.
  */
 size_t moe_linear_ce_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t dtype);
 int moe_linear_ce_bwd(const float *d_loss, int32_t reduction, const float *total, const void *x,

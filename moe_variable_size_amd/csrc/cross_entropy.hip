@@ -6,15 +6,19 @@
 // exp(l - largest) of their columns (linear.hip, ce_stats); the parts of a row are joined here.  Backward:
 // the vocabulary goes by in pieces; a piece's dl, M x piece, comes out of the product that computes its
 // logits again (ce_grad), then dW's rows of the piece are one product, and dX another that adds to a sum in
-// fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it; of many rows the
-// roundings average out to one more like dX's and dW's own, but of few a row's largest entry, its target's, would move all of
-// the row's gradients by up to 2^-8 of them, where their own rounding is 2^-8 / sqrt 3 in norm at most.  There (bf16, up
-// to 512 rows: 3 deviations of their mean within a quarter of it) dl is two rows, its rounding and what that leaves.
-// bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
+// fp32.  dl is rounded once, to nearest, to the operands' type, as the matrix instructions take it.  In bf16 a rounding is up to
+// 2^-8 of an entry, and the target's entry, g (p - 1) for small p, carries most of its row's gradient: were g in it, rows that share
+// g, as those of a mean do, would all be off by the same part in the same direction (with 1020 rows and g = 1 / 1020, 2^-8: the
+// gradients by 2.4 times their own rounding in norm).  So dl is taken without g, and g goes in fp32 into dX's epilogue, row by
+// row, and where all rows share it into dW's.  Then a target's entry p - 1 is off by at most p, and by 2^-9, and differs from row to
+// row as p does.  Where rows differ in g, dW = G dl^T x' with G the largest |g| that is finite and x' = bf16(g / G x): one more
+// rounding of its own (none where they are alike), but of every element for itself.  Up to 512 rows of bf16 dl, with g, is two rows,
+// its rounding and what that leaves, at the cost of twice the rows in two of the three products: the gradients then are as good as
+// their own rounding at any p.  bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
-// bf16, 8192 x 4096 x 65536: 12.7 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.39 PFLOP/s and 43 us
-// besides; the loss of 2048 x 4096 x 50257 646 us.  fp32, 1074 x 600 x
+// bf16, 8192 x 4096 x 65536: 12.7 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.39 PFLOP/s and 68 us
+// besides (20 of them x by the rows' weights, not for a mean or a sum); the loss of 2048 x 4096 x 50257 646 us.  fp32, 1074 x 600 x
 // 47121, loss and gradients: 1.60 ms (2.36 by fp32 instructions; 1.99 for logits kept and three such products).  One row x 4096 x 32000: 51 us, 38 of them the streamed product (7.0 TB/s),
 // the others two launches.
 #include "cross_entropy.hpp"
@@ -152,15 +156,58 @@ __global__ __launch_bounds__(1024) void total_kernel(CeArgs a, int64_t M, const 
   total[2] = count ? (float)(sum / (double)count) : 0.f;
 }
 
+// factor [M + 1]: g is kept out of dl and put there, 0 for a row that does not count; behind the rows' the one that all share
 __global__ __launch_bounds__(256) void rows_kernel(CeArgs a, int64_t M, const float *d_loss, const float *lse,
-                                                   const float *total, int reduction, float z, CeRow *rows) {
+                                                   const float *total, int reduction, float z, CeRow *rows, float *factor) {
   const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (m >= M) return;
   const int64_t t = ce_target_id(a, m);
   float g = d_loss[reduction == MOE_REDUCE_NONE ? m : 0];
-  if (reduction == MOE_REDUCE_MEAN) g /= total[1];
+  if (reduction == MOE_REDUCE_MEAN) g = total[1] > 0.f ? g / total[1] : 0.f;
+  if (factor) {
+    factor[m] = t < 0 ? 0.f : g;
+    if (m == 0 && reduction != MOE_REDUCE_NONE) factor[M] = g;
+    g = 1.f;
+  }
   const float v = lse[m];
   rows[m] = CeRow{v, g * (1.f + 2.f * z * v), g, (int)t};
+}
+
+// factor[M]: the largest of the rows' magnitudes that are finite, 1 if there is none but 0
+__global__ __launch_bounds__(1024) void largest_kernel(float *factor, int64_t M) {
+  __shared__ float red[16];
+  float top = 0.f;
+  for (int64_t m = threadIdx.x; m < M; m += 1024) {
+    const float g = fabsf(factor[m]);
+    if (g < INFINITY) top = fmaxf(top, g);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, red[i]);
+  factor[M] = top > 0.f ? top : 1.f;
+}
+// y = x with its rows times their part of factor[M], 8 W elements of a row per thread (W: on 16-byte lines) or one
+template <bool W>
+__global__ __launch_bounds__(256) void weigh_kernel(const bf16_t *__restrict__ x, bf16_t *__restrict__ y, const float *factor, int64_t M,
+                                                    int64_t K) {
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  constexpr int E = W ? 8 : 1;
+  const float top = factor[M];
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E; i < M * K; i += (int64_t)gridDim.x * 256 * E) {
+    const float f = factor[i / K] / top;
+    if constexpr (W) {
+      const bf16x8 v = *(const bf16x8 *)(x + i);
+      bf16x8 r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = (__bf16)((float)v[e] * f);
+      *(bf16x8 *)(y + i) = r;
+    } else {
+      st(y + i, bf16_to_f32(x[i]) * f);
+    }
+  }
 }
 
 // x twice, for the two parts of dl
@@ -239,10 +286,11 @@ Fwd fwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
 
 struct Bwd {
   int64_t piece;
-  size_t dl, x2, sum, logits, gemm, total;  // offsets after the rows
+  size_t factor, dl, x2, sum, logits, gemm, total;  // offsets after the rows
 };
-// Parts of dl
+// Parts of dl; whether it is taken without g
 int dl_parts(int64_t M, int dtype) { return dtype == MOE_BF16 && M <= 512 ? 2 : 1; }
+bool dl_bare(int64_t M, int dtype) { return dtype == MOE_BF16 && dl_parts(M, dtype) == 1; }
 // 256 MB of dl in bf16
 int64_t bwd_piece(int64_t M, int64_t K, int64_t V) {
   const int64_t most = greatest(256, ((int64_t)1 << 27) / M / 256 * 256);
@@ -266,9 +314,11 @@ Bwd bwd_space(int64_t M, int64_t K, int64_t V, int dtype, Way way) {
   const int parts = dl_parts(M, dtype);
   Bwd w;
   w.piece = bwd_piece(M, K, V);
-  w.dl = up256((size_t)M * sizeof(CeRow));
+  const bool bare = dl_bare(M, dtype);
+  w.factor = up256((size_t)M * sizeof(CeRow));
+  w.dl = w.factor + (bare ? up256((size_t)(M + 1) * 4) : 0);
   w.x2 = w.dl + up256((size_t)parts * M * bwd_ld(w.piece) * es);
-  w.sum = w.x2 + (parts == 2 ? up256((size_t)2 * M * K * es) : 0);
+  w.sum = w.x2 + (parts == 2 || bare ? up256((size_t)parts * M * K * es) : 0);
   w.logits = w.sum + (parts == 2 || (w.piece < V && dtype == MOE_BF16) ? up256((size_t)parts * M * K * 4) : 0);
   w.gemm = w.logits + (way == MEMORY ? up256((size_t)M * w.piece * 4) : 0);
   size_t g = 0;
@@ -361,7 +411,9 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
   float *sum = dtype == MOE_F32 ? (float *)dX : (float *)((char *)ws + b.sum);
   float *logits = (float *)((char *)ws + b.logits);
   void *part = (char *)ws + b.gemm;
-  rows_kernel<<<(int)((M + 255) / 256), 256, 0, st>>>(a, M, d_loss, lse, total, reduction, z, (CeRow *)ws);
+  const bool bare = dl_bare(M, dtype);
+  float *factor = bare ? (float *)((char *)ws + b.factor) : nullptr;
+  rows_kernel<<<(int)((M + 255) / 256), 256, 0, st>>>(a, M, d_loss, lse, total, reduction, z, (CeRow *)ws, factor);
   hipError_t e = hipGetLastError();
   const int parts = dl_parts(M, dtype), rows = (int)M * parts;
   const bool once = b.piece >= V && parts == 1;
@@ -369,6 +421,16 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
   if (e == hipSuccess && dW && parts == 2) {
     xs = (char *)ws + b.x2;
     twice_kernel<<<(int)least((M * K + 255) / 256, 2048), 256, 0, st>>>((const bf16_t *)x, (bf16_t *)((char *)ws + b.x2), M * K);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && dW && bare && reduction == MOE_REDUCE_NONE) {
+    bf16_t *y = (bf16_t *)((char *)ws + b.x2);
+    xs = y;
+    largest_kernel<<<1, 1024, 0, st>>>(factor, M);
+    if (on_line(x) && K % 8 == 0)
+      weigh_kernel<true><<<(int)least((M * K / 8 + 255) / 256, 8192), 256, 0, st>>>((const bf16_t *)x, y, factor, M, K);
+    else
+      weigh_kernel<false><<<(int)least((M * K + 255) / 256, 8192), 256, 0, st>>>((const bf16_t *)x, y, factor, M, K);
     e = hipGetLastError();
   }
   for (int64_t v = 0; v < V && e == hipSuccess; v += b.piece) {
@@ -390,9 +452,9 @@ hipError_t launch_linear_ce_bwd(const float *d_loss, int reduction, const float 
       e = hipGetLastError();
     }
     if (e == hipSuccess && dW)
-      e = launch_ce_dw(dl, a.ld, xs, (char *)dW + (size_t)v * K * es, rows, (int)K, n, dtype, part, st);
+      e = launch_ce_dw(dl, a.ld, xs, bare ? factor + M : nullptr, (char *)dW + (size_t)v * K * es, rows, (int)K, n, dtype, part, st);
     if (e == hipSuccess && dX)
-      e = launch_ce_dx(dl, a.ld, w, v ? sum : nullptr, once ? dX : sum, !once, rows, (int)K, n, dtype, part, st);
+      e = launch_ce_dx(dl, a.ld, w, v ? sum : nullptr, factor, once ? dX : sum, !once, rows, (int)K, n, dtype, part, st);
   }
   if (e == hipSuccess && dX && !once && dtype == MOE_BF16) {
     const int64_t n = M * K;

@@ -71,9 +71,10 @@ hipError_t launch_ce_staged(const void *x, const void *W, void *dl, const CeArgs
 size_t ce_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
 size_t ce_logits_part_bytes(int64_t M, int64_t K, int64_t V, int dtype);
 hipError_t launch_ce_logits(const void *x, const void *W, float *logits, int M, int K, int V, int dtype, void *part, hipStream_t st);
-// out = dl W + sum (sum NULL: 0; fp32, may be out)
-hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
-                        int V, int dtype, void *part, hipStream_t st);
-hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, void *dW, int M, int K, int V, int dtype, void *part,
-                        hipStream_t st);
+// out = factor dl W + sum (factor [M], NULL: 1; sum NULL: 0; fp32, may be out)
+hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, const float *factor, void *out, bool out_f32,
+                        int M, int K, int V, int dtype, void *part, hipStream_t st);
+// dW = factor dl^T x (factor [1], NULL: 1)
+hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, const float *factor, void *dW, int M, int K, int V, int dtype,
+                        void *part, hipStream_t st);
 }  // namespace moe

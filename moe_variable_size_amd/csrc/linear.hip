@@ -30,6 +30,9 @@ struct GemmArgs {
   int M, N, K;
   int64_t lda, ldb;  // K-major: elements between rows; MN-major: between reduction rows
   bool vec;          // N a multiple of 8; out, z, residual and bias on 16-byte lines
+  // without an activation, row m's products times factor[m * factor_step], before bias and residual; NULL: 1
+  const float *factor = nullptr;
+  int64_t factor_step = 0;
 };
 
 // buffer resource from wave-uniform values, in scalar registers
@@ -72,6 +75,10 @@ MOE_DEV void finish8(const GemmArgs &p, f32x4 (&v)[2], int64_t at) {
     for (int i = 0; i < 4; ++i) v[h][i] = act_fwd<ACT>(v[h][i]) + r[h][i];
   put8((To *)p.out + at, v);
 }
+template <int ACT>
+MOE_DEV float factor_of(const GemmArgs &p, int64_t m) {
+  return ACT == MOE_ACT_NONE && p.factor ? p.factor[m * p.factor_step] : 1.f;
+}
 template <typename T, typename To, int ACT>
 MOE_DEV void finish1(const GemmArgs &p, float v, int64_t at) {
   if (p.z) stf((T *)p.z + at, v);
@@ -93,6 +100,11 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
         v[0] += get4(part + s * total + at);
         v[1] += get4(part + s * total + at + 4);
       }
+      if (ACT == MOE_ACT_NONE && p.factor) {
+        const float f = factor_of<ACT>(p, at / p.N);
+        v[0] *= f;
+        v[1] *= f;
+      }
       if (p.bias) {
         const int n = (int)(at % p.N);
         v[0] += get4((const T *)p.bias + n);
@@ -104,6 +116,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, const float *part
     for (int64_t at = i0; at < total; at += step) {
       float v = part[at];
       for (int s = 1; s < splits; ++s) v += part[s * total + at];
+      if (ACT == MOE_ACT_NONE && p.factor) v *= factor_of<ACT>(p, at / p.N);
       if (p.bias) v += ldf((const T *)p.bias + at % p.N);
       finish1<T, To, ACT>(p, v, at);
     }
@@ -286,7 +299,7 @@ MOE_DEV void staged_out(const GemmArgs &p, int splits, int split, float *part, c
         if (splits > 1)
           part[at] = acc[i][j][e];
         else
-          finish1<T, To, ACT>(p, acc[i][j][e] + b, at);
+          finish1<T, To, ACT>(p, acc[i][j][e] * factor_of<ACT>(p, m) + b, at);
       }
   }
 }
@@ -706,6 +719,11 @@ MOE_DEV void tile_epilogue(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2
           put8(pout + at, v);
           continue;
         }
+        if (ACT == MOE_ACT_NONE && p.factor) {
+          const float f = factor_of<ACT>(p, m);
+          v[0] *= f;
+          v[1] *= f;
+        }
         v[0] += b[0];
         v[1] += b[1];
         finish8<bf16_t, To, ACT>(p, v, at);
@@ -720,7 +738,7 @@ MOE_DEV void tile_epilogue(const PipeArgs &q, char *lds, const f32x4 (&acc)[2][2
           if (part)
             pout[at] = v;
           else
-            finish1<bf16_t, To, ACT>(p, v + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
+            finish1<bf16_t, To, ACT>(p, v * factor_of<ACT>(p, m) + (p.bias ? ldf((const bf16_t *)p.bias + n0 + c) : 0.f), at);
         }
       }
     }
@@ -1417,6 +1435,7 @@ hipError_t gemm(GemmArgs a, int act, void *part, hipStream_t st) {
         b.out = (To *)a.out + m0 * a.N;
         if (a.res) b.res = (const To *)a.res + m0 * a.N;
         if (a.z) b.z = (T *)a.z + m0 * a.N;
+        if (a.factor) b.factor = a.factor + m0 * a.factor_step;
         const hipError_t e = gemm<AK, BKM, T, To>(b, act, part, st);
         if (e != hipSuccess) return e;
       }
@@ -1593,17 +1612,17 @@ hipError_t launch_ce_logits(const void *x, const void *W, float *logits, int M, 
     return fine<true, true>(GemmArgs{x, W, nullptr, nullptr, logits, nullptr, M, V, K, K, K, false}, part, st);
   return launch_linear_fwd(x, W, nullptr, nullptr, logits, nullptr, M, K, V, MOE_ACT_NONE, dtype, MOE_F32, part, st);
 }
-hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, void *out, bool out_f32, int M, int K,
-                        int V, int dtype, void *part, hipStream_t st) {
-  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false};
+hipError_t launch_ce_dx(const void *dl, int64_t ld, const void *W, const float *sum, const float *factor, void *out, bool out_f32,
+                        int M, int K, int V, int dtype, void *part, hipStream_t st) {
+  const GemmArgs a{dl, W, nullptr, sum, out, nullptr, M, K, V, ld, K, false, factor, 1};
   if (takes_parts(M, K, V, dtype)) return fine<true, false>(a, part, st);
   if (dtype == MOE_F32) return gemm<true, false, float, float>(a, MOE_ACT_NONE, part, st);
   if (out_f32) return gemm<true, false, bf16_t, float>(a, MOE_ACT_NONE, part, st);
   return gemm<true, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
 }
-hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, void *dW, int M, int K, int V, int dtype, void *part,
-                        hipStream_t st) {
-  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false};
+hipError_t launch_ce_dw(const void *dl, int64_t ld, const void *x, const float *factor, void *dW, int M, int K, int V, int dtype,
+                        void *part, hipStream_t st) {
+  const GemmArgs a{dl, x, nullptr, nullptr, dW, nullptr, V, K, M, ld, K, false, factor, 0};
   if (takes_parts(M, K, V, dtype)) return fine<false, false>(a, part, st);
   if (dtype == MOE_F32) return gemm<false, false, float, float>(a, MOE_ACT_NONE, part, st);
   return gemm<false, false, bf16_t, bf16_t>(a, MOE_ACT_NONE, part, st);
