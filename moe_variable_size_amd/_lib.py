@@ -137,6 +137,8 @@ SIGNATURES = {
                                          _P, _SZ, _P]),
     "moe_adamw_step": (ctypes.c_int, [_P, _I32, _F64, _P, _F64, _F64, _F64, _F64, _I64, _P, _P, _U32, _I32,
                                       _I32, _I32, _P]),
+    "moe_adamw_step_counts": (ctypes.c_int, [_P, _I32, _F64, _P, _F64, _F64, _F64, _F64, _P, _I64, _P, _U32, _I32,
+                                             _I32, _I32, _P]),
     "moe_tile_map": (ctypes.c_int, [_SCHED_P, _I64, _I32, _I32, _P, _P, _P, _I64, _P]),
     "moe_set_tile_rows": (ctypes.c_int, [_I32]),
     "moe_set_combine": (ctypes.c_int, [_I32]),

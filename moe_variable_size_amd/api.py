@@ -990,7 +990,8 @@ def _tensors(ts, name: str, count: int, dtypes, sizes, index: int) -> list:
 
 def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                    weight_decay: float = 0.01, masters=None, m_scales=None, v_scales=None,
-                   grad_scale: Optional[torch.Tensor] = None, seed: int = 0, numbers=None, stream=None) -> None:
+                   grad_scale: Optional[torch.Tensor] = None, seed: int = 0, numbers=None,
+                   counts: Optional[torch.Tensor] = None, stream=None) -> None:
     """One AdamW step on lists of tensors, in place, in one launch per 48 of
     them: params (float32 or bfloat16), grads (float32 or bfloat16) and the
     states exp_avgs and exp_avg_sqs, float32, or float8_e4m3fn codes of m and
@@ -999,7 +1000,9 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9
     tensor's (its place in the list, or ``numbers``).  ``masters``: float32
     copies of bfloat16 params, on which the step is then taken.  ``step`` (from
     1 on) and ``lr`` are numbers, or tensors of one element (int32, float32) on
-    the device, which a captured graph reads anew at each replay.
+    the device, which a captured graph reads anew at each replay; with
+    ``counts`` (int32, on the device) each tensor's step is the entry at its
+    number instead.
     ``grad_scale`` [1] float32 multiplies the gradients; where it is not finite
     nothing is changed.  No two tensors may overlap."""
     lib = _lib.load()
@@ -1042,14 +1045,22 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9
             _require(t, name, dt)
             if t.numel() != 1 or t.get_device() != index:
                 raise ValueError(f"{name} must be one number on {dev}")
+    if counts is not None:
+        _require(counts, "counts", torch.int32, 1)
+        if counts.get_device() != index:
+            raise ValueError(f"counts must be on {dev}")
     on_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
     table = array.array("q", [a for row in zip(p, g, m, v, ms, vs, w, sizes, numbers) for a in row])
+    rate = 0.0 if on_dev[1] else lr, _ptr(lr) if on_dev[1] else None, betas[0], betas[1], eps, weight_decay
+    kinds = _DTYPES[params[0].dtype], _DTYPES[grads[0].dtype], 8 if eight else 32
     ctx, raw = _launch(params[0], stream)
     with ctx:
-        st = lib.moe_adamw_step(table.buffer_info()[0], count, 0.0 if on_dev[1] else lr, _ptr(lr) if on_dev[1] else None,
-                                betas[0], betas[1], eps, weight_decay, 1 if on_dev[0] else step,
-                                _ptr(step) if on_dev[0] else None, _ptr(grad_scale), seed & 0xFFFFFFFF,
-                                _DTYPES[params[0].dtype], _DTYPES[grads[0].dtype], 8 if eight else 32, raw)
+        if counts is None:
+            st = lib.moe_adamw_step(table.buffer_info()[0], count, *rate, 1 if on_dev[0] else step,
+                                    _ptr(step) if on_dev[0] else None, _ptr(grad_scale), seed & 0xFFFFFFFF, *kinds, raw)
+        else:
+            st = lib.moe_adamw_step_counts(table.buffer_info()[0], count, *rate, _ptr(counts), counts.numel(),
+                                           _ptr(grad_scale), seed & 0xFFFFFFFF, *kinds, raw)
     _lib.check("moe_adamw_step", st)
 
 
@@ -1057,8 +1068,9 @@ class AdamW:
     """AdamW over a list of parameters, float32 or bfloat16 and dense, by
     ``moe_adamw_step``: the states in 32 or 8 bits (``state_bits``), with
     ``master`` a float32 copy of every bfloat16 parameter.  ``step()`` takes
-    each parameter's ``.grad``; those without one are left as they are.
-    ``capturable`` keeps the step's number and ``lr`` on the device, so that a
+    each parameter's ``.grad``; those without one are left as they are, and
+    their steps are not counted (``t`` is the largest count).
+    ``capturable`` keeps the steps' numbers and ``lr`` on the device, so that a
     step captured in a graph counts on and follows ``set_lr`` when replayed."""
 
     def __init__(self, params, *, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -1089,8 +1101,13 @@ class AdamW:
         self.v_scale = [zeros(-(-p.numel() // 256), torch.float32) for p in self.params] if eight else None
         self.masters = [p.detach().float() if p.dtype == torch.bfloat16 else None
                         for p in self.params] if master else None
-        self.t = torch.zeros(1, dtype=torch.int32, device=dev) if capturable else 0
+        # steps taken by each parameter
+        self._t = torch.zeros(len(self.params), dtype=torch.int32, device=dev) if capturable else [0] * len(self.params)
         self.lr = torch.full((1,), float(lr), device=dev) if capturable else float(lr)
+
+    @property
+    def t(self):
+        return self._t.max() if isinstance(self._t, torch.Tensor) else max(self._t)
 
     def set_lr(self, lr: float) -> None:
         if self.capturable:
@@ -1104,26 +1121,44 @@ class AdamW:
 
     @torch.no_grad()
     def step(self, grad_scale: Optional[torch.Tensor] = None) -> None:
-        self.t += 1
+        on_dev = isinstance(self._t, torch.Tensor)
         sets = {}
         for i, p in enumerate(self.params):
             if p.grad is not None:
-                sets.setdefault((p.dtype, p.grad.dtype), []).append(i)
-        for (dtype, _), at in sets.items():
+                sets.setdefault((0 if on_dev else self._t[i], p.dtype, p.grad.dtype), []).append(i)
+        for (t, dtype, _), at in sets.items():
             def of(a, at=at):
                 return None if a is None else [a[i] for i in at]
             params = of(self.params)
-            moe_adamw_step([p.detach() for p in params], [p.grad.contiguous() for p in params], of(self.m), of(self.v),
-                           step=self.t, lr=self.lr, betas=self.betas, eps=self.eps, weight_decay=self.weight_decay,
-                           masters=of(self.masters) if dtype == torch.bfloat16 else None, m_scales=of(self.m_scale),
-                           v_scales=of(self.v_scale), grad_scale=grad_scale, seed=self.seed, numbers=at)
+            if on_dev:
+                self._count(at, 1)
+            try:
+                moe_adamw_step([p.detach() for p in params], [p.grad.contiguous() for p in params], of(self.m), of(self.v),
+                               step=t + 1, counts=self._t if on_dev else None, lr=self.lr, betas=self.betas,
+                               eps=self.eps, weight_decay=self.weight_decay,
+                               masters=of(self.masters) if dtype == torch.bfloat16 else None, m_scales=of(self.m_scale),
+                               v_scales=of(self.v_scale), grad_scale=grad_scale, seed=self.seed, numbers=at)
+            except BaseException:
+                if on_dev:  # (a refused step is not counted)
+                    self._count(at, -1)
+                raise
             torch.autograd.graph.increment_version(params)
+            if not on_dev:
+                for i in at:
+                    self._t[i] = t + 1
+
+    def _count(self, at, by) -> None:
+        if len(at) == len(self.params):
+            self._t += by
+        else:
+            torch._foreach_add_([self._t[i:i + 1] for i in at], by)
 
     _LISTS = ("m", "v", "m_scale", "v_scale", "masters")
 
     def state_dict(self) -> dict:
-        """The states themselves (not copies), the step's number and the learning rate."""
-        return {"t": int(self.t), "lr": float(self.lr), "state_bits": self.state_bits, "seed": self.seed,
+        """The states themselves (not copies), the steps' numbers and the learning rate."""
+        steps = self._t.tolist() if isinstance(self._t, torch.Tensor) else list(self._t)
+        return {"t": max(steps), "steps": steps, "lr": float(self.lr), "state_bits": self.state_bits, "seed": self.seed,
                 **{k: getattr(self, k) for k in self._LISTS}}
 
     @torch.no_grad()
@@ -1138,13 +1173,16 @@ class AdamW:
                     for x, y in zip(a, b)))):
                 raise ValueError(f"{k} does not fit these parameters")
             pairs += [(x, y) for x, y in zip(a or (), b or ()) if x is not None]
+        steps = [int(t) for t in d.get("steps", [d["t"]] * len(self.params))]  # (older states: one number for all)
+        if len(steps) != len(self.params):
+            raise ValueError("steps does not fit these parameters")
         for x, y in pairs:
             x.view(torch.uint8).copy_(y.view(torch.uint8)) if x.dtype == torch.float8_e4m3fn else x.copy_(y)
         self.seed = int(d["seed"])
-        if self.capturable:
-            self.t.fill_(int(d["t"]))
+        if isinstance(self._t, torch.Tensor):
+            self._t.copy_(torch.tensor(steps, dtype=torch.int32))
         else:
-            self.t = int(d["t"])
+            self._t = steps
         self.set_lr(d["lr"])
 
 

@@ -41,6 +41,7 @@ struct Args {
   Tensor t[kTensors];
   int first[kTensors + 1];  // first workgroup of each tensor, then the launch's workgroups
   uint32_t number[kTensors];
+  int count_at[kTensors];   // place of each tensor's t in t_dev
   uint64_t wide;            // bit i: tensor i lies on 16-byte lines
   int count;
   float lr, b1, a1, b2, a2, eps, wd;  // a = 1 - b
@@ -216,7 +217,7 @@ MOE_DEV float square_of(float b, float old, float a, float x) {
 
 // elements at .. at + 7 of tensor t (FULL: the whole workgroup's are there, on 16-byte lines)
 template <typename P, typename G, int BITS, bool FULL>
-MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, float s) {
+MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int count_at, int64_t at, float s) {
   const int left = FULL ? PER : (int)max((int64_t)0, min((int64_t)PER, t.n - at));
   float g[PER], m[PER], v[PER], w[PER], r[PER];
   get8((const G *)t.g + at, FULL, left, g);
@@ -232,9 +233,9 @@ MOE_DEV void step8(const Args &a, const Tensor &t, uint32_t number, int64_t at, 
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] *= v[i];
   }
-  const uint32_t step = a.t_dev ? (uint32_t)*a.t_dev : a.t_low;
-  const float c1 = a.t_dev ? -expm1f((float)*a.t_dev * a.ln1) : a.c1;
-  const float c2 = a.t_dev ? -expm1f((float)*a.t_dev * a.ln2) : a.c2;
+  const uint32_t step = a.t_dev ? (uint32_t)a.t_dev[count_at] : a.t_low;
+  const float c1 = a.t_dev ? -expm1f((float)a.t_dev[count_at] * a.ln1) : a.c1;
+  const float c2 = a.t_dev ? -expm1f((float)a.t_dev[count_at] * a.ln2) : a.c2;
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const float rate = lr / c1, keep = 1.f - lr * a.wd, root = 1.f / sqrtf(c2);
 #pragma unroll
@@ -299,8 +300,8 @@ __global__ __launch_bounds__(NT) void adamw_kernel(const Args a) {
     if (a.first[mid] <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
   }
   const int64_t first = (int64_t)((int)blockIdx.x - a.first[lo]) * CHUNK, at = first + threadIdx.x * PER;
-  if ((a.wide >> lo & 1) && first + CHUNK <= a.t[lo].n) step8<P, G, BITS, true>(a, a.t[lo], a.number[lo], at, s);
-  else step8<P, G, BITS, false>(a, a.t[lo], a.number[lo], at, s);
+  if ((a.wide >> lo & 1) && first + CHUNK <= a.t[lo].n) step8<P, G, BITS, true>(a, a.t[lo], a.number[lo], a.count_at[lo], at, s);
+  else step8<P, G, BITS, false>(a, a.t[lo], a.number[lo], a.count_at[lo], at, s);
 }
 
 template <typename P, typename G>
@@ -348,6 +349,7 @@ hipError_t launch_adamw(const moe_adamw_tensor *tensors, int count, const AdamwO
       const int k = a.count++;
       a.t[k] = Tensor{x.param, x.grad, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n};
       a.number[k] = (uint32_t)x.number;
+      a.count_at[k] = o.each ? (int)x.number : 0;
       a.first[k + 1] = a.first[k] + (int)blocks;
       if (line(x.param, 16) && line(x.grad, 16) && line(x.m, state) && line(x.v, state) && line(x.master, 16))
         a.wide |= 1ull << k;

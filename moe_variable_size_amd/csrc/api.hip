@@ -935,26 +935,25 @@ int moe_linear_ce_bwd(const float *d_loss, int32_t reduction, const float *total
   }));
 }
 
-int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
-                   double beta1, double beta2, double eps, double weight_decay, int64_t step,
-                   const int32_t *step_dev, const float *grad_scale, uint32_t seed,
-                   int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
+static int adamw_step(const moe_adamw_tensor *tensors, int32_t count, const AdamwOptions &o, int64_t steps,
+                      int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
   if ((param_dtype != MOE_F32 && param_dtype != MOE_BF16) ||
       (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16))
     return MOE_ERR_DTYPE;
   if (count < 0) return MOE_ERR_SHAPE;
   if (state_bits != 8 && state_bits != 32) return MOE_ERR_OPTION;
-  if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0) || !isfinite(eps) ||
-      !isfinite(lr) || !isfinite(weight_decay) || (!step_dev && (step < 1 || step >= kMax32)))
+  if (!(o.beta1 >= 0 && o.beta1 < 1 && o.beta2 >= 0 && o.beta2 < 1 && o.eps >= 0) || !isfinite(o.eps) ||
+      !isfinite(o.lr) || !isfinite(o.weight_decay) || (!o.step_dev && (o.step < 1 || o.step >= kMax32)))
     return MOE_ERR_OPTION;
   if (count > 0 && !tensors) return MOE_ERR_NULL;
-  if (!aligned(lr_dev, 4) || !aligned(step_dev, 4) || !aligned(grad_scale, 4)) return MOE_ERR_ALIGN;
+  if (!aligned(o.lr_dev, 4) || !aligned(o.step_dev, 4) || !aligned(o.grad_scale, 4)) return MOE_ERR_ALIGN;
   const size_t ep = esize(param_dtype), eg = esize(grad_dtype), es = state_bits == 8 ? 1 : 4;
   for (int32_t i = 0; i < count; ++i) {
     const moe_adamw_tensor &t = tensors[i];
     if (t.n < 0) return MOE_ERR_SHAPE;
     if (t.n == 0) continue;
     if (t.n > ((int64_t)1 << 34)) return MOE_ERR_LIMIT;
+    if (o.each && (t.number < 0 || t.number >= steps)) return MOE_ERR_SHAPE;
     if (t.master && param_dtype != MOE_BF16) return MOE_ERR_DTYPE;
     if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
       return MOE_ERR_NULL;
@@ -963,10 +962,27 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, co
       return MOE_ERR_ALIGN;
   }
   hipStream_t st = (hipStream_t)stream;
-  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev, grad_scale, seed};
   return hip_status(timed(F_ADAMW, st, [&] {
     return launch_adamw(tensors, count, o, param_dtype, grad_dtype, state_bits, st);
   }));
+}
+
+int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
+                   double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                   const int32_t *step_dev, const float *grad_scale, uint32_t seed,
+                   int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
+  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev, false, grad_scale, seed};
+  return adamw_step(tensors, count, o, 0, param_dtype, grad_dtype, state_bits, stream);
+}
+
+int moe_adamw_step_counts(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
+                          double beta1, double beta2, double eps, double weight_decay,
+                          const int32_t *steps_dev, int64_t steps, const float *grad_scale, uint32_t seed,
+                          int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
+  if (steps < 0 || steps >= kMax32) return MOE_ERR_SHAPE;
+  if (count > 0 && !steps_dev) return MOE_ERR_NULL;
+  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, 1, lr_dev, steps_dev, true, grad_scale, seed};
+  return adamw_step(tensors, count, o, steps, param_dtype, grad_dtype, state_bits, stream);
 }
 
 int moe_tile_map(const moe_schedule *sched, int64_t N, int32_t BM, int32_t BN, int32_t *tile_start,

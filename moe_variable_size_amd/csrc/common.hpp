@@ -216,6 +216,7 @@ struct AdamwOptions {
   int64_t step;
   const float *lr_dev;
   const int32_t *step_dev;
+  bool each;  // step_dev [by the tensors' numbers], else [1]
   const float *grad_scale;
   uint32_t seed;
 };
