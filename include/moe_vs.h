@@ -675,13 +675,14 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, co
                    int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream);
 
 /*
- * The same with a t for every tensor: steps_dev[number] on the device, 0 <= number <
- * steps (MOE_ERR_SHAPE), read when the launch runs: tensors that did not take part in
- * every step, also in graphs that are replayed.
+ * The same for tensors that do not take part in every step, also in graphs that are
+ * replayed: steps_dev[number], on the device, holds the steps that a tensor has taken
+ * and is first UPDATED to t, one more, unless grad_scale is not finite.  0 <= number <
+ * steps (MOE_ERR_SHAPE), all different; a tensor of n = 0 is not counted.
  */
 int moe_adamw_step_counts(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
                           double beta1, double beta2, double eps, double weight_decay,
-                          const int32_t *steps_dev, int64_t steps, const float *grad_scale, uint32_t seed,
+                          int32_t *steps_dev, int64_t steps, const float *grad_scale, uint32_t seed,
                           int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream);
 
 /*

@@ -1000,9 +1000,10 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9
     tensor's (its place in the list, or ``numbers``).  ``masters``: float32
     copies of bfloat16 params, on which the step is then taken.  ``step`` (from
     1 on) and ``lr`` are numbers, or tensors of one element (int32, float32) on
-    the device, which a captured graph reads anew at each replay; with
-    ``counts`` (int32, on the device) each tensor's step is the entry at its
-    number instead.
+    the device, which a captured graph reads anew at each replay.  With
+    ``counts`` (int32, on the device) ``step`` is not looked at: the entry at a
+    tensor's number (all different) holds the steps that it has taken, and
+    counts this one unless ``grad_scale`` is not finite.
     ``grad_scale`` [1] float32 multiplies the gradients; where it is not finite
     nothing is changed.  No two tensors may overlap."""
     lib = _lib.load()
@@ -1069,7 +1070,9 @@ class AdamW:
     ``moe_adamw_step``: the states in 32 or 8 bits (``state_bits``), with
     ``master`` a float32 copy of every bfloat16 parameter.  ``step()`` takes
     each parameter's ``.grad``; those without one are left as they are, and
-    their steps are not counted (``t`` is the largest count).
+    their steps are not counted (``t`` is the largest count).  Nor is a step
+    whose ``grad_scale`` is not finite, in which nothing is changed: from the
+    first one with a scale on the counts are kept on the device.
     ``capturable`` keeps the steps' numbers and ``lr`` on the device, so that a
     step captured in a graph counts on and follows ``set_lr`` when replayed."""
 
@@ -1107,7 +1110,9 @@ class AdamW:
 
     @property
     def t(self):
-        return self._t.max() if isinstance(self._t, torch.Tensor) else max(self._t)
+        if isinstance(self._t, torch.Tensor):
+            return self._t.max() if self.capturable else int(self._t.max())
+        return max(self._t)
 
     def set_lr(self, lr: float) -> None:
         if self.capturable:
@@ -1121,6 +1126,12 @@ class AdamW:
 
     @torch.no_grad()
     def step(self, grad_scale: Optional[torch.Tensor] = None) -> None:
+        if grad_scale is not None:
+            _require(grad_scale, "grad_scale", torch.float32)
+            if grad_scale.numel() != 1 or grad_scale.device != self.params[0].device:
+                raise ValueError(f"grad_scale must be one number on {self.params[0].device}")
+            if not isinstance(self._t, torch.Tensor):
+                self._t = torch.tensor(self._t, dtype=torch.int32, device=grad_scale.device)
         on_dev = isinstance(self._t, torch.Tensor)
         sets = {}
         for i, p in enumerate(self.params):
@@ -1130,28 +1141,15 @@ class AdamW:
             def of(a, at=at):
                 return None if a is None else [a[i] for i in at]
             params = of(self.params)
-            if on_dev:
-                self._count(at, 1)
-            try:
-                moe_adamw_step([p.detach() for p in params], [p.grad.contiguous() for p in params], of(self.m), of(self.v),
-                               step=t + 1, counts=self._t if on_dev else None, lr=self.lr, betas=self.betas,
-                               eps=self.eps, weight_decay=self.weight_decay,
-                               masters=of(self.masters) if dtype == torch.bfloat16 else None, m_scales=of(self.m_scale),
-                               v_scales=of(self.v_scale), grad_scale=grad_scale, seed=self.seed, numbers=at)
-            except BaseException:
-                if on_dev:  # (a refused step is not counted)
-                    self._count(at, -1)
-                raise
+            moe_adamw_step([p.detach() for p in params], [p.grad.contiguous() for p in params], of(self.m), of(self.v),
+                           step=t + 1, counts=self._t if on_dev else None, lr=self.lr, betas=self.betas, eps=self.eps,
+                           weight_decay=self.weight_decay, masters=of(self.masters) if dtype == torch.bfloat16 else None,
+                           m_scales=of(self.m_scale), v_scales=of(self.v_scale), grad_scale=grad_scale, seed=self.seed,
+                           numbers=at)
             torch.autograd.graph.increment_version(params)
             if not on_dev:
                 for i in at:
                     self._t[i] = t + 1
-
-    def _count(self, at, by) -> None:
-        if len(at) == len(self.params):
-            self._t += by
-        else:
-            torch._foreach_add_([self._t[i:i + 1] for i in at], by)
 
     _LISTS = ("m", "v", "m_scale", "v_scale", "masters")
 

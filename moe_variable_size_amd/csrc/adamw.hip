@@ -304,6 +304,13 @@ __global__ __launch_bounds__(NT) void adamw_kernel(const Args a) {
   else step8<P, G, BITS, false>(a, a.t[lo], a.number[lo], a.count_at[lo], at, s);
 }
 
+// one more step for each of the launch's tensors, before it
+__global__ __launch_bounds__(64) void count_kernel(const Args a, int32_t *counts) {
+  const float s = a.scale ? *a.scale : 1.f;
+  if (fabsf(s) < INFINITY && (int)threadIdx.x < a.count) ++counts[a.count_at[threadIdx.x]];
+}
+static_assert(kTensors <= 64, "a thread per tensor");
+
 template <typename P, typename G>
 hipError_t launch(const Args &a, int bits, hipStream_t st) {
   const int grid = a.first[a.count];
@@ -349,13 +356,18 @@ hipError_t launch_adamw(const moe_adamw_tensor *tensors, int count, const AdamwO
       const int k = a.count++;
       a.t[k] = Tensor{x.param, x.grad, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n};
       a.number[k] = (uint32_t)x.number;
-      a.count_at[k] = o.each ? (int)x.number : 0;
+      a.count_at[k] = o.counts ? (int)x.number : 0;
       a.first[k + 1] = a.first[k] + (int)blocks;
       if (line(x.param, 16) && line(x.grad, 16) && line(x.m, state) && line(x.v, state) && line(x.master, 16))
         a.wide |= 1ull << k;
     }
     if (!a.count) break;
     hipError_t e;
+    if (o.counts) {
+      count_kernel<<<1, 64, 0, st>>>(a, o.counts);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     if (param_dtype == MOE_F32)
       e = grad_dtype == MOE_F32 ? launch<float, float>(a, bits, st) : launch<float, bf16_t>(a, bits, st);
     else

@@ -953,7 +953,7 @@ static int adamw_step(const moe_adamw_tensor *tensors, int32_t count, const Adam
     if (t.n < 0) return MOE_ERR_SHAPE;
     if (t.n == 0) continue;
     if (t.n > ((int64_t)1 << 34)) return MOE_ERR_LIMIT;
-    if (o.each && (t.number < 0 || t.number >= steps)) return MOE_ERR_SHAPE;
+    if (o.counts && (t.number < 0 || t.number >= steps)) return MOE_ERR_SHAPE;
     if (t.master && param_dtype != MOE_BF16) return MOE_ERR_DTYPE;
     if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
       return MOE_ERR_NULL;
@@ -971,17 +971,17 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int32_t count, double lr, co
                    double beta1, double beta2, double eps, double weight_decay, int64_t step,
                    const int32_t *step_dev, const float *grad_scale, uint32_t seed,
                    int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
-  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev, false, grad_scale, seed};
+  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev, nullptr, grad_scale, seed};
   return adamw_step(tensors, count, o, 0, param_dtype, grad_dtype, state_bits, stream);
 }
 
 int moe_adamw_step_counts(const moe_adamw_tensor *tensors, int32_t count, double lr, const float *lr_dev,
                           double beta1, double beta2, double eps, double weight_decay,
-                          const int32_t *steps_dev, int64_t steps, const float *grad_scale, uint32_t seed,
+                          int32_t *steps_dev, int64_t steps, const float *grad_scale, uint32_t seed,
                           int32_t param_dtype, int32_t grad_dtype, int32_t state_bits, void *stream) {
   if (steps < 0 || steps >= kMax32) return MOE_ERR_SHAPE;
   if (count > 0 && !steps_dev) return MOE_ERR_NULL;
-  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, 1, lr_dev, steps_dev, true, grad_scale, seed};
+  const AdamwOptions o{lr, beta1, beta2, eps, weight_decay, 1, lr_dev, steps_dev, steps_dev, grad_scale, seed};
   return adamw_step(tensors, count, o, steps, param_dtype, grad_dtype, state_bits, stream);
 }
 

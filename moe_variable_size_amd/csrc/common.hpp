@@ -216,7 +216,7 @@ struct AdamwOptions {
   int64_t step;
   const float *lr_dev;
   const int32_t *step_dev;
-  bool each;  // step_dev [by the tensors' numbers], else [1]
+  int32_t *counts;  // the steps taken, by the tensors' numbers, in the place of step and step_dev; NULL: none
   const float *grad_scale;
   uint32_t seed;
 };

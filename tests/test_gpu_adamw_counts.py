@@ -153,6 +153,7 @@ def test_a_graph_replayed_after_some_went_ahead():
 def test_counts_by_number_of_more_tensors_than_a_launch():
     n = 70
     t = torch.arange(1, 2 * n + 1, dtype=torch.int32, device="cuda")
+    taken = t.clone()
     numbers = [2 * i + 1 for i in range(n)]
     for bits in (32, 8):
         kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
@@ -167,7 +168,11 @@ def test_counts_by_number_of_more_tensors_than_a_launch():
 
         a, b = build(), build()
         opts = dict(lr=LR, betas=BETAS, weight_decay=WD, seed=7)
-        api.moe_adamw_step(*a[:4], step=1, counts=t, numbers=numbers, m_scales=a[4], v_scales=a[5], **opts)
+        counts = t - 1
+        api.moe_adamw_step(*a[:4], step=1, counts=counts, numbers=numbers, m_scales=a[4], v_scales=a[5], **opts)
+        want = t - 1
+        want[1::2] += 1
+        assert torch.equal(counts, want) and torch.equal(t, taken)
         for i in range(n):
             each = [x[i:i + 1] if x is not None else None for x in b]
             api.moe_adamw_step(*each[:4], step=t[numbers[i]:numbers[i] + 1], numbers=[numbers[i]], m_scales=each[4],
@@ -238,3 +243,82 @@ def test_a_refused_step_is_not_counted(capturable):
         p.grad = None
     opt.step()
     assert opt.state_dict()["steps"] == [1, 0, 0, 0]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capturable", [False, True])
+@pytest.mark.parametrize("some", [False, True])
+def test_steps_left_out_are_not_counted(bits, capturable, some):
+    """A run in which some steps' scales are not finite equals, bit for bit, the run of the others alone."""
+    def run(scales):
+        ps = params(torch.bfloat16)
+        opt = api.AdamW(ps, lr=LR, betas=BETAS, state_bits=bits, master=True, capturable=capturable, seed=5)
+        n = 0
+        for s in scales:
+            for i, (p, g) in enumerate(zip(ps, gradients(n))):
+                p.grad = g.to(p.dtype) if not some or has(i, n) else None
+            opt.step(grad_scale=torch.tensor([s], device="cuda"))
+            n += bool(np.isfinite(s))
+        return ps, opt
+
+    inf, nan = float("inf"), float("nan")
+    ps, a = run([inf, 0.5, nan, -inf, 0.25, 1.0, inf, 2.0])
+    qs, b = run([0.5, 0.25, 1.0, 2.0])
+    assert a.state_dict()["steps"] == b.state_dict()["steps"] and int(a.t) == 4
+    for x, y in zip(ps + a.m + a.v + a.masters + (a.m_scale or []) + (a.v_scale or []),
+                    qs + b.m + b.v + b.masters + (b.m_scale or []) + (b.v_scale or [])):
+        assert torch.equal(x.detach().view(torch.uint8), y.detach().view(torch.uint8))
+
+
+def test_steps_with_and_without_a_scale():
+    """Counts go on through both; tolerances as above (the formulas at the counts)."""
+    ps, opt = make()
+    count = 0
+    for step, s in enumerate([None, None, float("inf"), 0.5, None, float("nan"), 2.0]):
+        before = [(f64(p), f64(m), f64(v)) for p, m, v in zip(ps, opt.m, opt.v)]
+        gs = gradients(step)
+        for p, g in zip(ps, gs):
+            p.grad = g
+        opt.step() if s is None else opt.step(grad_scale=torch.tensor([s], device="cuda"))
+        left_out = s is not None and not np.isfinite(s)
+        count += not left_out
+        assert opt.t == count and isinstance(opt.t, int)
+        for i, p in enumerate(ps):
+            w0, m0, v0 = before[i]
+            if left_out:
+                assert (f64(p) == w0).all()
+                continue
+            g = f64(gs[i]) * (1.0 if s is None else s)
+            w, m1, v1 = O.adamw(w0, g, m0, v0, count, LR, BETAS, 1e-8, WD)
+            room = abs(BETAS[0] * m0) + abs((1 - BETAS[0]) * g)
+            stepped = LR / (1 - BETAS[0] ** count) * room / (np.sqrt(v1 / (1 - BETAS[1] ** count)) + 1e-8)
+            assert (abs(f64(p) - w) <= H32 * (3 * abs(w) + 3 * abs(w0) + 28 * stepped)).all(), (step, i)
+    for bad in (torch.ones(2, device="cuda"), torch.ones(1)):
+        with pytest.raises(ValueError):
+            opt.step(grad_scale=bad)
+    with pytest.raises(TypeError):
+        opt.step(grad_scale=torch.ones(1, dtype=torch.float64, device="cuda"))
+    assert opt.t == count
+
+
+def test_captured_steps_left_out():
+    ps, a = make(capturable=True)
+    qs, b = make(capturable=True)
+    scale = torch.ones(1, device="cuda")
+    bufs = [torch.zeros(s, device="cuda") for s in SHAPES]
+    for p, q, g in zip(ps, qs, bufs):
+        p.grad = q.grad = g
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step(grad_scale=scale)
+    for step, s in enumerate([0.5, float("inf"), 1.0, float("nan"), 2.0, 0.25]):
+        for x, g in zip(bufs, gradients(step)):
+            x.copy_(g)
+        scale.fill_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        if np.isfinite(s):
+            b.step(grad_scale=scale)
+    assert a.state_dict()["steps"] == b.state_dict()["steps"] == [4] * 4
+    for x, y in zip(ps + a.m + a.v, qs + b.m + b.v):
+        assert torch.equal(x.detach(), y.detach())
