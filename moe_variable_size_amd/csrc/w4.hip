@@ -7,6 +7,8 @@
 //     sum (q - z) x = sum (16 + q) x - (16 + z) sum x,
 // with sum x from the matrix cores too (a product with ones; 16 of it is what the group's accumulator begins
 // with), and the scale applied to it in fp32.  So no weight is rounded, and products and sums are as exact as bf16's.
+// Where x is infinite, or so large that a sum with the 16s in it is, the difference is not the result: a sum that is not finite
+// is taken again, weight by weight (plain_sum).
 //
 // A 128-element block of a row is 64 bytes, 16 for each quarter q of a wave's lanes: word j holds elements 32 j + 8
 // q .. +7, what lane quarter q feeds into the block's j-th 16 x 16 x 32 product, so that a lane loads 16 bytes at a
@@ -76,6 +78,33 @@ MOE_DEV f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f
 template <bool ZEROS>
 MOE_DEV bf16x8 sum_factor() {  // 1, or -24
   return all_of(ZEROS ? 0x3F803F80u : 0xC1C0C1C0u);
+}
+
+// byte, in its row, of the word with the codes of element k and the seven behind it (k a multiple of 8)
+MOE_DEV uint32_t word_at(int k) { return (uint32_t)(k / BLK) * 64 + (k % 32 / 8) * 16 + (k % BLK / 32) * 4; }
+MOE_DEV bool is_finite(float s) { return fabsf(s) < INFINITY; }
+
+// x . W[n] of expert e by the formula itself, (q - z) s x, in fp32 (until it is NaN, which it stays).  For results that are not
+// finite alone: one thread each, 0.2 us for a word (16 x 8192 x 8192 with an infinity in one row: 211 us, without 16).
+template <int GP, bool ZEROS>
+MOE_DEV float plain_sum(const Weight &p, int64_t e, int n, const bf16_t *x) {
+  const uint8_t *codes = p.codes + e * p.per_codes + (int64_t)n * p.blocks * 64;
+  const int64_t first = e * p.per_scales + n;
+  float sum = 0.f;
+  for (int k0 = 0; k0 < p.K && sum == sum; k0 += BLK) {
+#pragma unroll 2
+    for (int k = k0; k < min(k0 + BLK, p.K); k += 8) {
+      const int64_t g = first + (int64_t)(k / (BLK / GP)) * p.cols;
+      const uint32_t word = *(const uint32_t *)(codes + word_at(k));
+      const u32x4 v = *(const u32x4 *)(x + k);
+      const float s = bf16_to_f32(p.scales[g]), z = ZEROS ? (float)p.zeros[g] : 8.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sum = fmaf(((float)(word >> (4 * ((i & 1) * 4 + i / 2)) & 15u) - z) * s,
+                   __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16), sum);
+    }
+  }
+  return sum;
 }
 
 // ---- some rows: 5 and more -------------------------------------------------------------
@@ -270,7 +299,10 @@ __global__ __launch_bounds__(WAVES * 64) void dense_kernel(DenseArgs a, int act)
     const int rows = a.M - m0 - i * 16;
     if (rows <= 0) break;
     join_waves<TJ>(red, v.acc[i], rows, [&](int r, int c, float s) {
-      if (n0 + c < p.N) finish<To>(a, act, m0 + i * 16 + r, n0 + c, s);
+      if (n0 + c >= p.N) return;
+      const int m = m0 + i * 16 + r;
+      if (!is_finite(s)) s = plain_sum<GP, ZEROS>(p, 0, n0 + c, a.x + (int64_t)m * p.K);
+      finish<To>(a, act, m, n0 + c, s);
     });
   }
 }
@@ -303,7 +335,9 @@ MOE_DEV void expert_rows(const ExpertArgs &a, float *red, int e, int n0, int row
       r += i * 16;
       if (n0 + c >= p.N) return;
       const int t = a.row_to_token[row0 + r];
-      if (t >= 0) unsafeAtomicAdd(a.y + (int64_t)t * p.N + n0 + c, s * a.row_weight[row0 + r]);
+      if (t < 0) return;
+      if (!is_finite(s)) s = plain_sum<GP, ZEROS>(p, e, n0 + c, a.x + (int64_t)t * p.K);
+      unsafeAtomicAdd(a.y + (int64_t)t * p.N + n0 + c, s * a.row_weight[row0 + r]);
     });
   }
 }
@@ -470,7 +504,10 @@ MOE_DEV void stream_rows(const ExpertArgs &a, char *lds, int e, int n0, int row0
       const int t = a.row_to_token[row0 + m];
       if (t < 0) continue;
       const float weight = a.row_weight[row0 + m];
-      if (n0 + r < p.N) unsafeAtomicAdd(a.y + (int64_t)t * p.N + n0 + r, acc[i][e2] * weight);
+      if (n0 + r >= p.N) continue;
+      float s = acc[i][e2];
+      if (!is_finite(s)) s = plain_sum<GP, ZEROS>(p, e, n0 + r, a.x + (int64_t)t * p.K);
+      unsafeAtomicAdd(a.y + (int64_t)t * p.N + n0 + r, s * weight);
     }
 }
 
@@ -617,7 +654,9 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(DenseArgs a, int act) {
     v.multiply(0, lds, pairs, 1.f);
   }
   join_few<TJ, WAVES>((float *)lds, v.acc, a.M, [&](int r, int c, float s) {
-    if (n0 + c < p.N) finish<To>(a, act, r, n0 + c, s);
+    if (n0 + c >= p.N) return;
+    if (!is_finite(s)) s = plain_sum<GP, ZEROS>(p, 0, n0 + c, a.x + (int64_t)r * p.K);
+    finish<To>(a, act, r, n0 + c, s);
   });
 }
 
@@ -700,14 +739,21 @@ __global__ __launch_bounds__(TOKEN_W * 64) void token_kernel(TokenArgs a) {
     }
   }
   join_few<1, TOKEN_W>((float *)lds, v.acc, 1, [&](int, int c, float s) {
-    if (n0 + c < p.N) a.y[t * p.N + n0 + c] = s;
+    if (n0 + c >= p.N) return;
+    if (!is_finite(s)) {
+      s = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int e = a.ids[t * a.k + j];
+        if (e >= 0 && e < a.E)
+          s = fmaf(a.weights ? a.weights[t * a.k + j] : 1.f, plain_sum<GP, ZEROS>(p, e, n0 + c, a.x + t * p.K), s);
+      }
+    }
+    a.y[t * p.N + n0 + c] = s;
   });
 }
 
 // ---- codes from weights and back -------------------------------------------------------
 // 8 elements per lane, G / 8 lanes per group; a wave takes 512 elements of a row.
-MOE_DEV uint32_t word_at(int k) { return (uint32_t)(k / BLK) * 64 + (k % 32 / 8) * 16 + (k % BLK / 32) * 4; }
-
 template <typename T, int G>
 __global__ __launch_bounds__(256) void quantize_kernel(const T *__restrict__ W, Weight p, int64_t rows, uint8_t *codes, bf16_t *scales,
                                                        uint8_t *zeros) {
