@@ -774,7 +774,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T *__restrict__ W, 
       lo = fminf(lo, __shfl_xor(lo, d, 64));
       hi = fmaxf(hi, __shfl_xor(hi, d, 64));
     }
-    const float wide = zeros ? (hi - lo) / 15.f : fmaxf(-lo, hi) / 7.f;
+    // (hi - lo may be past the largest number, a fifteenth of it is not)
+    const float range = is_finite(hi - lo) ? (hi - lo) / 15.f : (hi * 0.0625f - lo * 0.0625f) / 15.f * 16.f;
+    const float wide = zeros ? range : fmaxf(-lo, hi) / 7.f;
     const __bf16 s16 = (__bf16)wide;
     const float s = (float)s16, inv = s >= 0x1p-126f ? 1.f / s : 0.f;  // (no scale: every code the zero point)
     const float z = zeros ? fminf(fmaxf(rintf(-lo * inv), 0.f), 15.f) : 8.f;
