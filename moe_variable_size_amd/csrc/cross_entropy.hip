@@ -18,7 +18,7 @@
 // 0.0020.  bf16 rows off 16-byte lines do the same in the staged tiles, fp32 in tiles that multiply three parts of bf16.  Few rows, and products so small that their reduction
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
-// bf16, 8192 x 4096 x 65536: 12.7 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.39 PFLOP/s and 68 us
+// bf16, 8192 x 4096 x 65536: 12.7 to 13.1 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.34 to 1.39 PFLOP/s and 68 us
 // besides (20 of them x by the rows' weights, not for a mean or a sum); the loss of 2048 x 4096 x 50257 646 us.  fp32, 1074 x 600 x
 // 47121, loss and gradients: 1.60 ms (2.36 by fp32 instructions; 1.99 for logits kept and three such products).  One row x 4096 x 32000: 51 us, 38 of them the streamed product (7.0 TB/s),
 // the others two launches.
