@@ -667,7 +667,8 @@ typedef struct moe_adamw_tensor {
  *   that are replayed; step is then not looked at.
  *   grad_scale [1] (device, NULL for 1): s; where it is not finite, nothing is
  *   changed (t is the caller's: whether such a step counts).
- *   0 <= beta < 1, 0 <= eps, lr and weight_decay finite (MOE_ERR_OPTION).
+ *   0 <= beta < 1, 0 <= eps, lr and weight_decay finite (MOE_ERR_OPTION).  An eps
+ *   between 0 and 2^-126 is taken as 2^-126.
  *   param_dtype and grad_dtype MOE_F32 or MOE_BF16 each; a master copy needs
  *   MOE_BF16 parameters (MOE_ERR_DTYPE).
  */

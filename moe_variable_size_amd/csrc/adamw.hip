@@ -331,7 +331,8 @@ hipError_t launch_adamw(const moe_adamw_tensor *tensors, int count, const AdamwO
   a.a1 = (float)(1.0 - o.beta1);
   a.b2 = (float)o.beta2;
   a.a2 = (float)(1.0 - o.beta2);
-  a.eps = (float)o.eps;
+  // (the reciprocal of a number below the normal ones is infinite; v = 0 has then to give m / eps, mostly 0)
+  a.eps = o.eps > 0 ? fmaxf((float)o.eps, 0x1p-126f) : 0.f;
   a.wd = (float)o.weight_decay;
   a.ln1 = (float)log(o.beta1);
   a.ln2 = (float)log(o.beta2);
