@@ -19,7 +19,7 @@
 // is better split, write a piece's logits in fp32 to the workspace and read them back.
 //
 // bf16, 8192 x 4096 x 65536: 12.7 to 13.1 ms for the loss and both gradients, four products (17.6 TFLOP) at 1.34 to 1.39 PFLOP/s and 68 us
-// besides (20 of them x by the rows' weights, not for a mean or a sum); the loss of 2048 x 4096 x 50257 646 us.  fp32, 1074 x 600 x
+// besides (20 of them x by the rows' weights, not for a mean or a sum); the loss of 2048 x 4096 x 50257 646 to 676 us.  fp32, 1074 x 600 x
 // 47121, loss and gradients: 1.60 ms (2.36 by fp32 instructions; 1.99 for logits kept and three such products).  One row x 4096 x 32000: 51 us, 38 of them the streamed product (7.0 TB/s),
 // the others two launches.
 #include "cross_entropy.hpp"
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(256) void largest_kernel(float *factor, int64_t M) 
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
   if ((threadIdx.x & 63) == 0) atomicMax((uint32_t *)factor + M, __float_as_uint(top));
 }
-// y = x with its rows times their part of factor[M], 8 W elements of a row per thread (W: on 16-byte lines) or one
+// y = x with its rows times their part of factor[M], 8 elements of a row at a time (W: rows on 16-byte lines) or one
 template <bool W>
 __global__ __launch_bounds__(256) void weigh_kernel(const bf16_t *__restrict__ x, bf16_t *__restrict__ y, const float *factor, int64_t M,
                                                     int64_t K) {
